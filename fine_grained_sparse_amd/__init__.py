@@ -22,7 +22,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP4_E2M1 = 0, 1, 2, 3
 MOE_LAYOUT_ROWS, MOE_LAYOUT_FRAG16 = 0, 1
 _STATUS = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_ALIGN",
            4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_UNSUPPORTED", 6: "MOE_ERR_HIP", 7: "MOE_ERR_SCRATCH"}
@@ -33,7 +33,7 @@ EXPORTS = ("moe_workspace_size", "moe_router", "moe_forward", "moe_forward_noall
            "moe_bias_update", "moe_bias_quantile", "moe_status_str", "moe_slice_workspace_size",
            "moe_forward_slice")
 WEIGHT_NAMES = ("W_gate", "W_up", "W_down", "Ws_gate", "Ws_up", "Ws_down", "W_lat_down", "W_lat_up")
-SCALE_NAMES = ("W_gate_scale", "W_up_scale", "W_down_scale")  # FP8 routed experts only
+SCALE_NAMES = ("W_gate_scale", "W_up_scale", "W_down_scale")  # FP8 and FP4 routed experts only
 STAGES = ("start", "router", "dispatch", "latent", "up", "down", "end")
 NUM_STAGE_EVENTS = len(STAGES)
 
@@ -209,17 +209,28 @@ def _weights_desc(weights, T, d, E, K, scale, dt, dev, n_shared, n_group=1, topk
     """Validate the weight tensors; return (LayerDesc, ExpertWeights).
     Routed experts are of dtype dt, or float8_e4m3fn codes with uint8 E8M0
     block scales (W_gate_scale, W_up_scale [E, F/128, d_in/128];
-    W_down_scale [E, d_in/128, F/128]) when dt is bf16."""
+    W_down_scale [E, d_in/128, F/128]) when dt is bf16, or uint8 pairs of
+    E2M1 codes (W_gate, W_up [E, F, d_in/2]; W_down [E, d_in, F/2]) with
+    uint8 E8M0 scales per 32 columns (W_gate_scale, W_up_scale
+    [E, F, d_in/32]; W_down_scale [E, d_in, F/32])."""
     Wg, Wu, Wd = weights["W_gate"], weights["W_up"], weights["W_down"]
     f8 = isinstance(Wg, torch.Tensor) and Wg.dtype == torch.float8_e4m3fn and dt == torch.bfloat16
-    rdt = torch.float8_e4m3fn if f8 else dt
+    f4 = isinstance(Wg, torch.Tensor) and Wg.dtype == torch.uint8 and dt == torch.bfloat16
+    rdt = torch.float8_e4m3fn if f8 else torch.uint8 if f4 else dt
+    per = 2 if f4 else 1  # elements of a stored value
     _need(Wg, "W_gate", rdt, device=dev)
     if Wg.dim() != 3 or Wg.shape[0] != E:
         raise ValueError("W_gate must be [E, F, d_in]")
-    F, din = Wg.shape[1], Wg.shape[2]
-    _need(Wu, "W_up", rdt, (E, F, din), dev)
-    _need(Wd, "W_down", rdt, (E, din, F), dev)
+    F, din = Wg.shape[1], Wg.shape[2] * per
+    _need(Wu, "W_up", rdt, (E, F, din // per), dev)
+    _need(Wd, "W_down", rdt, (E, din, F // per), dev)
     scales = [None] * 3
+    if f4:
+        if F % 128 or din % 128:
+            raise ValueError("FP4 routed experts need F and d_in in whole 128-column blocks")
+        for i, (n, shp) in enumerate(zip(SCALE_NAMES, ((E, F, din // 32), (E, F, din // 32), (E, din, F // 32)))):
+            _need(weights.get(n), n, torch.uint8, shp, dev)
+            scales[i] = weights[n]
     if f8:
         if F % 128 or din % 128:
             raise ValueError("FP8 routed experts need F and d_in in whole 128-blocks")
@@ -247,7 +258,7 @@ def _weights_desc(weights, T, d, E, K, scale, dt, dev, n_shared, n_group=1, topk
         _need(Wsd, "Ws_down", dt, (d, ns * Fs), dev)
     layout = int(weights.get("layout", MOE_LAYOUT_ROWS))
     D = desc(T=T, d=d, E=E, K=K, F=F, n_shared=ns, F_shared=Fs, d_latent=d_lat,
-             scale=scale, act_dtype=_DT[dt], w_dtype=MOE_FP8_E4M3 if f8 else None,
+             scale=scale, act_dtype=_DT[dt], w_dtype=MOE_FP8_E4M3 if f8 else MOE_FP4_E2M1 if f4 else None,
              w_layout=layout, n_group=n_group, topk_group=topk_group)
     W = ExpertWeights(*[None if t is None else t.data_ptr() for t in
                         (Wg, Wu, Wd, Wsg, Wsu, Wsd, Wl_d, Wl_u, *scales)])
@@ -296,26 +307,27 @@ def bias_quantile(x, W_r, K, *, out=None, workspace=None, stream=None):
 
 
 def pack_weights(weights, *, n_shared=None, stream=None):
-    """moe_pack_weights: row-major weights (bf16, or FP8 routed experts with
-    bf16 shared / latent maps) -> a new dict of tensors of the same shapes
-    in MOE_LAYOUT_FRAG16, with "layout" set (FP8 block scales are carried
-    over as they are).  Run once, e.g. at model load; the packed tensors are
+    """moe_pack_weights: row-major weights (bf16, or FP8 or FP4 routed experts
+    with bf16 shared / latent maps) -> a new dict of tensors of the same
+    shapes in MOE_LAYOUT_FRAG16, with "layout" set (FP8 block scales are
+    carried over as they are, FP4 scales are repacked).  Run once, e.g. at model load; the packed tensors are
     what forward() then reads."""
     if int(weights.get("layout", MOE_LAYOUT_ROWS)) != MOE_LAYOUT_ROWS:
         raise ValueError("weights are already packed")
     Wg = weights["W_gate"]
-    if Wg.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise TypeError("only bf16 and FP8 weights have a packed layout")
-    E, F, din = Wg.shape
+    if Wg.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("only bf16, FP8 and FP4 weights have a packed layout")
+    f4 = Wg.dtype == torch.uint8
+    E, F, din = Wg.shape[0], Wg.shape[1], Wg.shape[2] * (2 if f4 else 1)
     d = weights["W_lat_down"].shape[1] if weights.get("W_lat_down") is not None else din
     D, src = _weights_desc(weights, 1, d, E, 1, 1.0, torch.bfloat16, Wg.device, n_shared)
     with _on(stream):
         out = {k: (torch.empty_like(weights[k]) if weights.get(k) is not None else None)
                for k in WEIGHT_NAMES}
-    dst = ExpertWeights(*[None if out[k] is None else out[k].data_ptr() for k in WEIGHT_NAMES])
-    for k in SCALE_NAMES:
-        if weights.get(k) is not None:
-            out[k] = weights[k]
+        for k in SCALE_NAMES:
+            if weights.get(k) is not None:
+                out[k] = torch.empty_like(weights[k]) if f4 else weights[k]
+    dst = ExpertWeights(*[None if out.get(k) is None else out[k].data_ptr() for k in WEIGHT_NAMES + SCALE_NAMES])
     rc = lib().moe_pack_weights(ctypes.byref(D), ctypes.byref(src), ctypes.byref(dst), _stream(stream))
     if rc:
         raise MoeError("moe_pack_weights", rc)
@@ -364,7 +376,8 @@ def forward(x, W_r, b, weights, K, scale=2.827, *, n_shared=None, out=None,
     [d_latent, d], W_lat_up [d, d_latent], plus "layout" (MOE_LAYOUT_ROWS
     when absent; pack_weights returns MOE_LAYOUT_FRAG16 weights).  With bf16
     x the routed experts may be float8_e4m3fn codes (packed) with uint8 E8M0
-    block scales W_gate_scale, W_up_scale, W_down_scale.  Returns
+    block scales W_gate_scale, W_up_scale, W_down_scale, or uint8 pairs of
+    E2M1 codes (packed) with uint8 E8M0 scales per 32 columns.  Returns
     out [T, d], or (out, routing dict) with return_routing=True.
     `stage_events` (optional) is a sequence of NUM_STAGE_EVENTS
     already-created torch.cuda.Event objects recorded at the stage
@@ -454,5 +467,5 @@ def forward_noalloc(x, W_r, b, weights, K, scale=2.827, *, n_shared=None, out=No
 
 
 __all__ = ["router", "forward", "forward_noalloc", "pack_weights", "bias_update", "bias_quantile", "workspace_size", "desc", "lib", "MoeError",
-           "LayerDesc", "ExpertWeights", "Workspace", "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3",
+           "LayerDesc", "ExpertWeights", "Workspace", "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP4_E2M1",
            "MOE_LAYOUT_ROWS", "MOE_LAYOUT_FRAG16", "EXPORTS", "WEIGHT_NAMES", "SCALE_NAMES"]

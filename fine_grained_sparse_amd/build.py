@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "moe")
 LIB = os.path.join(HERE, "libmoe.so")
-SOURCES = ["api.cpp", "gemm.hip", "router.hip", "dispatch.hip", "pack.hip", "noalloc.hip"]
+SOURCES = ["api.cpp", "gemm.hip", "fp4.hip", "router.hip", "dispatch.hip", "pack.hip", "noalloc.hip"]
 # measurement aid of bench.py (HBM streaming read, bf16 MFMA loop), a library
 # of its own so that libmoe.so exports only the layer's C ABI
 YARDSTICK_SOURCES = ["yardstick.hip"]

@@ -16,7 +16,9 @@
 // weights are packed (MOE_LAYOUT_FRAG16), the LDS tile otherwise.
 // FP8 routed experts (w_dtype MOE_FP8_E4M3): the up and down projections
 // run the FP8 form of the WIDE tile (WIDE16 at decode sizes), whose shared
-// (bf16) tiles take the bf16 path inside the same launch.
+// (bf16) tiles take the bf16 path inside the same launch.  FP4 routed experts
+// (MOE_FP4_E2M1) have projections of their own (fp4.hip) in the same places,
+// and keep the experts' outputs Y in fp32.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -43,6 +45,8 @@ struct Plan {
     DType dt;
     bool packed;                              // weights in MOE_LAYOUT_FRAG16
     bool f8;                                  // routed experts in block-scaled FP8
+    bool f4;                                  // routed experts in group-scaled FP4
+    int64_t ys;                               // element size of the experts' outputs Y
     int64_t es;                               // element size
     // router
     bool gemv;                                // logits by k_router_gemv (a few tokens)
@@ -63,7 +67,7 @@ moe_status check_desc(const moe_layer_desc* D, bool forward) {
     if (!D) return MOE_ERR_NULL;
     if (D->act_dtype != MOE_F32 && D->act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
     if (forward) {
-        if (D->w_dtype == MOE_FP8_E4M3) {  // bf16 activations, packed weights
+        if (D->w_dtype == MOE_FP8_E4M3 || D->w_dtype == MOE_FP4_E2M1) {  // bf16 activations, packed weights
             if (D->act_dtype != MOE_BF16 || D->w_layout != MOE_LAYOUT_FRAG16) return MOE_ERR_UNSUPPORTED;
         } else {
             if (D->w_dtype != D->act_dtype) return MOE_ERR_UNSUPPORTED;
@@ -89,6 +93,9 @@ moe_status check_desc(const moe_layer_desc* D, bool forward) {
         if (D->w_dtype == MOE_FP8_E4M3) {  // whole 128 x 128 scale blocks; K <= 8192 per GEMM
             const int64_t din = D->d_latent ? D->d_latent : D->d;
             if (din % 128 || D->F % 128 || din > 8192 || D->F > 8192) return MOE_ERR_SHAPE;
+        }
+        if (D->w_dtype == MOE_FP4_E2M1) {  // whole 16 x 128 blocks
+            if ((D->d_latent ? D->d_latent : D->d) % 128 || D->F % 128) return MOE_ERR_SHAPE;
         }
     }
     return MOE_OK;
@@ -148,6 +155,8 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
     // 8.28 vs 3.37 at 43; K3 shapes 10.7 vs 10.6 at 9.1, 22.1 vs 10.5 at 37.
     p.packed = forward && D->w_layout == MOE_LAYOUT_FRAG16;
     p.f8 = forward && D->w_dtype == MOE_FP8_E4M3;
+    p.f4 = forward && D->w_dtype == MOE_FP4_E2M1;
+    p.ys = p.f4 ? 4 : p.es;
     const TileCfg big = p.packed ? TILE_WIDE : TILE_LARGE;
     const int64_t arows = slice ? cdiv(p.A * p.E, E_total) : p.A;  // expected routed rows
     p.ecfg = (arows >= 10ll * p.E && p.dt == DT_BF16) ? big : (p.f8 ? TILE_WIDE16 : TILE_SMALL);
@@ -159,7 +168,7 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
         const int64_t nt = std::max<int64_t>(cdiv(std::max(p.F, p.Fsh), 256), cdiv(p.din, 512));
         if (mt * nt < 128) p.ecfg = TILE_NARROW;
     }
-    p.bm = tile_bm(p.ecfg);
+    p.bm = p.f4 ? fp4_bm() : tile_bm(p.ecfg);
     // dense maps of the latent form: 128-row tiles from 512 tokens (K3
     // shapes: 12.5 -> 10.3 ms at 768 tokens with the expert switch above;
     // below 512 the two measured the same within run-to-run noise)
@@ -197,7 +206,7 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
         p.o_H = take(p.A * p.F * p.es);
         if (p.ns) p.o_Hs = take(T * p.Fsh * p.es);
         const int64_t yrows = p.A + ((p.ns && !p.dl) ? T : 0);
-        p.o_Y = take(yrows * p.din * p.es);
+        p.o_Y = take(yrows * p.din * p.ys);
         if (p.dl) p.o_R = take(T * p.dl * p.es);
     }
     p.total = off;
@@ -273,6 +282,16 @@ hipError_t launch_f8(const Plan& p, GemmArgs g, const uint8_t* bs, const uint8_t
     return launch_gemm_f8(g, epi, p.ecfg, p.max_tiles, max_n, s);
 }
 
+// The same with FP4 weights.
+hipError_t launch_f4(const Plan& p, GemmArgs g, const uint8_t* bs, const uint8_t* bsu, Epi epi, int max_n,
+                     hipStream_t s) {
+    g.g[0].bs = bs;
+    g.g[0].bsu = bsu;
+    g.g[0].b_estride = static_cast<int64_t>(g.g[0].N) * g.g[0].seg[0].K / 2;
+    g.g[0].s_estride = static_cast<int64_t>(g.g[0].N) * g.g[0].seg[0].K / 32;
+    return launch_gemm_fp4(g, epi, p.max_tiles, max_n, s);
+}
+
 hipError_t record(void* const* ev, int i, hipStream_t s) {
     if (!ev || !ev[i]) return hipSuccess;
     return hipEventRecord(static_cast<hipEvent_t>(ev[i]), s);
@@ -335,7 +354,9 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         S1.ldc = p.Fsh;
         g.tiles = tiles;
         g.ntiles = ntiles;
-        if (p.f8)
+        if (p.f4)
+            MOE_HIP(launch_f4(p, g, W->W_gate_scale, W->W_up_scale, EPI_SWIGLU, std::max(p.F, p.Fsh), s));
+        else if (p.f8)
             MOE_HIP(launch_f8(p, g, W->W_gate_scale, W->W_up_scale, EPI_SWIGLU, std::max(p.F, p.Fsh), s));
         else
             MOE_HIP(launch_gemm(g, p.dt, false, EPI_SWIGLU, p.ecfg, p.max_tiles, std::max(p.F, p.Fsh), p.packed, s));
@@ -356,7 +377,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
             S1.seg[0] = GemmSeg{Hs, W->Ws_down, nullptr, p.Fsh, p.Fsh, p.Fsh, 0};
             S1.nseg = 1;
             S1.N = p.d;
-            S1.C = Y + p.A * p.d * p.es;
+            S1.C = Y + p.A * p.d * p.ys;
             S1.ldc = p.d;
         } else {
             S1.N = 0;  // shared tiles (latent form) do nothing here
@@ -364,20 +385,22 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         }
         g.tiles = tiles;
         g.ntiles = ntiles;
-        if (p.f8)
+        if (p.f4)
+            MOE_HIP(launch_f4(p, g, W->W_down_scale, nullptr, EPI_STORE, p.din, s));
+        else if (p.f8)
             MOE_HIP(launch_f8(p, g, W->W_down_scale, nullptr, EPI_STORE, p.din, s));
         else
             MOE_HIP(launch_gemm(g, p.dt, false, EPI_STORE, p.ecfg, p.max_tiles, p.din, p.packed, s));
     }
     MOE_HIP(record(ev, MOE_EV_DOWN, s));
     if (!latent) {
-        const void* ysh = p.ns ? static_cast<const void*>(Y + p.A * p.d * p.es) : nullptr;
-        MOE_HIP(launch_combine(p.dt, Y, p.d, ysh, pos, w, p.T, p.K, p.d, out, p.d, s));
+        const void* ysh = p.ns ? static_cast<const void*>(Y + p.A * p.d * p.ys) : nullptr;
+        MOE_HIP(launch_combine(p.dt, p.f4, Y, p.d, ysh, pos, w, p.T, p.K, p.d, out, p.d, s));
         MOE_HIP(record(ev, MOE_EV_END, s));
         return MOE_OK;
     }
     // latent form: R = sum_k w Y[pos];  out = Hs Ws_down^T + R W_lat_up^T
-    MOE_HIP(launch_combine(p.dt, Y, p.dl, nullptr, pos, w, p.T, p.K, p.dl, R, p.dl, s));
+    MOE_HIP(launch_combine(p.dt, p.f4, Y, p.dl, nullptr, pos, w, p.T, p.K, p.dl, R, p.dl, s));
     GemmArgs g = gemm_args();
     GemmGroup& G = g.g[0];
     int ns = 0;
@@ -421,7 +444,8 @@ moe_status check_slice(const moe_layer_desc* desc, int e0, int E_total) {
 // The weight pointers every forward needs, with their alignment.
 moe_status check_weights(const moe_layer_desc* desc, const moe_expert_weights* W) {
     if (!W->W_gate || !W->W_up || !W->W_down) return MOE_ERR_NULL;
-    if (desc->w_dtype == MOE_FP8_E4M3 && (!W->W_gate_scale || !W->W_up_scale || !W->W_down_scale))
+    if ((desc->w_dtype == MOE_FP8_E4M3 || desc->w_dtype == MOE_FP4_E2M1) &&
+        (!W->W_gate_scale || !W->W_up_scale || !W->W_down_scale))
         return MOE_ERR_NULL;
     if (desc->n_shared > 0 && (!W->Ws_gate || !W->Ws_up || !W->Ws_down)) return MOE_ERR_NULL;
     if (desc->d_latent > 0 && (!W->W_lat_down || !W->W_lat_up)) return MOE_ERR_NULL;
@@ -431,6 +455,9 @@ moe_status check_weights(const moe_layer_desc* desc, const moe_expert_weights* W
     if (desc->n_shared > 0 && (!aligned16(W->Ws_gate) || !aligned16(W->Ws_up) || !aligned16(W->Ws_down)))
         return MOE_ERR_ALIGN;
     if (desc->d_latent > 0 && (!aligned16(W->W_lat_down) || !aligned16(W->W_lat_up))) return MOE_ERR_ALIGN;
+    if (desc->w_dtype == MOE_FP4_E2M1 &&
+        (!aligned16(W->W_gate_scale) || !aligned16(W->W_up_scale) || !aligned16(W->W_down_scale)))
+        return MOE_ERR_ALIGN;
     return MOE_OK;
 }
 
@@ -571,45 +598,65 @@ moe_status moe_pack_weights(const moe_layer_desc* desc, const moe_expert_weights
                             const moe_expert_weights* dst, void* stream) {
     if (!desc || !src || !dst) return MOE_ERR_NULL;
     moe_layer_desc D = *desc;
-    if (D.w_dtype != MOE_BF16 && D.w_dtype != MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+    if (D.w_dtype != MOE_BF16 && D.w_dtype != MOE_FP8_E4M3 && D.w_dtype != MOE_FP4_E2M1) return MOE_ERR_UNSUPPORTED;
     // shapes as for the forward over the packed result (src is row-major)
     D.w_layout = MOE_LAYOUT_FRAG16;
     const moe_status st = check_desc(&D, true);
     if (st != MOE_OK) return st;
     const int din = D.d_latent ? D.d_latent : D.d, Fsh = D.n_shared * D.F_shared;
-    const bool f8 = D.w_dtype == MOE_FP8_E4M3;  // routed matrices: one byte per element
+    // routed matrices: one byte per FP8 element; two FP4 elements per byte,
+    // whose scales (one byte per 32 elements) move with them
+    const bool f8 = D.w_dtype == MOE_FP8_E4M3, f4 = D.w_dtype == MOE_FP4_E2M1;
+    enum Form { BF16, FP8, FP4 };
+    const Form routed = f4 ? FP4 : f8 ? FP8 : BF16;
     struct Mat {
         const void* s;
         const void* d;
         int64_t count;
         int rows, cols;
-        bool f8;
+        Form form;
+        const uint8_t* ss;
+        const uint8_t* sd;
     };
     const Mat mats[] = {
-        {src->W_gate, dst->W_gate, D.E, D.F, din, f8},     {src->W_up, dst->W_up, D.E, D.F, din, f8},
-        {src->W_down, dst->W_down, D.E, din, D.F, f8},     {src->Ws_gate, dst->Ws_gate, 1, Fsh, D.d, false},
-        {src->Ws_up, dst->Ws_up, 1, Fsh, D.d, false},      {src->Ws_down, dst->Ws_down, 1, D.d, Fsh, false},
-        {src->W_lat_down, dst->W_lat_down, 1, D.d_latent, D.d, false},
-        {src->W_lat_up, dst->W_lat_up, 1, D.d, D.d_latent, false},
+        {src->W_gate, dst->W_gate, D.E, D.F, din, routed, src->W_gate_scale, dst->W_gate_scale},
+        {src->W_up, dst->W_up, D.E, D.F, din, routed, src->W_up_scale, dst->W_up_scale},
+        {src->W_down, dst->W_down, D.E, din, D.F, routed, src->W_down_scale, dst->W_down_scale},
+        {src->Ws_gate, dst->Ws_gate, 1, Fsh, D.d, BF16, nullptr, nullptr},
+        {src->Ws_up, dst->Ws_up, 1, Fsh, D.d, BF16, nullptr, nullptr},
+        {src->Ws_down, dst->Ws_down, 1, D.d, Fsh, BF16, nullptr, nullptr},
+        {src->W_lat_down, dst->W_lat_down, 1, D.d_latent, D.d, BF16, nullptr, nullptr},
+        {src->W_lat_up, dst->W_lat_up, 1, D.d, D.d_latent, BF16, nullptr, nullptr},
+    };
+    auto overlap = [](const void* p, const void* q, uintptr_t bytes) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+        return a < b + bytes && b < a + bytes;
     };
     for (const Mat& m : mats) {  // validate everything before enqueueing
         if (!m.s) continue;
         if (!m.d) return MOE_ERR_NULL;
         if (!aligned16(m.s) || !aligned16(m.d)) return MOE_ERR_ALIGN;
         if (m.rows <= 0 || m.cols <= 0) return MOE_ERR_SHAPE;
-        const uintptr_t bytes = static_cast<uintptr_t>(m.count) * m.rows * m.cols * (m.f8 ? 1 : 2);
-        const uintptr_t a = reinterpret_cast<uintptr_t>(m.s), b = reinterpret_cast<uintptr_t>(m.d);
-        if (a < b + bytes && b < a + bytes) return MOE_ERR_SHAPE;  // overlapping buffers
+        const uintptr_t n = static_cast<uintptr_t>(m.count) * m.rows * m.cols;
+        if (overlap(m.s, m.d, m.form == BF16 ? 2 * n : m.form == FP8 ? n : n / 2)) return MOE_ERR_SHAPE;
+        if (m.form == FP4) {
+            if (!m.ss || !m.sd) return MOE_ERR_NULL;
+            if (!aligned16(m.ss) || !aligned16(m.sd)) return MOE_ERR_ALIGN;
+            if (overlap(m.ss, m.sd, n / 32)) return MOE_ERR_SHAPE;
+        }
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     for (const Mat& m : mats) {
         if (!m.s) continue;
-        if (m.f8)
-            MOE_HIP(launch_pack_frag16_fp8(static_cast<const uint8_t*>(m.s), static_cast<uint8_t*>(const_cast<void*>(m.d)),
-                                           m.count, m.rows, m.cols, s));
+        uint8_t* d8 = static_cast<uint8_t*>(const_cast<void*>(m.d));
+        if (m.form == FP4)
+            MOE_HIP(launch_pack_fp4(static_cast<const uint8_t*>(m.s), m.ss, d8, const_cast<uint8_t*>(m.sd), m.count,
+                                    m.rows, m.cols, s));
+        else if (m.form == FP8)
+            MOE_HIP(launch_pack_frag16_fp8(static_cast<const uint8_t*>(m.s), d8, m.count, m.rows, m.cols, s));
         else
-            MOE_HIP(launch_pack_frag16(static_cast<const uint16_t*>(m.s), static_cast<uint16_t*>(const_cast<void*>(m.d)),
-                                       m.count, m.rows, m.cols, s));
+            MOE_HIP(launch_pack_frag16(static_cast<const uint16_t*>(m.s), reinterpret_cast<uint16_t*>(d8), m.count,
+                                       m.rows, m.cols, s));
     }
     return MOE_OK;
 }

@@ -187,8 +187,8 @@ __device__ __forceinline__ void unpack8_once(const bf16_t* p, float (&o)[8]) {
 }
 __device__ __forceinline__ void unpack8_once(const float* p, float (&o)[8]) { unpack8(p, o); }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_combine(const T* __restrict__ Y, int64_t ldy, const T* __restrict__ Ysh,
+template <typename TY, typename T>
+__global__ __launch_bounds__(256) void k_combine(const TY* __restrict__ Y, int64_t ldy, const TY* __restrict__ Ysh,
                                                  const int32_t* __restrict__ pos, const float* __restrict__ w, int K,
                                                  int N, T* __restrict__ out, int64_t ldo) {
     const int t = blockIdx.x;
@@ -242,14 +242,17 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int 
     return hipGetLastError();
 }
 
-hipError_t launch_combine(DType dt, const void* Y, int64_t ldy, const void* Yshared, const int32_t* pos, const float* w,
+hipError_t launch_combine(DType dt, bool y_f32, const void* Y, int64_t ldy, const void* Yshared, const int32_t* pos, const float* w,
                           int T, int K, int N, void* out, int64_t ldo, hipStream_t stream) {
     if (T <= 0) return hipSuccess;
     if (dt == DT_F32)
-        hipLaunchKernelGGL(k_combine<float>, dim3(T), dim3(256), 0, stream, static_cast<const float*>(Y), ldy,
+        hipLaunchKernelGGL((k_combine<float, float>), dim3(T), dim3(256), 0, stream, static_cast<const float*>(Y), ldy,
                            static_cast<const float*>(Yshared), pos, w, K, N, static_cast<float*>(out), ldo);
+    else if (y_f32)
+        hipLaunchKernelGGL((k_combine<float, bf16_t>), dim3(T), dim3(256), 0, stream, static_cast<const float*>(Y), ldy,
+                           static_cast<const float*>(Yshared), pos, w, K, N, static_cast<bf16_t*>(out), ldo);
     else
-        hipLaunchKernelGGL(k_combine<bf16_t>, dim3(T), dim3(256), 0, stream, static_cast<const bf16_t*>(Y), ldy,
+        hipLaunchKernelGGL((k_combine<bf16_t, bf16_t>), dim3(T), dim3(256), 0, stream, static_cast<const bf16_t*>(Y), ldy,
                            static_cast<const bf16_t*>(Yshared), pos, w, K, N, static_cast<bf16_t*>(out), ldo);
     return hipGetLastError();
 }

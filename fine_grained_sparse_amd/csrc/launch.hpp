@@ -126,6 +126,23 @@ hipError_t launch_gemm_f8(const GemmArgs& args, Epi epi, TileCfg cfg, int max_ti
 hipError_t launch_pack_frag16_fp8(const uint8_t* src, uint8_t* dst, int64_t count, int rows, int cols,
                                   hipStream_t stream);
 
+// The projections with 4-bit routed experts (fp4.hip): C = epi(A * B^T) over
+// a tile table of fp4_bm() rows per tile, bf16 A; C bf16 for the SwiGLU,
+// fp32 for the plain store.  Group 0: E2M1 codes (b_estride in bytes) with
+// E8M0 scales bs / bsu per 32 columns (s_estride in bytes), both in 16 x 128
+// blocks; group 1: packed bf16.  One K segment each.
+int fp4_bm();
+hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int max_tiles, int max_n, hipStream_t stream);
+// whether the grid of that launch stays within 31 bits
+bool fp4_grid_fits(int64_t max_tiles, int64_t max_n);
+
+// Row-major E2M1 codes [rows, cols / 2] and scales [rows, cols / 32] (count
+// matrices each, consecutive) -> 16 x 128 blocks: lane l of a block holds the
+// 16 bytes of columns 32 (l / 16) .. + 31 of row l % 16, its scale at byte
+// l of the block's 64.
+hipError_t launch_pack_fp4(const uint8_t* src, const uint8_t* ssrc, uint8_t* dst, uint8_t* sdst, int64_t count,
+                           int rows, int cols, hipStream_t stream);
+
 // Row-major [rows, cols] bf16 matrices (count of them, consecutive) -> the
 // fragment-block layout: block (rows/16) x (cols/32) of 1 KiB each.
 hipError_t launch_pack_frag16(const uint16_t* src, uint16_t* dst, int64_t count, int rows, int cols,
@@ -177,8 +194,8 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int 
                            hipStream_t stream);
 
 // out[t] = (Yshared ? Yshared[t] : 0) + sum_k w[t,k] * Y[pos[t,k]], over
-// the slots with pos >= 0
-hipError_t launch_combine(DType dt, const void* Y, int64_t ldy,
+// the slots with pos >= 0; y_f32: Y and Yshared in fp32 under a bf16 out
+hipError_t launch_combine(DType dt, bool y_f32, const void* Y, int64_t ldy,
                           const void* Yshared, const int32_t* pos,
                           const float* w, int T, int K, int N, void* out,
                           int64_t ldo, hipStream_t stream);

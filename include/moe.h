@@ -54,8 +54,11 @@ extern "C" {
 /* MOE_FP8_E4M3 is a weight dtype only: OCP FP8 E4M3FN codes (sign, 4
  * exponent bits with bias 7, 3 mantissa bits; 0x7F and 0xFF are NaN, no
  * infinities) with one E8M0 scale per 128 x 128 block (see
- * moe_expert_weights).                                                      */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+ * moe_expert_weights).  MOE_FP4_E2M1 likewise: OCP FP4 E2M1 codes (sign, 2
+ * exponent bits with bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; no infinities or NaN), two to a byte with the even column
+ * in the low four bits, with one E8M0 scale per 32 consecutive columns.    */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_FP4_E2M1 = 3 } moe_dtype;
 
 typedef enum {
     MOE_OK = 0,
@@ -85,10 +88,12 @@ typedef struct {
                        /* MOE_FP8_E4M3: routed experts in block-scaled FP8,   */
                        /* shared and latent weights bf16 (act_dtype bf16,     */
                        /* MOE_LAYOUT_FRAG16; d_in and F multiples of 128 and  */
-                       /* at most 8192)                                       */
-    int32_t w_layout;  /* moe_weight_layout of those weights (bf16 and FP8    */
-                       /* may be, and FP8 must be, MOE_LAYOUT_FRAG16; fp32    */
-                       /* must be MOE_LAYOUT_ROWS)                            */
+                       /* at most 8192), or MOE_FP4_E2M1: routed experts in   */
+                       /* group-scaled FP4, the rest as with FP8 (d_in and F  */
+                       /* multiples of 128)                                   */
+    int32_t w_layout;  /* moe_weight_layout of those weights (bf16 may be,    */
+                       /* FP8 and FP4 must be MOE_LAYOUT_FRAG16; fp32 must be */
+                       /* MOE_LAYOUT_ROWS)                                    */
     int32_t n_group;   /* group-limited choice: expert groups (0 or 1: none)  */
     int32_t topk_group;/* groups kept per token when n_group > 1              */
 } moe_layer_desc;
@@ -108,6 +113,14 @@ typedef struct {
  *     element (r, c) at byte (((c % 32) / 8) * 16 + r) * 16 + (c / 32) * 8
  *     + c % 8, so lane l's 16 bytes hold the codes of the two bf16 operands
  *     (columns 0-31 and 32-63) that lane feeds.
+ *   MOE_LAYOUT_FRAG16, FP4 matrices (the routed experts under
+ *     MOE_FP4_E2M1): (rows/16) x (cols/128) blocks of 16 rows x 128 columns,
+ *     block (i, j) at byte (i * (cols/128) + j) * 1024 of the codes and byte
+ *     (i * (cols/128) + j) * 64 of the scales; inside a block, the code of
+ *     element (r, c) is in byte ((c / 32) * 16 + r) * 16 + (c % 32) / 2 (even
+ *     c in the low four bits) and the scale of columns 32 g .. 32 g + 31 of
+ *     row r at byte 16 g + r, so lane l's 16 bytes of codes have one scale,
+ *     byte l.
  *   Stacked matrices (W_gate etc.) keep their per-expert stride rows * cols
  *   elements; the sizes of all buffers are those of the row-major layout.
  *   moe_pack_weights converts.                                              */
@@ -128,7 +141,14 @@ typedef enum { MOE_LAYOUT_ROWS = 0, MOE_LAYOUT_FRAG16 = 1 } moe_weight_layout;
  *   not repacked), so that element (r, c) of a matrix is
  *   code(r, c) * 2^(s[r/128][c/128] - 127).  The product is rounded to
  *   bf16 before the MFMA; it is exact (3 mantissa bits) while it lies in
- *   bf16's normal range.  s = 255 (NaN in E8M0) is not supported.           */
+ *   bf16's normal range.  s = 255 (NaN in E8M0) is not supported.
+ * Codes and scales of FP4 routed experts (w_dtype MOE_FP4_E2M1): row-major,
+ * W_gate, W_up [E, F, d_in/2] and W_down [E, d_in, F/2] bytes; W_gate_scale,
+ * W_up_scale [E, F, d_in/32] and W_down_scale [E, d_in, F/32], 16-byte
+ * aligned like the matrices and repacked with them, so that element (r, c)
+ * is code(r, c) * 2^(s[r][c/32] - 127), exact in bf16 in the same range and
+ * under the same limit.  The experts' outputs are then kept in fp32 until
+ * the combine (H and x_lat are rounded to bf16).                            */
 typedef struct {
     const void *W_gate, *W_up, *W_down;
     const void *Ws_gate, *Ws_up, *Ws_down;
@@ -292,7 +312,9 @@ moe_status moe_bias_quantile(const moe_layer_desc *desc, const void *x,
  * non-NULL, 16-byte aligned, of the same size and not overlap it.
  * Requires w_dtype MOE_BF16, or MOE_FP8_E4M3 (routed matrices as FP8 codes,
  * shared and latent ones bf16; the block scales are not touched and keep
- * their layout).  Shapes are checked as for moe_forward on the packed
+ * their layout), or MOE_FP4_E2M1 (likewise, but each routed matrix's scales
+ * are repacked with it: both scale members are then required and must not
+ * overlap).  Shapes are checked as for moe_forward on the packed
  * result.  Enqueued on `stream` like the other calls.                       */
 moe_status moe_pack_weights(const moe_layer_desc *desc,
                             const moe_expert_weights *src,
