@@ -469,3 +469,7 @@ def forward_noalloc(x, W_r, b, weights, K, scale=2.827, *, n_shared=None, out=No
 __all__ = ["router", "forward", "forward_noalloc", "pack_weights", "bias_update", "bias_quantile", "workspace_size", "desc", "lib", "MoeError",
            "LayerDesc", "ExpertWeights", "Workspace", "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP4_E2M1",
            "MOE_LAYOUT_ROWS", "MOE_LAYOUT_FRAG16", "EXPORTS", "WEIGHT_NAMES", "SCALE_NAMES"]
+
+from .train import balance_loss, gate_backward, router_backward, router_train  # noqa: E402  (needs the names above)
+
+__all__ += ["router_train", "balance_loss", "gate_backward", "router_backward"]

@@ -15,6 +15,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "moe")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cpp", "gemm.hip", "fp4.hip", "router.hip", "dispatch.hip", "pack.hip", "noalloc.hip"]
+# the router's training side (include/moe_train.h), which calls into libmoe.so
+TRAIN_SOURCES = ["train_api.cpp", "train.hip"]
+TRAIN_LIB = os.path.join(HERE, "libmoe_train.so")
 # measurement aid of bench.py (HBM streaming read, bf16 MFMA loop), a library
 # of its own so that libmoe.so exports only the layer's C ABI
 YARDSTICK_SOURCES = ["yardstick.hip"]
@@ -39,9 +42,11 @@ def _compile(src, verbose):
     return obj
 
 
-def _link(objs, lib, verbose):
+def _link(objs, lib, verbose, needs=()):
     tmp = lib + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp] + objs
+    if needs:  # libraries of this folder, found next to this one when it is loaded
+        cmd += ["-L" + HERE, "-Wl,-rpath,$ORIGIN"] + ["-l:" + os.path.basename(n) for n in needs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
@@ -50,10 +55,11 @@ def _link(objs, lib, verbose):
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    srcs = SOURCES + YARDSTICK_SOURCES
+    srcs = SOURCES + TRAIN_SOURCES + YARDSTICK_SOURCES
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
     _link([objs[s] for s in SOURCES], LIB, verbose)
+    _link([objs[s] for s in TRAIN_SOURCES], TRAIN_LIB, verbose, needs=[LIB])
     _link([objs[s] for s in YARDSTICK_SOURCES], YARDSTICK_LIB, verbose)
     return LIB
 

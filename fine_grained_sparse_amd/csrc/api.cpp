@@ -26,6 +26,7 @@
 
 #include "../../include/moe.h"
 #include "launch.hpp"
+#include "train.hpp"
 
 using namespace moe;
 
@@ -264,11 +265,11 @@ int64_t split_stride(const Plan& p) { return static_cast<int64_t>(p.T) * p.ldz; 
 
 // Router: logits, then the top-K gate.
 moe_status run_router(const Plan& p, const void* x, const float* W_r, const float* b, int32_t* idx, float* w,
-                      int32_t* counts, void* ws, hipStream_t s) {
+                      int32_t* counts, float* logits, void* ws, hipStream_t s) {
     moe_status st = run_logits(p, x, W_r, ws, s);
     if (st != MOE_OK) return st;
     MOE_HIP(launch_topk_gate(at<float>(ws, p.o_z), p.nsplit, split_stride(p), p.ldz, b, p.T, p.E, p.K, p.ng, p.tg,
-                             p.scale, idx, w, counts, s));
+                             p.scale, idx, w, counts, logits, s));
     return MOE_OK;
 }
 
@@ -423,7 +424,7 @@ moe_status run_forward(const Plan& p, const void* x, const float* W_r, const flo
     int32_t* idx = u_idx ? u_idx : at<int32_t>(ws, p.o_idx);
     float* w = u_w ? u_w : at<float>(ws, p.o_w);
     MOE_HIP(record(ev, MOE_EV_START, s));
-    moe_status st = run_router(p, x, W_r, b, idx, w, nullptr, ws, s);
+    moe_status st = run_router(p, x, W_r, b, idx, w, nullptr, nullptr, ws, s);
     if (st != MOE_OK) return st;
     MOE_HIP(record(ev, MOE_EV_ROUTER, s));
     return run_experts(p, x, idx, w, 0, W, out, u_counts, u_offsets, u_sorted, ws, s, ev);
@@ -461,7 +462,40 @@ moe_status check_weights(const moe_layer_desc* desc, const moe_expert_weights* W
     return MOE_OK;
 }
 
+// moe_router; logits [T, E] are written too when `train` asks for them.
+moe_status route(const moe_layer_desc* desc, const void* x, const float* W_r, const float* b, int32_t* topk_idx,
+                 float* topk_w, int32_t* expert_counts, float* logits, bool train, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+    moe_status st = check_desc(desc, false);
+    if (st != MOE_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (desc->T == 0) {  // no tokens: empty tensors may come as NULL pointers
+        if (expert_counts && !aligned16(expert_counts)) return MOE_ERR_ALIGN;
+        if (expert_counts) MOE_HIP(launch_fill_i32(expert_counts, 0, desc->E, s));
+        return MOE_OK;
+    }
+    if (!x || !W_r || !b || !topk_idx || !topk_w || (train && !logits) || !workspace) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(W_r) || !aligned16(b) || !aligned16(topk_idx) || !aligned16(topk_w) ||
+        !aligned16(workspace) || !aligned16(logits) || (expert_counts && !aligned16(expert_counts)))
+        return MOE_ERR_ALIGN;
+    const Plan p = make_plan(desc, false);
+    if (workspace_bytes < static_cast<size_t>(p.total)) return MOE_ERR_WORKSPACE;
+    return run_router(p, x, W_r, b, topk_idx, topk_w, expert_counts, logits, workspace, s);
+}
+
 }  // namespace
+
+namespace moe {
+
+moe_status router_check(const moe_layer_desc* desc) { return check_desc(desc, false); }
+
+moe_status router_with_logits(const moe_layer_desc* desc, const void* x, const float* W_r, const float* b,
+                              int32_t* topk_idx, float* topk_w, int32_t* expert_counts, float* logits,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    return route(desc, x, W_r, b, topk_idx, topk_w, expert_counts, logits, true, workspace, workspace_bytes, stream);
+}
+
+}  // namespace moe
 
 extern "C" {
 
@@ -486,21 +520,7 @@ const char* moe_status_str(moe_status st) {
 
 moe_status moe_router(const moe_layer_desc* desc, const void* x, const float* W_r, const float* b, int32_t* topk_idx,
                       float* topk_w, int32_t* expert_counts, void* workspace, size_t workspace_bytes, void* stream) {
-    moe_status st = check_desc(desc, false);
-    if (st != MOE_OK) return st;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    if (desc->T == 0) {  // no tokens: empty tensors may come as NULL pointers
-        if (expert_counts && !aligned16(expert_counts)) return MOE_ERR_ALIGN;
-        if (expert_counts) MOE_HIP(launch_fill_i32(expert_counts, 0, desc->E, s));
-        return MOE_OK;
-    }
-    if (!x || !W_r || !b || !topk_idx || !topk_w || !workspace) return MOE_ERR_NULL;
-    if (!aligned16(x) || !aligned16(W_r) || !aligned16(b) || !aligned16(topk_idx) || !aligned16(topk_w) ||
-        !aligned16(workspace) || (expert_counts && !aligned16(expert_counts)))
-        return MOE_ERR_ALIGN;
-    const Plan p = make_plan(desc, false);
-    if (workspace_bytes < static_cast<size_t>(p.total)) return MOE_ERR_WORKSPACE;
-    return run_router(p, x, W_r, b, topk_idx, topk_w, expert_counts, workspace, s);
+    return route(desc, x, W_r, b, topk_idx, topk_w, expert_counts, nullptr, false, workspace, workspace_bytes, stream);
 }
 
 moe_status moe_forward(const moe_layer_desc* desc, const void* x, const float* W_r, const float* b,

@@ -171,12 +171,13 @@ hipError_t launch_split3(const float* W, int64_t n, uint16_t* hi,
 // Sigmoid, biased top-K (limited to the topk_group best of n_group expert
 // groups when n_group > 1), renormalise and scale; z holds nsplit partial
 // logit planes of [T, ldz].  counts (nullable, E <= 1024) gets the number of
-// selections of each expert.
+// selections of each expert; logits (nullable) the summed
+// logits, [T, E].
 hipError_t launch_topk_gate(const float* z, int nsplit, int64_t split_stride,
                             int ldz, const float* b, int T, int E, int K,
                             int n_group, int topk_group, float scale,
                             int32_t* idx, float* w, int32_t* counts,
-                            hipStream_t stream);
+                            float* logits, hipStream_t stream);
 
 hipError_t launch_fill_i32(int32_t* p, int32_t v, int64_t n,
                            hipStream_t stream);

@@ -204,7 +204,7 @@ __global__ __launch_bounds__(256) void k_topk_gate(const float* __restrict__ z, 
                                                    int ldz, const float* __restrict__ b, int T, int E, int K,
                                                    int n_group, int topk_group, float scale,
                                                    int32_t* __restrict__ idx, float* __restrict__ w,
-                                                   int32_t* __restrict__ counts) {
+                                                   int32_t* __restrict__ counts, float* __restrict__ logits) {
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
     // the per-expert counts start at zero here; k_expert_counts, launched
@@ -228,6 +228,7 @@ __global__ __launch_bounds__(256) void k_topk_gate(const float* __restrict__ z, 
 #pragma unroll
             for (int p = 0; p < kMaxSplit; ++p)
                 if (p < nsplit) zz += part[p];
+            if (logits) logits[static_cast<int64_t>(t) * E + e] = zz;
             s[j] = 1.0f / (1.0f + expf(-zz));  // step 2: per-expert sigmoid
             v[j] = s[j] + b[e];                // step 3: the bias only chooses
             // A NaN score would never win a comparison and leave the arg-max
@@ -469,7 +470,7 @@ hipError_t launch_fill_i32(int32_t* p, int32_t v, int64_t n, hipStream_t stream)
 
 hipError_t launch_topk_gate(const float* z, int nsplit, int64_t split_stride, int ldz, const float* b, int T, int E,
                             int K, int n_group, int topk_group, float scale, int32_t* idx, float* w, int32_t* counts,
-                            hipStream_t stream) {
+                            float* logits, hipStream_t stream) {
     if (T <= 0) return hipSuccess;
     if (n_group < 1 || n_group > 64 || E % n_group || topk_group < 1 || topk_group > n_group ||
         (n_group > 1 && E / n_group < 2) || nsplit < 1 || nsplit > kMaxSplit)
@@ -478,7 +479,7 @@ hipError_t launch_topk_gate(const float* z, int nsplit, int64_t split_stride, in
     const int J = (E + 63) / 64;
 #define MOE_TOPK(JJ)                                                                                           \
     hipLaunchKernelGGL(k_topk_gate<JJ>, grid, block, 0, stream, z, nsplit, split_stride, ldz, b, T, E, K, n_group, \
-                       topk_group, scale, idx, w, counts)
+                       topk_group, scale, idx, w, counts, logits)
     if (J <= 1)
         MOE_TOPK(1);
     else if (J <= 2)

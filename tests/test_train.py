@@ -1,0 +1,532 @@
+"""The router's training side (include/moe_train.h): refusals on the CPU, and
+on the GPU the logits, the balance loss, its counts and every gradient
+against float64 (torch autograd of the plain formulas, and differences).
+
+Tolerances.  e = 2^-24 is half a step of fp32 relative to the value, u = 2^-8
+that of bf16.  sigma and 1 - sigma carry at most 8 e; a row's sums are of
+positive terms and at most 22 additions deep (16 in the lane, 6 over the
+wave), so the normalised scores and the gate weights carry at most 60 e, and
+each gradient term at most 128 e of the absolute values that enter it:
+  balance  inv s (1 - s) (a_j + sum_i a_i p_i),
+  gate     scale / D s (1 - s) (|dw_k| + sum_j |dw_j| s_j / D).
+"""
+import ctypes
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import fine_grained_sparse_amd as moe
+from fine_grained_sparse_amd import train
+from test_abi import ALIGN, FAKE, FAKE_ODD, NULL, OK, SHAPE, UNSUP, WS, _k2
+
+E32, U = 2.0 ** -24, 2.0 ** -8
+DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _log(msg):
+    print(msg, flush=True)
+
+
+# ------------------------------------------------------------- refusals (CPU)
+def test_train_library_exports_what_its_header_declares():
+    text = open(os.path.join(ROOT, "include", "moe_train.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    declared = set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text))
+    assert declared == set(train.TRAIN_EXPORTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", train.TRAIN_LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    assert set(re.findall(r"\bT (moe_\w+)", out)) == declared
+    for n in declared:
+        assert hasattr(train.train_lib(), n)
+
+
+def _bal(S=2, off=FAKE, mask=None, alpha=1e-3):
+    return train.Balance(S, off, mask, alpha)
+
+
+def _ref(B):
+    return None if B is None else ctypes.byref(B)
+
+
+def test_router_train_rejects_bad_arguments():
+    L, vp = train.train_lib(), ctypes.c_void_p
+
+    def f(D, x=FAKE, z=FAKE, ws=FAKE, nbytes=None, counts=None):
+        n = moe.workspace_size(D, False) if nbytes is None else nbytes
+        return L.moe_router_train(ctypes.byref(D), vp(x), vp(FAKE), vp(FAKE), vp(FAKE), vp(FAKE), vp(counts), vp(z),
+                                  vp(ws), n, None)
+    assert f(_k2(), z=None) == NULL
+    assert f(_k2(), x=None) == NULL
+    assert f(_k2(), z=FAKE_ODD) == ALIGN
+    assert f(_k2(), nbytes=moe.workspace_size(_k2(), False) - 1) == WS
+    assert f(_k2(K=17)) == SHAPE
+    assert f(_k2(act_dtype=3)) == UNSUP
+    assert f(_k2(T=0), x=None, z=None, ws=None) == OK
+    assert L.moe_router_train(None, None, None, None, None, None, None, None, None, 0, None) == NULL
+
+
+def test_balance_loss_rejects_bad_arguments():
+    L, vp = train.train_lib(), ctypes.c_void_p
+
+    def f(D, B=_bal(), z=FAKE, idx=FAKE, loss=FAKE, counts=FAKE, ws=FAKE, nbytes=1 << 40):
+        return L.moe_balance_loss(ctypes.byref(D), vp(z), vp(idx), _ref(B), vp(loss), vp(counts), vp(ws), nbytes, None)
+    D = _k2()
+    n = L.moe_balance_workspace_size(ctypes.byref(D), 2)
+    assert n > 0
+    for kw in (dict(B=None), dict(z=None), dict(idx=None), dict(loss=None), dict(counts=None), dict(ws=None)):
+        assert f(D, **kw) == NULL, kw
+    assert f(D, B=_bal(off=None)) == NULL            # two sequences need their offsets
+    for kw in (dict(z=FAKE_ODD), dict(idx=FAKE_ODD), dict(counts=FAKE_ODD), dict(ws=FAKE_ODD), dict(loss=FAKE + 2),
+               dict(B=_bal(off=FAKE_ODD)), dict(B=_bal(mask=FAKE + 1))):
+        assert f(D, **kw) == ALIGN, kw
+    assert f(D, nbytes=n - 1) == WS
+    for S in (0, -1, 65536):
+        assert f(D, B=_bal(S=S)) == SHAPE
+        assert L.moe_balance_workspace_size(ctypes.byref(D), S) == 0
+    assert f(_k2(E=1025)) == SHAPE
+    assert f(_k2(K=0)) == SHAPE
+    assert L.moe_balance_workspace_size(ctypes.byref(_k2(T=-1)), 1) == 0
+    assert L.moe_balance_loss(None, None, None, None, None, None, None, 0, None) == NULL
+
+
+def test_backward_rejects_bad_arguments():
+    L, vp = train.train_lib(), ctypes.c_void_p
+
+    def g(D, B=_bal(), z=FAKE, idx=FAKE, dw=FAKE, counts=FAKE, dl=None, out=FAKE):
+        return L.moe_gate_backward(ctypes.byref(D), vp(z), vp(idx), vp(dw), _ref(B), vp(counts), vp(dl), vp(out), None)
+
+    def r(D, B=_bal(), x=FAKE, W=FAKE, z=FAKE, idx=FAKE, dw=FAKE, counts=FAKE, dl=None, dx=FAKE, dW=FAKE, ws=FAKE,
+          nbytes=1 << 50):
+        return L.moe_router_backward(ctypes.byref(D), vp(x), vp(W), vp(z), vp(idx), vp(dw), _ref(B), vp(counts),
+                                     vp(dl), vp(dx), vp(dW), vp(ws), nbytes, None)
+    D = _k2()
+    n = L.moe_router_backward_workspace_size(ctypes.byref(D))
+    assert n > 0 and L.moe_router_backward_workspace_size(ctypes.byref(_k2(d=100))) == 0
+    for f in (g, r):
+        assert f(D, z=None) == NULL
+        assert f(D, idx=None) == NULL
+        assert f(D, B=None) == NULL                      # counts without their sequences
+        assert f(D, dw=None, counts=None) == NULL        # no gradient at all
+        assert f(D, B=_bal(off=None)) == NULL
+        for kw in (dict(z=FAKE_ODD), dict(idx=FAKE_ODD), dict(dw=FAKE_ODD), dict(counts=FAKE_ODD), dict(dl=FAKE + 2),
+                   dict(B=_bal(mask=FAKE_ODD))):
+            assert f(D, **kw) == ALIGN, kw
+        assert f(D, B=_bal(S=70000)) == SHAPE
+        assert f(_k2(E=1025)) == SHAPE
+        assert f(_k2(T=1 << 30)) == SHAPE                # T K past 31 bits
+    assert g(D, out=None) == NULL
+    assert g(D, out=FAKE_ODD) == ALIGN
+    assert r(D, dx=None, dW=None) == NULL
+    assert r(D, x=None) == NULL                          # dW_r needs x
+    assert r(D, W=None) == NULL                          # dx needs W_r
+    assert r(D, ws=None) == NULL
+    assert r(D, dx=FAKE_ODD) == ALIGN
+    assert r(D, nbytes=n - 1) == WS
+    assert r(_k2(act_dtype=2)) == UNSUP
+    assert g(_k2(T=0), z=None, idx=None, dw=None, counts=None, out=None) == OK
+    assert r(_k2(T=0), x=None, z=None, idx=None, dw=None, counts=None, dW=None, ws=None) == OK
+
+
+# ------------------------------------------------------------------ reference
+def _make(seed, T, E, K, S, masked=0.0, outside=False, spread=1.0):
+    """Inputs on the CPU: logits, chosen ids, gate-weight gradients, offsets, mask."""
+    r = np.random.default_rng(seed)
+    z = r.normal(0, spread, (T, E)).astype(np.float32)
+    idx = np.sort(np.argsort(-z - 0.3 * r.random((T, E)), axis=1)[:, :K], axis=1).astype(np.int32)
+    dw = r.normal(0, 1, (T, K)).astype(np.float32)
+    lo, hi = (T // 5, T - T // 7) if outside else (0, T)
+    off = np.sort(np.concatenate([[lo, hi], r.integers(lo, hi + 1, S - 1)])).astype(np.int32)
+    mask = (r.random(T) >= masked).astype(np.uint8) if masked else None
+    return z, idx, dw, off, mask
+
+
+def _loss64(s, idx, off, mask, alpha):
+    """The loss in float64 from its definition, of the scores s, and the counts."""
+    T, E = s.shape
+    K, S = idx.shape[1], len(off) - 1
+    p = s / (s.sum(1, keepdim=True) + 1e-20)
+    loss, counts = torch.zeros((), dtype=torch.float64), torch.zeros(S, E, dtype=torch.int32)
+    for q in range(S):
+        t = torch.arange(int(off[q]), int(off[q + 1]))
+        if mask is not None:
+            t = t[mask[t] != 0]
+        n = len(t)
+        if n == 0:
+            continue
+        counts[q] = torch.bincount(idx[t].flatten().long(), minlength=E).int()
+        f = counts[q].double() * E / (K * n)
+        loss = loss + alpha / S * (f * p[t].mean(0)).sum()
+    return loss, counts
+
+
+def _weights64(s, idx, scale):
+    s = s.gather(1, idx.long())
+    return scale * s / (s.sum(1, keepdim=True) + 1e-20)
+
+
+def _reference(z, idx, dw, off, mask, alpha, scale, gate=True, balance=True, d_loss=1.0):
+    """loss, counts, dz in float64, and dz's tolerance: autograd to the scores s, then
+    ds/dz = sigmoid(z) sigmoid(-z) (1 - s itself would lose, in float64 too, what lies below 2^-53)."""
+    Z = torch.from_numpy(z).double()
+    s = torch.sigmoid(Z).requires_grad_()
+    I, O = torch.from_numpy(idx), torch.from_numpy(off)
+    M = None if mask is None else torch.from_numpy(mask)
+    live = torch.ones(len(z), 1, dtype=torch.float64) if M is None else (M != 0).double()[:, None]
+    loss, counts = _loss64(s, I, O, M, alpha)
+    total = torch.zeros((), dtype=torch.float64)
+    if balance:
+        total = total + d_loss * loss
+    if gate:
+        total = total + (torch.from_numpy(dw).double() * live * _weights64(s, I, scale)).sum()
+    if total.requires_grad:
+        total.backward()
+    with torch.no_grad():
+        sc = s * torch.sigmoid(-Z)
+        dz = s.grad * sc if s.grad is not None else torch.zeros_like(Z)
+        tol = torch.zeros_like(s)
+        if balance:
+            S, T, E, K = len(off) - 1, *z.shape, idx.shape[1]
+            a = torch.zeros(T, E, dtype=torch.float64)
+            for q in range(S):
+                n = counts[q].sum().item() / K
+                if n:
+                    a[int(off[q]):int(off[q + 1])] = abs(d_loss) * alpha / S * E / (K * n * n) * counts[q].double()
+            tot = s.sum(1, keepdim=True)
+            tol += sc / tot * (a + (a * s).sum(1, keepdim=True) / tot)
+        if gate:
+            si, g = s.gather(1, I.long()), torch.from_numpy(dw).double().abs()
+            den = si.sum(1, keepdim=True)
+            tol.scatter_add_(1, I.long(), sc.gather(1, I.long()) * scale / den * (g + (g * si).sum(1, keepdim=True) / den))
+        tol = tol * live * 128 * E32 + 1e-38
+    return loss.detach(), counts, dz.detach(), tol
+
+
+def _dev(*arrays):
+    return [None if a is None else torch.from_numpy(a).to(DEV) for a in arrays]
+
+
+CASES = [  # T, E, K, S, masked, outside
+    (1, 1, 1, 1, 0.0, False),
+    (1, 384, 8, 1, 0.0, False),
+    (3, 2, 1, 2, 0.0, False),
+    (7, 63, 5, 3, 0.0, True),
+    (33, 65, 16, 40, 0.0, False),       # more sequences than tokens
+    (64, 129, 4, 1, 0.3, False),
+    (65, 128, 16, 2, 0.0, True),
+    (128, 32, 4, 1, 0.0, False),
+    (257, 385, 8, 5, 0.2, True),
+    (300, 1023, 16, 4, 0.1, False),
+    (500, 896, 16, 3, 0.0, False),
+    (513, 1024, 3, 64, 0.5, False),
+    (1000, 513, 2, 7, 0.9, True),
+    (4097, 48, 6, 9, 0.05, False),
+    (40000, 20, 3, 11, 0.05, True),     # 64-token chunks
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
+def test_loss_counts_and_logit_gradient(case):
+    T, E, K, S, masked, outside = case
+    _log(f"[gpu] balance T={T} E={E} K={K} S={S} masked={masked} outside={outside}")
+    z, idx, dw, off, mask = _make(5, T, E, K, S, masked, outside)
+    alpha, scale = 0.37, 2.827
+    loss, counts, dz, tol = _reference(z, idx, dw, off, mask, alpha, scale)
+    gz, gi, gw, go, gm = _dev(z, idx, dw, off, mask)
+    l, c = moe.balance_loss(gz, gi, alpha, seq_offsets=go, token_mask=gm)
+    kw = dict(alpha=alpha, seq_counts=c, seq_offsets=go, token_mask=gm)
+    both = moe.gate_backward(gz, gi, gw, scale, **kw)
+    gate = moe.gate_backward(gz, gi, gw, scale, seq_offsets=go, token_mask=gm)
+    bal = moe.gate_backward(gz, gi, None, scale, d_loss=torch.tensor(-2.5, device=DEV), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(c.cpu(), counts)
+    # positive terms: 60 e each, the token sums at most 16 + 4 + T / 512 + 16 deep, E / 64 + 26 more for the loss
+    assert abs(l.item() - loss.item()) <= (160 + T / 256) * E32 * abs(loss.item())
+    worst = ((both.cpu().double() - dz).abs() / tol).max().item()
+    _, _, dg, tg = _reference(z, idx, dw, off, mask, alpha, scale, balance=False)
+    wg = ((gate.cpu().double() - dg).abs() / tg).max().item()
+    _, _, db, tb = _reference(z, idx, dw, off, mask, alpha, scale, gate=False, d_loss=-2.5)
+    wb = ((bal.cpu().double() - db).abs() / tb).max().item()
+    _log(f"[gpu]   worst element: both {worst:.3f}, gate {wg:.3f}, balance {wb:.3f} of the tolerance")
+    assert max(worst, wg, wb) <= 1.0
+    again = moe.balance_loss(gz, gi, alpha, seq_offsets=go, token_mask=gm)
+    assert torch.equal(again[0], l) and torch.equal(again[1], c)
+    assert torch.equal(moe.gate_backward(gz, gi, gw, scale, **kw), both)
+
+
+@pytest.mark.gpu
+def test_gradient_against_differences():
+    # central differences of the float64 loss along random directions, step h: the truncation is
+    # h^2 / 6 |third derivative|, below 1e-7 relative at h = 1e-3, and the kernel's own error 128 e
+    z, idx, dw, off, mask = _make(17, 96, 40, 5, 3, 0.1)
+    alpha, scale = 0.5, 2.827
+    gz, gi, gw, go, gm = _dev(z, idx, dw, off, mask)
+    _, c = moe.balance_loss(gz, gi, alpha, seq_offsets=go, token_mask=gm)
+    d = moe.gate_backward(gz, gi, gw, scale, alpha=alpha, seq_counts=c, seq_offsets=go, token_mask=gm).cpu().double()
+    I, O, M = torch.from_numpy(idx), torch.from_numpy(off), torch.from_numpy(mask)
+    live = (M != 0).double()[:, None]
+
+    def total(Z):
+        s = torch.sigmoid(Z)
+        return _loss64(s, I, O, M, alpha)[0] + (torch.from_numpy(dw).double() * live * _weights64(s, I, scale)).sum()
+    Z = torch.from_numpy(z).double()
+    r = np.random.default_rng(1)
+    for _ in range(8):
+        v = torch.from_numpy(r.normal(0, 1, z.shape))
+        h = 1e-3
+        want = (total(Z + h * v) - total(Z - h * v)) / (2 * h)
+        # |error| <= 128 e of the terms' absolute sum, and the truncation (third derivatives of s and w are
+        # below 1, v^3 averages 1.6): h^2 / 6 * 8 * sum |dw| scale / K
+        slack = 128 * E32 * (d.abs() * v.abs()).sum() * 4 + h * h / 6 * 8 * scale * np.abs(dw).sum() / 5
+        assert abs((d * v).sum() - want) <= slack
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread", [30.0, 200.0])
+def test_saturated_logits(spread):
+    # sigma at both ends: 1 - s keeps its relative accuracy, rows of vanishing scores stay finite
+    z, idx, dw, off, mask = _make(23, 70, 50, 4, 2, spread=spread)
+    z[5] = -300.0
+    z[6] = 300.0
+    gz, gi, gw, go, _ = _dev(z, idx, dw, off, mask)
+    l, c = moe.balance_loss(gz, gi, 0.1, seq_offsets=go)
+    d = moe.gate_backward(gz, gi, gw, alpha=0.1, seq_counts=c, seq_offsets=go)
+    torch.cuda.synchronize()
+    assert torch.isfinite(l) and torch.isfinite(d).all()
+    loss, counts, dz, tol = _reference(z, idx, dw, off, mask, 0.1, 2.827)
+    assert torch.equal(c.cpu(), counts)
+    # rows whose every score is below the 1e-20 guard (row 5) are governed by the guard: skipped below
+    keep = torch.ones(70, dtype=torch.bool)
+    keep[5] = False
+    # logits are held at +-87 (s = 1.6e-38), where the exact s is smaller still: 1e-36 covers any term of them
+    err = (d.cpu().double() - dz).abs()
+    assert (err[keep] <= tol[keep] + 1e-30).all()
+    assert abs(l.item() - loss.item()) <= 1e-4 * abs(loss.item())
+
+
+@pytest.mark.gpu
+def test_masked_tokens_may_hold_anything():
+    z, idx, dw, off, mask = _make(29, 130, 96, 6, 4, 0.4)
+    alpha = 0.2
+    dead = np.flatnonzero(mask == 0)
+    clean = _dev(z, idx, dw, off, mask)
+    z2, idx2, dw2 = z.copy(), idx.copy(), dw.copy()
+    z2[dead[0]], z2[dead[1], 3], z2[dead[2]] = np.nan, np.inf, -np.inf
+    idx2[dead[3]] = 12345678
+    idx2[dead[4]] = -1
+    dw2[dead] = np.nan
+    dirty = _dev(z2, idx2, dw2, off, mask)
+    outs = []
+    for gz, gi, gw, go, gm in (clean, dirty):
+        l, c = moe.balance_loss(gz, gi, alpha, seq_offsets=go, token_mask=gm)
+        outs.append((l, c, moe.gate_backward(gz, gi, gw, alpha=alpha, seq_counts=c, seq_offsets=go, token_mask=gm)))
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert (outs[0][2][torch.from_numpy(dead).to(DEV)] == 0).all()
+
+
+@pytest.mark.gpu
+def test_empty_sequences_and_batches():
+    gz = torch.randn(10, 16, device=DEV)
+    gi = torch.arange(2, dtype=torch.int32, device=DEV).repeat(10, 1)
+    off = torch.tensor([4, 4, 4, 9, 9], dtype=torch.int32, device=DEV)
+    l, c = moe.balance_loss(gz, gi, 1.0, seq_offsets=off)
+    d = moe.gate_backward(gz, gi, None, alpha=1.0, seq_counts=c, seq_offsets=off)
+    assert (c[[0, 1, 3]] == 0).all() and c[2].sum() == 10
+    assert (d[:4] == 0).all() and (d[9] == 0).all() and (d[4:9] != 0).any()
+    assert torch.isfinite(l)
+    none = torch.zeros(10, dtype=torch.bool, device=DEV)
+    l, c = moe.balance_loss(gz, gi, 1.0, token_mask=none)
+    assert l.item() == 0 and (c == 0).all()
+    assert (moe.gate_backward(gz, gi, torch.ones(10, 2, device=DEV), alpha=1.0, seq_counts=c, token_mask=none) == 0).all()
+    l, c = moe.balance_loss(gz[:0], gi[:0], 1.0, seq_offsets=torch.zeros(4, dtype=torch.int32, device=DEV))
+    assert l.item() == 0 and c.shape == (3, 16) and (c == 0).all()
+    x = torch.randn(0, 64, device=DEV)
+    dx, dW = moe.router_backward(x, torch.randn(16, 64, device=DEV), gz[:0], gi[:0], torch.ones(0, 2, device=DEV))
+    assert dx.shape == (0, 64) and (dW == 0).all()
+
+
+@pytest.mark.gpu
+def test_repeated_and_foreign_ids():
+    # an id twice in a token adds its two gradients; ids outside 0 .. E - 1 are skipped
+    z = torch.randn(3, 8, device=DEV)
+    dw = torch.randn(3, 3, device=DEV)
+    idx = torch.tensor([[1, 1, 4], [0, 8, -5], [7, 2, 3]], dtype=torch.int32, device=DEV)
+    d = moe.gate_backward(z, idx, dw).double().cpu()
+    for t in range(3):
+        Z = z[t].double().cpu().requires_grad_()
+        ok = [(k, int(idx[t, k])) for k in range(3) if 0 <= int(idx[t, k]) < 8]
+        s = torch.sigmoid(Z)[[e for _, e in ok]]
+        (2.827 * s / s.sum() * dw[t].double().cpu()[[k for k, _ in ok]]).sum().backward()
+        assert ((d[t] - Z.grad).abs() <= 256 * E32 * 2.827 * dw[t].double().cpu().abs().sum()).all()
+    _, c = moe.balance_loss(z, idx, 1.0)
+    assert c[0].tolist() == [1, 2, 1, 1, 1, 0, 0, 1]
+
+
+BACK = [  # T, d, E, K, S, masked, dtype
+    (1, 64, 1, 1, 1, 0.0, "f32"),
+    (1, 128, 20, 3, 1, 0.0, "bf16"),
+    (5, 320, 48, 6, 2, 0.0, "bf16"),
+    (63, 192, 65, 4, 1, 0.2, "bf16"),
+    (64, 1024, 384, 8, 1, 0.0, "bf16"),
+    (65, 64, 63, 16, 3, 0.0, "f32"),
+    (77, 320, 20, 3, 1, 0.0, "f32"),
+    (300, 1024, 48, 6, 2, 0.1, "bf16"),
+    (301, 576, 129, 5, 4, 0.0, "f32"),
+    (513, 448, 897, 16, 5, 0.05, "bf16"),
+    (777, 1088, 385, 8, 3, 0.3, "bf16"),
+    (1200, 256, 1024, 16, 2, 0.0, "bf16"),
+    (3001, 704, 200, 2, 3, 0.1, "bf16"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", BACK, ids=lambda c: "x".join(map(str, c)))
+def test_router_backward(case):
+    T, d, E, K, S, masked, dt = case
+    _log(f"[gpu] router backward T={T} d={d} E={E} K={K} S={S} {dt}")
+    z, idx, dw, off, mask = _make(41, T, E, K, S, masked)
+    r = np.random.default_rng(3)
+    x = torch.from_numpy(r.normal(0, 1, (T, d)).astype(np.float32))
+    x = x.bfloat16() if dt == "bf16" else x
+    W = torch.from_numpy((r.normal(0, 1, (E, d)) / d ** 0.5).astype(np.float32))
+    alpha, scale = 0.3, 2.827
+    _, counts, dz, tz = _reference(z, idx, dw, off, mask, alpha, scale)
+    gz, gi, gw, go, gm = _dev(z, idx, dw, off, mask)
+    gx, gW = x.to(DEV), W.to(DEV)
+    kw = dict(alpha=alpha, seq_counts=counts.to(DEV), seq_offsets=go, token_mask=gm)
+    dx, dW = moe.router_backward(gx, gW, gz, gi, gw, scale, **kw)
+    only_x = moe.router_backward(gx, gW, gz, gi, gw, scale, need_dW=False, **kw)
+    only_w = moe.router_backward(gx, gW, gz, gi, gw, scale, need_dx=False, **kw)
+    torch.cuda.synchronize()
+    assert dx.dtype == x.dtype and dW.dtype == torch.float32
+    assert torch.equal(only_x[0], dx) and only_x[1] is None
+    assert torch.equal(only_w[1], dW) and only_w[0] is None
+    X, Wd, a = x.double(), W.double(), dz.abs()
+    # dx: sums of E (bf16: 3 E) products, each part of 16 bits: 2^-16 from dz, from W_r and from the product
+    # of the two low parts left out; then the rounding to x's type
+    parts = 3 * 2.0 ** -16 if dt == "bf16" else 0.0
+    ref = dz @ Wd
+    tol = (a @ Wd.abs()) * (parts + 3 * (E + 64) * E32) + tz @ Wd.abs()
+    tol = tol + (U if dt == "bf16" else E32) * (ref.abs() + tol) + 1e-38
+    wx = ((dx.cpu().double() - ref).abs() / tol).max().item()
+    # dW_r: the parts hold dz exactly, 3 T products
+    refw = dz.T @ X
+    tolw = (a.T @ X.abs()) * 3 * (T + 64) * E32 + tz.T @ X.abs() + 1e-38
+    ww = ((dW.cpu().double() - refw).abs() / tolw).max().item()
+    # as squares: sqrt of the number of roundings, four of them each
+    relw = ((dW.cpu().double() - refw).norm() / refw.norm()).item()
+    relx = ((dx.cpu().double() - ref).norm() / ref.norm()).item()
+    _log(f"[gpu]   worst of the tolerance: dx {wx:.3f}, dW {ww:.3f}; l2 dx {relx:.2e}, dW {relw:.2e}")
+    assert max(wx, ww) <= 1.0
+    if E == 1:  # one expert: p and w are constants, every gradient is exactly 0, and nothing to be relative to
+        return
+    assert relw <= (128 + 4 * (3 * T) ** 0.5) * E32
+    assert relx <= (U if dt == "bf16" else (128 + 4 * (3 * E) ** 0.5) * E32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,E,K,dt,groups", [(1, 256, 20, 3, "bf16", (1, 1)), (40, 512, 384, 8, "bf16", (8, 4)),
+                                               (300, 1024, 48, 6, "bf16", (1, 1)), (77, 320, 20, 3, "f32", (1, 1)),
+                                               (5, 128, 1023, 16, "bf16", (1, 1))])
+def test_router_train_is_the_router_with_its_logits(T, d, E, K, dt, groups):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn(T, d, device=DEV, generator=g)
+    x = x.bfloat16() if dt == "bf16" else x
+    W = torch.randn(E, d, device=DEV, generator=g) * d ** -0.5
+    b = torch.rand(E, device=DEV, generator=g) * 0.04 - 0.02
+    kw = dict(n_group=groups[0], topk_group=groups[1])
+    ref = moe.router(x, W, b, K, **kw)
+    idx, w, cnt, z = moe.router_train(x, W, b, K, **kw)
+    torch.cuda.synchronize()
+    for u, v in zip(ref, (idx, w, cnt)):
+        assert torch.equal(u, v)
+    want = x.double() @ W.double().T
+    # fp32 sums of d products (bf16: of 3 d), exact products
+    tol = 3 * (d + 64) * E32 * (x.double().abs() @ W.double().abs().T)
+    assert ((z.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+def test_a_training_step_captured_and_replayed():
+    # router -> balance loss -> backward -> bias update as one graph on a side stream, replayed with new inputs
+    # and eager work in between; and the whole chain against float64
+    T, d, E, K, S = 200, 256, 48, 4, 3
+    g = torch.Generator(device=DEV).manual_seed(77)
+    xs = [torch.randn(T, d, device=DEV, generator=g).bfloat16() for _ in range(3)]
+    W = torch.randn(E, d, device=DEV, generator=g) * d ** -0.5
+    dw = torch.randn(T, K, device=DEV, generator=g)
+    off = torch.tensor([0, 50, 120, 200], dtype=torch.int32, device=DEV)
+    x, b = xs[0].clone(), torch.zeros(E, device=DEV)
+    ws = moe.Workspace()
+
+    def step(x, b, ws, stream=None):
+        idx, w, cnt, z = moe.router_train(x, W, b, K, workspace=ws, stream=stream)
+        loss, c = moe.balance_loss(z, idx, 0.01, seq_offsets=off, workspace=ws, stream=stream)
+        dx, dW = moe.router_backward(x, W, z, idx, dw, alpha=0.01, seq_counts=c, seq_offsets=off, workspace=ws,
+                                     stream=stream)
+        moe.bias_update(cnt, b, stream=stream)
+        return loss, c, dx, dW, idx, z
+    want = []
+    for xi in xs:
+        bi = torch.zeros(E, device=DEV)
+        want.append([t.clone() for t in step(xi, bi, moe.Workspace())] + [bi])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    step(x, b, ws, s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step(x, b, ws, s)
+    for i in (1, 2, 0, 2):
+        x.copy_(xs[i])
+        b.zero_()
+        step(xs[1], torch.zeros(E, device=DEV), moe.Workspace())   # eager work between the replays
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip((*out, b), want[i]):
+            assert torch.equal(got, ref), i
+    loss, c, dx, dW, idx, z = (t.cpu() for t in want[0][:6])
+    l64, c64, dz, _ = _reference(z.numpy(), idx.numpy(), dw.cpu().numpy(), off.cpu().numpy(), None, 0.01, 2.827)
+    assert torch.equal(c, c64) and abs(loss.item() - l64.item()) <= 200 * E32 * abs(l64.item())
+    assert torch.equal(c.sum(0), torch.bincount(idx.flatten().long(), minlength=E))
+    assert (dx.double() - dz @ W.double().cpu()).norm() <= U * dx.double().norm()
+    assert (dW.double() - dz.T @ xs[0].double().cpu()).norm() <= 256 * E32 * dW.double().norm()
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    z = torch.randn(6, 10, device=DEV)
+    idx = torch.zeros(6, 2, dtype=torch.int32, device=DEV)
+    dw = torch.zeros(6, 2, device=DEV)
+    _, c = moe.balance_loss(z, idx, 1.0)
+    bad = [lambda: moe.balance_loss(z.double(), idx, 1.0),
+           lambda: moe.balance_loss(z.T, idx, 1.0),
+           lambda: moe.balance_loss(z, idx.long(), 1.0),
+           lambda: moe.balance_loss(z, idx[:5], 1.0),
+           lambda: moe.balance_loss(z, idx, 1.0, seq_offsets=torch.zeros(1, dtype=torch.int32, device=DEV)),
+           lambda: moe.balance_loss(z, idx, 1.0, token_mask=torch.ones(5, dtype=torch.uint8, device=DEV)),
+           lambda: moe.balance_loss(z, idx, 1.0, token_mask=torch.ones(6, device=DEV)),
+           lambda: moe.balance_loss(z.cpu(), idx, 1.0),
+           lambda: moe.gate_backward(z, idx, None),
+           lambda: moe.gate_backward(z, idx, dw, alpha=1.0),
+           lambda: moe.gate_backward(z, idx, dw, seq_counts=c),
+           lambda: moe.gate_backward(z, idx, dw[:, :1], alpha=1.0, seq_counts=c),
+           lambda: moe.gate_backward(z, idx, dw, alpha=1.0, seq_counts=c[:, :9]),
+           lambda: moe.gate_backward(z, idx, dw, alpha=1.0, seq_counts=c, d_loss=torch.ones(2, device=DEV)),
+           lambda: moe.router_backward(torch.zeros(6, 64, device=DEV), torch.zeros(10, 128, device=DEV), z, idx, dw),
+           lambda: moe.router_backward(torch.zeros(5, 64, device=DEV), torch.zeros(10, 64, device=DEV), z, idx, dw),
+           lambda: moe.router_backward(torch.zeros(6, 64, device=DEV), torch.zeros(10, 64, device=DEV), z, idx, dw,
+                                       need_dx=False, need_dW=False),
+           lambda: moe.router_backward(torch.zeros(6, 60, device=DEV), torch.zeros(10, 60, device=DEV), z, idx, dw)]
+    for i, f in enumerate(bad):
+        with pytest.raises((TypeError, ValueError, moe.MoeError)):
+            f()
+            _log(f"case {i} was accepted")
