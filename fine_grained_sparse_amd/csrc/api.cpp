@@ -35,6 +35,11 @@ namespace {
 constexpr int64_t kAlign = 256;
 constexpr int kRouterGemvT = 32;  // router logits by k_router_gemv up to this many tokens
 static_assert(kRouterGemvT <= kRouterGemvMaxT, "the kernel's token capacity");
+// Latent maps of FP4 layers by launch_dense_rows16 up to this many tokens.
+// A 7168-to-3584 layer with few weights otherwise, against the GEMM tiles: 95
+// against 338 us at 8 tokens, 270 / 437 at 64, 367 / 441 at 128, 609 / 488 at
+// 256 (every 16 tokens are another pass over the weights).
+constexpr int kDenseRows16T = 128;
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -47,6 +52,7 @@ struct Plan {
     bool packed;                              // weights in MOE_LAYOUT_FRAG16
     bool f8;                                  // routed experts in block-scaled FP8
     bool f4;                                  // routed experts in group-scaled FP4
+    bool direct, fused;                       // ... without a dispatch; down projection and combine in one
     int64_t ys;                               // element size of the experts' outputs Y
     int64_t es;                               // element size
     // router
@@ -158,6 +164,8 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
     p.f8 = forward && D->w_dtype == MOE_FP8_E4M3;
     p.f4 = forward && D->w_dtype == MOE_FP4_E2M1;
     p.ys = p.f4 ? 4 : p.es;
+    p.direct = p.f4 && fp4_direct(p.T);
+    p.fused = p.direct && fp4_fused(p.T);
     const TileCfg big = p.packed ? TILE_WIDE : TILE_LARGE;
     const int64_t arows = slice ? cdiv(p.A * p.E, E_total) : p.A;  // expected routed rows
     p.ecfg = (arows >= 10ll * p.E && p.dt == DT_BF16) ? big : (p.f8 ? TILE_WIDE16 : TILE_SMALL);
@@ -169,7 +177,7 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
         const int64_t nt = std::max<int64_t>(cdiv(std::max(p.F, p.Fsh), 256), cdiv(p.din, 512));
         if (mt * nt < 128) p.ecfg = TILE_NARROW;
     }
-    p.bm = p.f4 ? fp4_bm() : tile_bm(p.ecfg);
+    p.bm = p.f4 ? fp4_bm(arows, p.E, p.ns > 0) : tile_bm(p.ecfg);
     // dense maps of the latent form: 128-row tiles from 512 tokens (K3
     // shapes: 12.5 -> 10.3 ms at 768 tokens with the expert switch above;
     // below 512 the two measured the same within run-to-run noise)
@@ -284,13 +292,34 @@ hipError_t launch_f8(const Plan& p, GemmArgs g, const uint8_t* bs, const uint8_t
 }
 
 // The same with FP4 weights.
-hipError_t launch_f4(const Plan& p, GemmArgs g, const uint8_t* bs, const uint8_t* bsu, Epi epi, int max_n,
-                     hipStream_t s) {
+GemmArgs f4_args(GemmArgs g, const uint8_t* bs, const uint8_t* bsu) {
     g.g[0].bs = bs;
     g.g[0].bsu = bsu;
     g.g[0].b_estride = static_cast<int64_t>(g.g[0].N) * g.g[0].seg[0].K / 2;
     g.g[0].s_estride = static_cast<int64_t>(g.g[0].N) * g.g[0].seg[0].K / 32;
-    return launch_gemm_fp4(g, epi, p.max_tiles, max_n, s);
+    return g;
+}
+hipError_t launch_f4(const Plan& p, const GemmArgs& args, const uint8_t* bs, const uint8_t* bsu, Epi epi, int max_n,
+                     const int32_t* idx, int e0, hipStream_t s) {
+    const GemmArgs g = f4_args(args, bs, bsu);
+    if (p.direct) return launch_fp4_direct(g, epi, idx, p.T, p.K, e0, p.E, s);
+    return launch_gemm_fp4(g, epi, p.bm, p.max_tiles, max_n, s);
+}
+
+// A dense map of the latent form over the batch.
+hipError_t launch_dense(const Plan& p, const GemmArgs& g, int n, hipStream_t s) {
+    if (p.f4 && p.T <= kDenseRows16T) return launch_dense_rows16(g, s);
+    return launch_gemm(g, p.dt, false, EPI_STORE, p.dcfg, static_cast<int>(cdiv(p.T, tile_bm(p.dcfg))), n, p.packed, s);
+}
+
+// Y (and the shared experts' rows ysh) -> sum of a token's rows.
+hipError_t combine(const Plan& p, const void* Y, const void* ysh, const int32_t* idx, int e0, const int32_t* pos,
+                   const float* w, int N, void* out, hipStream_t s) {
+    if (p.fused) return hipSuccess;  // the down projection did it
+    if (p.direct)
+        return launch_combine_direct(static_cast<const float*>(Y), N, static_cast<const float*>(ysh), idx, e0, p.E, w,
+                                     p.T, p.K, N, static_cast<uint16_t*>(out), N, s);
+    return launch_combine(p.dt, p.f4, Y, N, ysh, pos, w, p.T, p.K, N, out, N, s);
 }
 
 hipError_t record(void* const* ev, int i, hipStream_t s) {
@@ -317,8 +346,10 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
     const bool latent = p.dl > 0;
 
     // shared tiles ride in the routed launches (rows = tokens)
-    MOE_HIP(launch_dispatch(idx, p.T, p.E, e0, p.K, p.bm, p.ns ? p.T : 0, at<uint64_t>(ws, p.o_masks),
-                            at<int32_t>(ws, p.o_cbase), counts, offsets, sorted, pos, tiles, ntiles, s));
+    // (a direct launch needs no dispatch, but its results may be asked for)
+    if (!p.direct || u_counts || u_offsets || u_sorted)
+        MOE_HIP(launch_dispatch(idx, p.T, p.E, e0, p.K, p.bm, p.ns ? p.T : 0, at<uint64_t>(ws, p.o_masks),
+                                at<int32_t>(ws, p.o_cbase), counts, offsets, sorted, pos, tiles, ntiles, s));
     MOE_HIP(record(ev, MOE_EV_DISPATCH, s));
 
     const void* xin = x;
@@ -330,8 +361,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         g.g[0].C = xlat;
         g.g[0].ldc = p.dl;
         g.M = p.T;
-        MOE_HIP(launch_gemm(g, p.dt, false, EPI_STORE, p.dcfg, static_cast<int>(cdiv(p.T, tile_bm(p.dcfg))), p.dl,
-                            p.packed, s));
+        MOE_HIP(launch_dense(p, g, p.dl, s));
         xin = xlat;
     }
     MOE_HIP(record(ev, MOE_EV_LATENT, s));
@@ -344,7 +374,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         R0.nseg = 1;
         R0.N = p.F;
         R0.b_estride = static_cast<int64_t>(p.F) * p.din;
-        R0.rowmap = sorted;
+        R0.rowmap = p.direct ? nullptr : sorted;
         R0.C = H;
         R0.ldc = p.F;
         GemmGroup& S1 = g.g[1];
@@ -356,7 +386,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         g.tiles = tiles;
         g.ntiles = ntiles;
         if (p.f4)
-            MOE_HIP(launch_f4(p, g, W->W_gate_scale, W->W_up_scale, EPI_SWIGLU, std::max(p.F, p.Fsh), s));
+            MOE_HIP(launch_f4(p, g, W->W_gate_scale, W->W_up_scale, EPI_SWIGLU, std::max(p.F, p.Fsh), idx, e0, s));
         else if (p.f8)
             MOE_HIP(launch_f8(p, g, W->W_gate_scale, W->W_up_scale, EPI_SWIGLU, std::max(p.F, p.Fsh), s));
         else
@@ -386,8 +416,12 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         }
         g.tiles = tiles;
         g.ntiles = ntiles;
-        if (p.f4)
-            MOE_HIP(launch_f4(p, g, W->W_down_scale, nullptr, EPI_STORE, p.din, s));
+        if (p.fused) {
+            g = f4_args(g, W->W_down_scale, nullptr);
+            MOE_HIP(launch_fp4_down_combine(g, idx, w, p.T, p.K, e0, p.E, static_cast<uint16_t*>(latent ? R : out),
+                                            p.din, s));
+        } else if (p.f4)
+            MOE_HIP(launch_f4(p, g, W->W_down_scale, nullptr, EPI_STORE, p.din, idx, e0, s));
         else if (p.f8)
             MOE_HIP(launch_f8(p, g, W->W_down_scale, nullptr, EPI_STORE, p.din, s));
         else
@@ -396,12 +430,12 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
     MOE_HIP(record(ev, MOE_EV_DOWN, s));
     if (!latent) {
         const void* ysh = p.ns ? static_cast<const void*>(Y + p.A * p.d * p.ys) : nullptr;
-        MOE_HIP(launch_combine(p.dt, p.f4, Y, p.d, ysh, pos, w, p.T, p.K, p.d, out, p.d, s));
+        MOE_HIP(combine(p, Y, ysh, idx, e0, pos, w, p.d, out, s));
         MOE_HIP(record(ev, MOE_EV_END, s));
         return MOE_OK;
     }
     // latent form: R = sum_k w Y[pos];  out = Hs Ws_down^T + R W_lat_up^T
-    MOE_HIP(launch_combine(p.dt, p.f4, Y, p.dl, nullptr, pos, w, p.T, p.K, p.dl, R, p.dl, s));
+    MOE_HIP(combine(p, Y, nullptr, idx, e0, pos, w, p.dl, R, s));
     GemmArgs g = gemm_args();
     GemmGroup& G = g.g[0];
     int ns = 0;
@@ -412,8 +446,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
     G.C = out;
     G.ldc = p.d;
     g.M = p.T;
-    MOE_HIP(launch_gemm(g, p.dt, false, EPI_STORE, p.dcfg, static_cast<int>(cdiv(p.T, tile_bm(p.dcfg))), p.d,
-                        p.packed, s));
+    MOE_HIP(launch_dense(p, g, p.d, s));
     MOE_HIP(record(ev, MOE_EV_END, s));
     return MOE_OK;
 }

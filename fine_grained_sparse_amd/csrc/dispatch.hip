@@ -96,14 +96,10 @@ __global__ __launch_bounds__(256) void k_dispatch_chunk_scan(const uint64_t* __r
     if (lane == 63) counts[e] = incl;
 }
 
-// One block of 1024 threads; thread e owns expert e (its count from
-// k_dispatch_chunk_scan).
-__global__ __launch_bounds__(1024) void k_dispatch_scan(int E, int bm, int shared_rows,
-                                                        int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
-                                                        TileInfo* __restrict__ tiles, int32_t* __restrict__ ntiles) {
-    __shared__ int sh[17];
-    const int e = threadIdx.x;
-    const int cnt = e < E ? counts[e] : 0;
+// The tables of one expert (thread e) and, after the routed tiles, those of
+// the shared rows; shared by the scan kernels.
+__device__ __forceinline__ int write_tables(int e, int cnt, int E, int bm, int shared_rows, int32_t* offsets,
+                                            TileInfo* tiles, int32_t* ntiles, int* sh) {
     int total = 0, ttotal = 0;
     const int off = block_exclusive_scan(cnt, &total, sh);
     const int nt = (cnt + bm - 1) / bm;
@@ -142,6 +138,17 @@ __global__ __launch_bounds__(1024) void k_dispatch_scan(int E, int bm, int share
         ntiles[0] = ttotal + nsh;
         ntiles[1] = ttotal;
     }
+    return off;
+}
+
+// One block of 1024 threads; thread e owns expert e (its count from
+// k_dispatch_chunk_scan).
+__global__ __launch_bounds__(1024) void k_dispatch_scan(int E, int bm, int shared_rows,
+                                                        int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                                                        TileInfo* __restrict__ tiles, int32_t* __restrict__ ntiles) {
+    __shared__ int sh[17];
+    const int e = threadIdx.x;
+    write_tables(e, e < E ? counts[e] : 0, E, bm, shared_rows, offsets, tiles, ntiles, sh);
 }
 
 __global__ __launch_bounds__(1024) void k_fill_counts_zero(int32_t* __restrict__ counts, int E) {
@@ -169,6 +176,58 @@ __global__ __launch_bounds__(256) void k_dispatch_scatter(const int32_t* __restr
         const int64_t ce = static_cast<int64_t>(c) * E + e;
         const int p = offsets[e] + chunk_base[ce] + __popcll(masks[ce] & below);
         sorted_token[p] = t;
+        pos[a] = p;
+    }
+}
+
+// The whole dispatch of a small batch in one block: the masks and running
+// bases of all chunks stay in LDS.  The four kernels, whose grids such a batch
+// leaves mostly empty, take 3 to 5 us each.  Layers of few weights, so that the
+// dispatch shows, one block against four launches: 40 against 51 us at 4096
+// assignments, 48 / 52 at 8192 over 48 experts but 95 / 92 over 384, 61 / 52 at
+// 16384: one block up to 4096 (kSmallA).
+__global__ __launch_bounds__(1024) void k_dispatch_small(const int32_t* __restrict__ idx, int T, int E, int e0, int K,
+                                                         int nch, int bm, int shared_rows,
+                                                         int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                                                         int32_t* __restrict__ sorted_token, int32_t* __restrict__ pos,
+                                                         TileInfo* __restrict__ tiles, int32_t* __restrict__ ntiles) {
+    extern __shared__ unsigned long long sm_masks[];  // [nch][E], then the bases [nch][E] int
+    int* const sm_base = reinterpret_cast<int*>(sm_masks + nch * E);
+    __shared__ int sh[17];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int i = tid; i < nch * E; i += 1024) sm_masks[i] = 0ull;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = w; i < nch * K; i += 16) {  // (chunk, slot) pairs, a wave each
+        const int c = i / K, t = c * 64 + lane;
+        if (t >= T) continue;
+        const unsigned e = static_cast<unsigned>(idx[static_cast<int64_t>(t) * K + i % K] - e0);
+        if (e < static_cast<unsigned>(E)) atomicOr(&sm_masks[c * E + e], 1ull << lane);
+    }
+    __syncthreads();
+    int cnt = 0;
+    if (tid < E)
+        for (int c = 0; c < nch; ++c) {
+            sm_base[c * E + tid] = cnt;
+            cnt += __popcll(sm_masks[c * E + tid]);
+        }
+    if (tid < E) counts[tid] = cnt;
+    const int off = write_tables(tid, cnt, E, bm, shared_rows, offsets, tiles, ntiles, sh);
+    if (tid < E)
+        for (int c = 0; c < nch; ++c) sm_base[c * E + tid] += off;
+    __syncthreads();
+    const uint64_t below = (1ull << lane) - 1ull;
+#pragma unroll 4
+    for (int i = w; i < nch * K; i += 16) {
+        const int c = i / K, t = c * 64 + lane;
+        if (t >= T) continue;
+        const int64_t a = static_cast<int64_t>(t) * K + i % K;
+        const int e = idx[a] - e0;
+        int p = -1;  // another slice's expert
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) {
+            p = sm_base[c * E + e] + __popcll(sm_masks[c * E + e] & below);
+            sorted_token[p] = t;
+        }
         pos[a] = p;
     }
 }
@@ -213,13 +272,65 @@ __global__ __launch_bounds__(256) void k_combine(const TY* __restrict__ Y, int64
     }
 }
 
+constexpr int64_t kSmallA = 4096;      // assignments of k_dispatch_small
+constexpr int kSmallLds = 128 * 1024;  // and its LDS (12 bytes per chunk and expert), of the 160 KiB
+
+// The combine of a direct launch: few tokens, so the columns of a token are
+// spread over blocks of one wave and every row a thread needs is asked for
+// before the first is used (one after the other, at one token, took 12 us).
+constexpr int kDirectK = 16;
+__global__ __launch_bounds__(64) void k_combine_direct(const float* __restrict__ Y, int64_t ldy,
+                                                       const float* __restrict__ Ysh, const int32_t* __restrict__ idx,
+                                                       int e0, int E, const float* __restrict__ w, int K, int N,
+                                                       bf16_t* __restrict__ out, int64_t ldo) {
+    const int t = blockIdx.y, c = (blockIdx.x * 64 + threadIdx.x) * 4;
+    if (c >= N) return;
+    float4 v[kDirectK];
+    float wk[kDirectK];
+#pragma unroll
+    for (int k = 0; k < kDirectK; ++k) {
+        const int64_t a = static_cast<int64_t>(t) * K + k;
+        const bool use = k < K && static_cast<unsigned>(idx[k < K ? a : 0] - e0) < static_cast<unsigned>(E);
+        wk[k] = use ? w[a] : 0.f;
+        v[k] = use ? *reinterpret_cast<const float4*>(Y + a * ldy + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float4 s = Ysh ? *reinterpret_cast<const float4*>(Ysh + t * ldy + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kDirectK; ++k) {
+        s.x += wk[k] * v[k].x;
+        s.y += wk[k] * v[k].y;
+        s.z += wk[k] * v[k].z;
+        s.w += wk[k] * v[k].w;
+    }
+    *reinterpret_cast<uint2*>(out + t * ldo + c) =
+        make_uint2(f32_to_bf16(s.x) | (static_cast<uint32_t>(f32_to_bf16(s.y)) << 16),
+                   f32_to_bf16(s.z) | (static_cast<uint32_t>(f32_to_bf16(s.w)) << 16));
+}
+
 }  // namespace
+
+hipError_t launch_combine_direct(const float* Y, int64_t ldy, const float* Yshared, const int32_t* idx, int e0, int E,
+                                 const float* w, int T, int K, int N, uint16_t* out, int64_t ldo, hipStream_t stream) {
+    if (T < 1 || K > kDirectK || N % 4) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_combine_direct, dim3((N / 4 + 63) / 64, T), dim3(64), 0, stream, Y, ldy, Yshared, idx, e0, E,
+                       w, K, N, out, ldo);
+    return hipGetLastError();
+}
 
 hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int bm, int shared_rows, uint64_t* masks,
                            int32_t* chunk_base, int32_t* counts, int32_t* offsets, int32_t* sorted_token, int32_t* pos,
                            TileInfo* tiles, int32_t* ntiles, hipStream_t stream) {
     const int nch = (T + 63) / 64;
     const dim3 g4((nch + 3) / 4);
+    const int64_t lds = static_cast<int64_t>(nch) * E * 12;
+    if (nch > 0 && lds <= kSmallLds && static_cast<int64_t>(T) * K <= kSmallA) {
+        const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_dispatch_small),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
+        if (err != hipSuccess) return err;
+        hipLaunchKernelGGL(k_dispatch_small, dim3(1), dim3(1024), static_cast<size_t>(lds), stream, idx, T, E, e0, K,
+                           nch, bm, shared_rows, counts, offsets, sorted_token, pos, tiles, ntiles);
+        return hipGetLastError();
+    }
     if (nch > 0) {
         hipLaunchKernelGGL(k_dispatch_masks, g4, dim3(256), 0, stream, idx, T, E, e0, K, nch, masks);
         hipError_t err = hipGetLastError();

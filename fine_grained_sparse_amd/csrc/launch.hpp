@@ -127,14 +127,29 @@ hipError_t launch_pack_frag16_fp8(const uint8_t* src, uint8_t* dst, int64_t coun
                                   hipStream_t stream);
 
 // The projections with 4-bit routed experts (fp4.hip): C = epi(A * B^T) over
-// a tile table of fp4_bm() rows per tile, bf16 A; C bf16 for the SwiGLU,
+// a tile table of bm rows per tile (fp4_bm), bf16 A; C bf16 for the SwiGLU,
 // fp32 for the plain store.  Group 0: E2M1 codes (b_estride in bytes) with
 // E8M0 scales bs / bsu per 32 columns (s_estride in bytes), both in 16 x 128
 // blocks; group 1: packed bf16.  One K segment each.
-int fp4_bm();
-hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int max_tiles, int max_n, hipStream_t stream);
-// whether the grid of that launch stays within 31 bits
-bool fp4_grid_fits(int64_t max_tiles, int64_t max_n);
+hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, int max_tiles, int max_n, hipStream_t stream);
+// rows per tile for this many routed rows over E experts
+int fp4_bm(int64_t rows, int E, bool shared);
+// The same without a tile table, for batches that fp4_direct() takes: rows of
+// C are assignments a = t K + k (group 1: tokens), whose experts the kernel
+// finds in idx (ids outside e0 .. e0 + E - 1: their rows are not written).
+bool fp4_direct(int64_t T);
+hipError_t launch_fp4_direct(const GemmArgs& args, Epi epi, const int32_t* idx, int T, int K, int e0, int E,
+                             hipStream_t stream);
+// The down projection (group 0: H rows by assignment, group 1: the shared
+// experts) and the combine in one launch, for the batches of fp4_fused():
+// out[t] = shared + sum_k w[t,k] W_down[idx[t,k] - e0] H[t K + k].
+bool fp4_fused(int64_t T);
+hipError_t launch_fp4_down_combine(const GemmArgs& args, const int32_t* idx, const float* w, int T, int K, int e0, int E,
+                                   uint16_t* out, int64_t ldo, hipStream_t stream);
+
+// C = A B^T for a few rows: bf16 A and C, packed bf16 B, one or two K segments
+// (group 0, no tile table).
+hipError_t launch_dense_rows16(const GemmArgs& args, hipStream_t stream);
 
 // Row-major E2M1 codes [rows, cols / 2] and scales [rows, cols / 32] (count
 // matrices each, consecutive) -> 16 x 128 blocks: lane l of a block holds the
@@ -195,10 +210,14 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int 
                            hipStream_t stream);
 
 // out[t] = (Yshared ? Yshared[t] : 0) + sum_k w[t,k] * Y[pos[t,k]], over
-// the slots with pos >= 0; y_f32: Y and Yshared in fp32 under a bf16 out
+// the slots with pos >= 0; y_f32: Y and Yshared in fp32 under a bf16 out.
+// launch_combine_direct: pos[t,k] = t K + k where idx[t,k] is one of e0 ..
+// e0 + E - 1, -1 elsewhere.
 hipError_t launch_combine(DType dt, bool y_f32, const void* Y, int64_t ldy,
                           const void* Yshared, const int32_t* pos,
                           const float* w, int T, int K, int N, void* out,
                           int64_t ldo, hipStream_t stream);
+hipError_t launch_combine_direct(const float* Y, int64_t ldy, const float* Yshared, const int32_t* idx, int e0, int E,
+                                 const float* w, int T, int K, int N, uint16_t* out, int64_t ldo, hipStream_t stream);
 
 }  // namespace moe
