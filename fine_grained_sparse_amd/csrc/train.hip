@@ -6,7 +6,11 @@
 // that traffic.  A wave owns a token: lane l holds experts 128 j + 2 l and
 // + 1, so a row is read in 512-byte pieces and its sums are one butterfly.
 #include "common.hpp"
+#include "launch.hpp"
 #include "train.hpp"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -31,23 +35,46 @@ __device__ __forceinline__ Sigm sigm(float z) {
     return o;
 }
 
+// Sums over the 16 lanes of a row, and over the wave, in every lane: lane
+// moves inside the adds (partners at distance 1, 2, then the mirrored half
+// and row, whose sums are complete by then) and two half-wave swaps, where
+// shuffles through LDS took six round trips.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+    return v + __uint_as_float(static_cast<uint32_t>(
+                   __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+    v = add_dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = add_dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = add_dpp<0x141>(v);  // row_half_mirror
+    return add_dpp<0x140>(v);  // row_mirror
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-    return v;
+    v = row16_sum(v);
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Two neighbours of a row, which may start at any 4-byte address (odd E).
+// A lane's two neighbours e, e + 1 of a row of E, which may start at any
+// 4-byte address (odd E).  FULL: both exist in every lane; otherwise the pair
+// is read where it fits and what lies past the row is 0.
 typedef float f32x2_any __attribute__((ext_vector_type(2), aligned(4)));
+template <bool FULL>
 __device__ __forceinline__ float2 load2(const float* p, int e, int E) {
-    if (e + 1 < E) {
+    if (FULL) {
         const f32x2_any v = *reinterpret_cast<const f32x2_any*>(p + e);
         return make_float2(v[0], v[1]);
     }
-    return make_float2(e < E ? p[e] : 0.f, 0.f);
+    if (E < 2) return make_float2(e == 0 ? p[0] : 0.f, 0.f);  // (uniform)
+    const f32x2_any v = *reinterpret_cast<const f32x2_any*>(p + min(e, E - 2));
+    return make_float2(e <= E - 2 ? v[0] : e == E - 1 ? v[1] : 0.f, e <= E - 2 ? v[1] : 0.f);
 }
+template <bool FULL>
 __device__ __forceinline__ void store2(float* p, int e, int E, float a, float b) {
-    if (e + 1 < E) {
+    if (FULL || e + 1 < E) {
         f32x2_any v;
         v[0] = a;
         v[1] = b;
@@ -56,12 +83,33 @@ __device__ __forceinline__ void store2(float* p, int e, int E, float a, float b)
         p[e] = a;
     }
 }
+// A lane's 2 J2 experts of a row: 128 j + 2 lane and + 1; E lies in the last
+// of the J2 pieces, so only that one looks at its end.
+template <int J2>
+__device__ __forceinline__ void load_row(const float* p, int lane, int E, float (&o)[2 * J2]) {
+#pragma unroll
+    for (int j = 0; j < J2; ++j) {
+        const int e = j * 128 + lane * 2;
+        const float2 v = j + 1 < J2 ? load2<true>(p, e, E) : load2<false>(p, e, E);
+        o[2 * j] = v.x;
+        o[2 * j + 1] = v.y;
+    }
+}
+template <int J2>
+__device__ __forceinline__ bool in_row(int j, int lane, int E) {  // element j of the lane lies in the row
+    return (j >> 1) + 1 < J2 || (j >> 1) * 128 + lane * 2 + (j & 1) < E;
+}
 
 __device__ __forceinline__ int seq_lo(const SeqArgs& a, int q) { return a.off ? min(max(a.off[q], 0), a.T) : 0; }
 __device__ __forceinline__ int seq_hi(const SeqArgs& a, int q) { return a.off ? min(max(a.off[q + 1], 0), a.T) : a.T; }
 
 // The first sequence that ends after token t (S if none does).
 __device__ __forceinline__ int seq_of(const SeqArgs& a, int t) {
+    if (!a.off) return 0;
+    if (a.S <= 64) {  // one look at all of them
+        const int l = threadIdx.x & 63;
+        return __popcll(__ballot(l < a.S && seq_hi(a, l < a.S ? l : 0) <= t));
+    }
     int lo = 0, hi = a.S;
     while (lo < hi) {
         const int m = (lo + hi) >> 1;
@@ -75,64 +123,76 @@ __device__ __forceinline__ int seq_of(const SeqArgs& a, int t) {
 
 constexpr int kMaxE = 1024;
 
-// One block per chunk of C tokens (C <= 64).  For every sequence q that the
-// chunk c meets, the sums of p and the counts over their common tokens go to
-// partial row c + q: along the ascending sequences c + q grows with every
-// (chunk, sequence) pair that meets, so the rows are distinct and at most
-// chunks + S.  The balance over blocks does not depend on the sequences.
+// One block per chunk of 64 tokens.  For every sequence q that the chunk c
+// meets, the sums of p and the counts over their common tokens go to partial
+// row c + q: along the ascending sequences c + q grows with every (chunk,
+// sequence) pair that meets, so the rows are distinct and at most chunks + S,
+// and the blocks' work does not depend on the sequences.  A wave takes four
+// tokens at a time, so that their rows are in flight together.
+constexpr int kChunk = 64;
+constexpr int toks(int j2) { return j2 <= 4 ? 4 : 2; }  // tokens in hand (more experts: fewer, for the registers' sake)
 template <int J2>
-__global__ __launch_bounds__(256) void k_balance_partial(const SeqArgs a, int C, const float* __restrict__ z,
+__global__ __launch_bounds__(512) void k_balance_partial(const SeqArgs a, const float* __restrict__ z,
                                                          const int32_t* __restrict__ idx, float* __restrict__ part_p,
                                                          int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
                                                          int32_t* __restrict__ ticket) {
-    __shared__ float sp[4][kMaxE];
+    constexpr int NW = 8, kTok = toks(J2);
+    __shared__ float sp[NW][J2 * 128];
     __shared__ int hist[kMaxE];
-    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    const int c = blockIdx.x, c0 = c * C, c1 = min(a.T, c0 + C);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = blockIdx.x, c0 = c * kChunk, c1 = min(a.T, c0 + kChunk);
     if (c == 0 && tid == 0) *ticket = 0;  // for k_balance_final
     for (int q = seq_of(a, c0); q < a.S && seq_lo(a, q) < c1; ++q) {
         const int lo = max(seq_lo(a, q), c0), hi = min(seq_hi(a, q), c1);
         if (lo >= hi) continue;
         const int64_t slot = c + q;
-        for (int e = tid; e < a.E; e += 256) hist[e] = 0;
+        for (int e = tid; e < a.E; e += 64 * NW) hist[e] = 0;
         float acc[2 * J2];
 #pragma unroll
         for (int j = 0; j < 2 * J2; ++j) acc[j] = 0.f;
-        for (int t = lo + wid; t < hi; t += 4) {
-            if (a.mask && !a.mask[t]) continue;
-            const float* row = z + static_cast<int64_t>(t) * a.E;
-            float s[2 * J2], sum = 0.f;
+        for (int t = lo + wid * kTok; t < hi; t += NW * kTok) {
+            float v[kTok][2 * J2], sum[kTok];
+            bool live[kTok];
 #pragma unroll
-            for (int j = 0; j < J2; ++j) {
-                const int e = j * 128 + lane * 2;
-                const float2 v = load2(row, e, a.E);
-                s[2 * j] = e < a.E ? sigm(v.x).s : 0.f;
-                s[2 * j + 1] = e + 1 < a.E ? sigm(v.y).s : 0.f;
-                sum += s[2 * j] + s[2 * j + 1];
+            for (int u = 0; u < kTok; ++u) {
+                const int tu = min(t + u, hi - 1);
+                live[u] = t + u < hi && (!a.mask || a.mask[tu]);
+                load_row<J2>(z + static_cast<int64_t>(tu) * a.E, lane, a.E, v[u]);
             }
-            const float inv = 1.f / (wave_sum(sum) + 1e-20f);
 #pragma unroll
-            for (int j = 0; j < 2 * J2; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
+            for (int u = 0; u < kTok; ++u) {
+                sum[u] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2 * J2; ++j) {
+                    v[u][j] = in_row<J2>(j, lane, a.E) ? sigm(v[u][j]).s : 0.f;
+                    sum[u] += v[u][j];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kTok; ++u) {
+                const float inv = live[u] ? 1.f / (wave_sum(sum[u]) + 1e-20f) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 2 * J2; ++j) acc[j] = fmaf(v[u][j], inv, acc[j]);
+            }
         }
         __syncthreads();
-        const int64_t i1 = static_cast<int64_t>(hi) * a.K;
-        for (int64_t i = static_cast<int64_t>(lo) * a.K + tid; i < i1; i += 256) {
-            const unsigned e = static_cast<unsigned>(idx[i]);
-            if (e < static_cast<unsigned>(a.E) && (!a.mask || a.mask[i / a.K])) atomicAdd(&hist[e], 1);
+        for (int i = tid; i < (hi - lo) * a.K; i += 64 * NW) {
+            const unsigned e = static_cast<unsigned>(idx[static_cast<int64_t>(lo) * a.K + i]);
+            if (e < static_cast<unsigned>(a.E) && (!a.mask || a.mask[lo + i / a.K])) atomicAdd(&hist[e], 1);
         }
 #pragma unroll
-        for (int j = 0; j < J2; ++j) {
-            sp[wid][j * 128 + lane * 2] = acc[2 * j];
-            sp[wid][j * 128 + lane * 2 + 1] = acc[2 * j + 1];
-        }
+        for (int j = 0; j < J2; ++j)
+            *reinterpret_cast<float2*>(&sp[wid][j * 128 + lane * 2]) = make_float2(acc[2 * j], acc[2 * j + 1]);
         if (wid == 0) {
             const int t = lo + lane;
             const uint64_t live = __ballot(t < hi && (!a.mask || a.mask[t < hi ? t : lo]));
             if (lane == 0) part_n[slot] = __popcll(live);
         }
         __syncthreads();
-        for (int e = tid; e < a.E; e += 256) {
-            part_p[slot * a.E + e] = (sp[0][e] + sp[1][e]) + (sp[2][e] + sp[3][e]);
+        for (int e = tid; e < a.E; e += 64 * NW) {
+            part_p[slot * a.E + e] = ((sp[0][e] + sp[1][e]) + (sp[2][e] + sp[3][e])) +
+                                     ((sp[4][e] + sp[5][e]) + (sp[6][e] + sp[7][e]));
             part_c[slot * a.E + e] = hist[e];
         }
         __syncthreads();
@@ -143,7 +203,7 @@ __global__ __launch_bounds__(256) void k_balance_partial(const SeqArgs a, int C,
 // rows in turn, their sums meet in LDS in wave order; the counts go out, and
 // the block's share of the loss goes to part_l.  The last block to finish
 // adds the shares up in a fixed order.
-__global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, int C, const float* __restrict__ part_p,
+__global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const float* __restrict__ part_p,
                                                         const int32_t* __restrict__ part_c,
                                                         const int32_t* __restrict__ part_n, float alpha,
                                                         float* part_l, int32_t* ticket, float* __restrict__ loss,
@@ -157,9 +217,9 @@ __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, int C, 
     float p = 0.f;
     int cnt = 0, n = 0;
     if (lo < hi) {
-        const int cl = (hi - 1) / C;
-#pragma unroll 4
-        for (int c = lo / C + wid; c <= cl; c += 16) {
+        const int cl = (hi - 1) / kChunk;
+#pragma unroll 8
+        for (int c = lo / kChunk + wid; c <= cl; c += 16) {
             const int64_t slot = c + q;
             if (e < a.E) {
                 p += part_p[slot * a.E + e];
@@ -206,160 +266,502 @@ __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, int C, 
     }
 }
 
-// A wave per token, kTW consecutive tokens per wave.  The gate term touches
-// only the K chosen experts: lane k < K computes its own and adds it to a
-// row in LDS (zero between tokens), from which the owning lanes take it.
-constexpr int kTW = 4;
-template <int J2>
+// Where k_gate_backward leaves dz as the two products' operands instead.
+struct PlaneArgs {
+    float *rows32, *cols32;  // (small products) dz as [T][Es] and as [Es][Ts], zero past E and T
+    int32_t Es, Ts;          // E and T in whole 16s
+    bf16_t* rows;   // [T][3 Ep]: hi | lo | hi of a token's row, zero past E
+    bf16_t* cols;   // [Tb][3][Eb] blocks of 16 experts x 32 tokens of its parts hi, mid, lo (hi + mid + lo == dz):
+                    // element (r, c) of a block at ((c / 8) 16 + r) 8 + c % 8, zero past E and T.  (What a slab of
+                    // tokens reads lies together: blocks a power of two apart, as with the tokens fastest, met in
+                    // the same memory channels and k_dw took 548 us for XXX at 16384 tokens.)
+    uint16_t* live; // [32 Tb]: 0xffff for the tokens that count, else 0
+    int32_t Ep, Eb, Tb;
+};
+
+enum GateOut { GATE_ROWS = 0, GATE_SMALL = 1, GATE_PLANES = 2 };
+
+// A wave takes a few consecutive tokens.  The gate term touches only the K
+// chosen experts of each: lane 16 u + k computes token u's slot k, and the
+// values reach the lanes that own the experts through a row in LDS that is
+// zero between tokens.
+template <int J2, int OUT>
 __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const float* __restrict__ z,
                                                        const int32_t* __restrict__ idx, const float* __restrict__ dw,
                                                        float scale, const int32_t* __restrict__ counts, float alpha,
-                                                       const float* __restrict__ d_loss, float* __restrict__ dz) {
-    __shared__ float rows[4][kMaxE];
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+                                                       const float* __restrict__ d_loss, float* __restrict__ dz,
+                                                       const PlaneArgs pl) {
+    constexpr int kTok = toks(J2);
+    __shared__ float rows[4][J2 * 128];
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float* row = rows[wid];
-    for (int e = lane; e < kMaxE; e += 64) row[e] = 0.f;
-    __syncthreads();
-    const int t0 = (blockIdx.x * 4 + wid) * kTW, t1 = min(a.T, t0 + kTW);
-    if (t0 >= t1) return;
-    float co[2 * J2];  // a_q of this lane's experts, for the sequence in hand
-    int q = -1, qlo = 0, qhi = 0;
-    for (int t = t0; t < t1; ++t) {
-        float* out = dz + static_cast<int64_t>(t) * a.E;
-        if (a.mask && !a.mask[t]) {
+    const int t0 = (blockIdx.x * 4 + wid) * kTok;
+    if (OUT == GATE_ROWS && t0 >= a.T) return;
+
+    bool live[kTok];
 #pragma unroll
-            for (int j = 0; j < J2; ++j) store2(out, j * 128 + lane * 2, a.E, 0.f, 0.f);
-            continue;
+    for (int u = 0; u < kTok; ++u) live[u] = t0 + u < a.T && (!a.mask || a.mask[min(t0 + u, a.T - 1)]);
+
+    // the gate term, in lane 16 u + k
+    float gv = 0.f;
+    int ge = -1;
+    if (dw) {
+        for (int e = lane; e < J2 * 128; e += 64) row[e] = 0.f;
+        const int u = lane >> 4, k = lane & 15, t = min(t0 + u, a.T - 1);
+        bool use = false;
+#pragma unroll
+        for (int v = 0; v < kTok; ++v) use = use || (u == v && live[v]);
+        use = use && k < a.K;
+        const int64_t i = static_cast<int64_t>(t) * a.K + (k < a.K ? k : 0);
+        const int e = idx[i];
+        const bool ok = use && static_cast<unsigned>(e) < static_cast<unsigned>(a.E);
+        const Sigm s = sigm(ok ? z[static_cast<int64_t>(t) * a.E + e] : 0.f);
+        const float g = ok ? dw[i] : 0.f, sc = ok ? s.s : 0.f;
+        const float den = row16_sum(sc) + 1e-20f;
+        const float mean = row16_sum(g * sc) / den;
+        gv = scale / den * (g - mean) * (s.s * s.c);
+        ge = ok ? e : -1;
+    }
+
+    float d[kTok][2 * J2];
+#pragma unroll
+    for (int u = 0; u < kTok; ++u)
+#pragma unroll
+        for (int j = 0; j < 2 * J2; ++j) d[u][j] = 0.f;
+    if (counts && t0 < a.T) {
+        float s[kTok][2 * J2], inv[kTok];
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) load_row<J2>(z + static_cast<int64_t>(min(t0 + u, a.T - 1)) * a.E, lane, a.E, s[u]);
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) {
+                const Sigm g = sigm(s[u][j]);
+                s[u][j] = in_row<J2>(j, lane, a.E) ? g.s : 0.f;
+                d[u][j] = s[u][j] * g.c;  // s (1 - s)
+                sum += s[u][j];
+            }
+            inv[u] = 1.f / (wave_sum(sum) + 1e-20f);
         }
-        const float* zr = z + static_cast<int64_t>(t) * a.E;
-        float d[2 * J2];
-        bool member = false;
-        if (counts) {
-            if (q < 0 || t >= qhi) {
-                q = seq_of(a, t);
-                qlo = q < a.S ? seq_lo(a, q) : a.T;
-                qhi = q < a.S ? seq_hi(a, q) : a.T;
-                if (q < a.S) {
-                    const int32_t* cr = counts + static_cast<int64_t>(q) * a.E;
-                    float total = 0.f;
+        bool done[kTok];
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) done[u] = false;
+        for (int q = seq_of(a, t0); q < a.S && seq_lo(a, q) < min(t0 + kTok, a.T); ++q) {
+            const int qlo = seq_lo(a, q), qhi = seq_hi(a, q);
+            if (qlo >= qhi) continue;
+            const int32_t* cr = counts + static_cast<int64_t>(q) * a.E;
+            float co[2 * J2], total = 0.f;  // a_q of this lane's experts
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) {
+                co[j] = in_row<J2>(j, lane, a.E) ? static_cast<float>(cr[(j >> 1) * 128 + lane * 2 + (j & 1)]) : 0.f;
+                total += co[j];
+            }
+            // K n_q is the sum of the counts
+            const float n = wave_sum(total) / static_cast<float>(a.K);
+            const float g = alpha * (d_loss ? *d_loss : 1.f) / static_cast<float>(a.S);
+            const float f = n > 0.f ? g * (static_cast<float>(a.E) / (static_cast<float>(a.K) * n) / n) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) co[j] *= f;
+#pragma unroll
+            for (int u = 0; u < kTok; ++u) {
+                if (t0 + u < qlo || t0 + u >= qhi || done[u]) continue;  // (uniform)
+                done[u] = true;
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2 * J2; ++j) dot = fmaf(co[j], s[u][j], dot);
+                const float mean = wave_sum(dot) * inv[u];
+#pragma unroll
+                for (int j = 0; j < 2 * J2; ++j) d[u][j] *= (co[j] - mean) * inv[u];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kTok; ++u)
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) d[u][j] = done[u] && live[u] ? d[u][j] : 0.f;
+    }
+    if (dw) {
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+            const bool mine = ge >= 0 && (lane >> 4) == u;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (mine) atomicAdd(&row[ge], gv);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int j = 0; j < J2; ++j) {
+                const float2 v = *reinterpret_cast<const float2*>(&row[j * 128 + lane * 2]);
+                d[u][2 * j] += v.x;
+                d[u][2 * j + 1] += v.y;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (mine) row[ge] = 0.f;
+        }
+    }
+    if constexpr (OUT == GATE_ROWS) {
+#pragma unroll
+        for (int u = 0; u < kTok; ++u)
+            if (t0 + u < a.T) {
+                float* o = dz + static_cast<int64_t>(t0 + u) * a.E;
+#pragma unroll
+                for (int j = 0; j < J2; ++j) {
+                    if (j + 1 < J2)
+                        store2<true>(o, j * 128 + lane * 2, a.E, d[u][2 * j], d[u][2 * j + 1]);
+                    else
+                        store2<false>(o, j * 128 + lane * 2, a.E, d[u][2 * j], d[u][2 * j + 1]);
+                }
+            }
+    } else if constexpr (OUT == GATE_SMALL) {
+        if (t0 >= pl.Ts) return;
+#pragma unroll
+        for (int j = 0; j < 2 * J2; ++j) {
+            const int e = (j >> 1) * 128 + lane * 2 + (j & 1);
+            if (e >= pl.Es) continue;
+#pragma unroll
+            for (int u = 0; u < kTok; ++u) {
+                if (t0 + u < a.T) pl.rows32[static_cast<int64_t>(t0 + u) * pl.Es + e] = d[u][j];
+                pl.cols32[static_cast<int64_t>(e) * pl.Ts + t0 + u] = d[u][j];
+            }
+        }
+    } else {
+        bf16_t hi[kTok][2 * J2], mid[kTok][2 * J2], lo[kTok][2 * J2];
+#pragma unroll
+        for (int u = 0; u < kTok; ++u)
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) {
+                hi[u][j] = f32_to_bf16(d[u][j]);
+                const float r = d[u][j] - bf16_to_f32(hi[u][j]);
+                mid[u][j] = f32_to_bf16(r);
+                lo[u][j] = f32_to_bf16(r - bf16_to_f32(mid[u][j]));
+            }
+        auto pair = [](bf16_t x, bf16_t y) { return x | (static_cast<uint32_t>(y) << 16); };
+        if (pl.rows) {
+#pragma unroll
+            for (int u = 0; u < kTok; ++u)
+                if (t0 + u < a.T) {
+                    uint32_t* o = reinterpret_cast<uint32_t*>(pl.rows + static_cast<int64_t>(t0 + u) * 3 * pl.Ep);
 #pragma unroll
                     for (int j = 0; j < J2; ++j) {
                         const int e = j * 128 + lane * 2;
-                        co[2 * j] = e < a.E ? static_cast<float>(cr[e]) : 0.f;
-                        co[2 * j + 1] = e + 1 < a.E ? static_cast<float>(cr[e + 1]) : 0.f;
-                        total += co[2 * j] + co[2 * j + 1];
+                        if (e >= pl.Ep) continue;
+                        const uint32_t h = pair(hi[u][2 * j], hi[u][2 * j + 1]);
+                        o[e / 2] = h;
+                        o[(pl.Ep + e) / 2] = pair(mid[u][2 * j], mid[u][2 * j + 1]);
+                        o[(2 * pl.Ep + e) / 2] = h;
                     }
-                    // K n_q is the sum of the counts
-                    const float n = wave_sum(total) / static_cast<float>(a.K);
-                    const float g = alpha * (d_loss ? *d_loss : 1.f) / static_cast<float>(a.S);
-                    const float f = n > 0.f ? g * (static_cast<float>(a.E) / (static_cast<float>(a.K) * n) / n) : 0.f;
+                }
+        }
+        if (pl.cols && t0 < pl.Tb * 32) {
+            if (lane < kTok) {
+                bool l = false;
 #pragma unroll
-                    for (int j = 0; j < 2 * J2; ++j) co[j] *= f;
+                for (int u = 0; u < kTok; ++u) l = l || (lane == u && live[u]);
+                pl.live[t0 + lane] = l ? 0xffffu : 0u;
+            }
+            const int64_t plane = static_cast<int64_t>(pl.Eb) * 512;
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) {
+                const int e = (j >> 1) * 128 + lane * 2 + (j & 1);
+                if (e >= pl.Eb * 16) continue;
+                bf16_t* o = pl.cols + (static_cast<int64_t>(t0 / 32) * 3 * pl.Eb + e / 16) * 512 + ((t0 % 32) / 8 * 16 + e % 16) * 8 + t0 % 8;
+                if constexpr (kTok == 4) {
+                    *reinterpret_cast<uint2*>(o) = make_uint2(pair(hi[0][j], hi[1][j]), pair(hi[2][j], hi[3][j]));
+                    *reinterpret_cast<uint2*>(o + plane) = make_uint2(pair(mid[0][j], mid[1][j]), pair(mid[2][j], mid[3][j]));
+                    *reinterpret_cast<uint2*>(o + 2 * plane) = make_uint2(pair(lo[0][j], lo[1][j]), pair(lo[2][j], lo[3][j]));
+                } else {
+                    *reinterpret_cast<uint32_t*>(o) = pair(hi[0][j], hi[1][j]);
+                    *reinterpret_cast<uint32_t*>(o + plane) = pair(mid[0][j], mid[1][j]);
+                    *reinterpret_cast<uint32_t*>(o + 2 * plane) = pair(lo[0][j], lo[1][j]);
                 }
             }
-            member = q < a.S && t >= qlo;
         }
-        if (member) {
-            float s[2 * J2], sum = 0.f, dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < J2; ++j) {
-                const int e = j * 128 + lane * 2;
-                const float2 v = load2(zr, e, a.E);
-                const Sigm s0 = sigm(v.x), s1 = sigm(v.y);
-                s[2 * j] = s0.s * s0.c;
-                s[2 * j + 1] = s1.s * s1.c;
-                const float x0 = e < a.E ? s0.s : 0.f, x1 = e + 1 < a.E ? s1.s : 0.f;
-                sum += x0 + x1;
-                dot = fmaf(co[2 * j], x0, fmaf(co[2 * j + 1], x1, dot));
-            }
-            const float inv = 1.f / (wave_sum(sum) + 1e-20f);
-            const float mean = wave_sum(dot) * inv;
-#pragma unroll
-            for (int j = 0; j < 2 * J2; ++j) d[j] = (co[j] - mean) * inv * s[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2 * J2; ++j) d[j] = 0.f;
-        }
-        if (dw) {
-            const bool use = lane < a.K;
-            const int64_t i = static_cast<int64_t>(t) * a.K + (use ? lane : 0);
-            const int e = idx[i];
-            const bool ok = use && static_cast<unsigned>(e) < static_cast<unsigned>(a.E);
-            const Sigm s = sigm(ok ? zr[e] : 0.f);
-            const float g = ok ? dw[i] : 0.f, sc = ok ? s.s : 0.f;
-            const float den = wave_sum(sc) + 1e-20f;
-            const float mean = wave_sum(g * sc) / den;
-            if (ok) atomicAdd(&row[e], scale / den * (g - mean) * (s.s * s.c));
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-            for (int j = 0; j < J2; ++j) {
-                d[2 * j] += row[j * 128 + lane * 2];
-                d[2 * j + 1] += row[j * 128 + lane * 2 + 1];
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (ok) row[e] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < J2; ++j) store2(out, j * 128 + lane * 2, a.E, d[2 * j], d[2 * j + 1]);
     }
 }
 
-__global__ __launch_bounds__(256) void k_split_rows(const float* __restrict__ src, int64_t R, int C, int Cp,
-                                                    bf16_t* __restrict__ dst) {
-    const int64_t n = R * Cp;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = i / Cp;
-        const int c = static_cast<int>(i % Cp);
-        const float v = c < C ? src[r * C + c] : 0.f;
-        const bf16_t h = f32_to_bf16(v), l = f32_to_bf16(v - bf16_to_f32(h));
-        bf16_t* o = dst + r * 3 * Cp + c;
-        o[0] = h;
-        o[Cp] = l;
-        o[2 * Cp] = h;
-    }
-}
-
-// 64 x 64 tiles through LDS.
-template <int KIND>
-__global__ __launch_bounds__(256) void k_transpose(const void* __restrict__ src, int64_t R, int64_t C, int64_t Rp,
-                                                   void* __restrict__ dst) {
-    __shared__ float tile[64][65];
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
+// W_r [E, d] -> the packed right operand of dx: W_r^T as [d, 3 Ep] in the
+// fragment-block layout of 16 x 32, its rows [hi | hi | lo].  A wave reads 64
+// columns of eight rows and writes their 16-byte pieces.
+__global__ __launch_bounds__(256) void k_pack_wt(const float* __restrict__ W, int E, int64_t d, int Ep,
+                                                 bf16_t* __restrict__ dst) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    for (int i = w; i < 64; i += 4) {
-        const int64_t r = r0 + i, c = c0 + lane;
-        float v = 0.f;
-        if (r < R && c < C)
-            v = KIND == TR_BF16 ? bf16_to_f32(static_cast<const bf16_t*>(src)[r * C + c])
-                                : static_cast<const float*>(src)[r * C + c];
-        tile[i][lane] = v;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + lane;  // (d is a multiple of 64)
+    const int e0 = blockIdx.y * 32 + w * 8, kb = 3 * Ep / 32;
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bf16_t hh[2], ll[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int e = e0 + 2 * i + b;
+            const float v = e < E ? W[e * d + n] : 0.f;
+            hh[b] = f32_to_bf16(v);
+            ll[b] = f32_to_bf16(v - bf16_to_f32(hh[b]));
+        }
+        h[i] = hh[0] | (static_cast<uint32_t>(hh[1]) << 16);
+        l[i] = ll[0] | (static_cast<uint32_t>(ll[1]) << 16);
     }
-    __syncthreads();
-    for (int i = w; i < 64; i += 4) {
-        const int64_t c = c0 + i, r = r0 + lane;
-        if (c >= C || r >= Rp) continue;
-        const float v = tile[lane][i];
-        if (KIND == TR_F32) {
-            static_cast<float*>(dst)[c * Rp + r] = v;
-            continue;
-        }
-        bf16_t* o = static_cast<bf16_t*>(dst);
-        const bf16_t h = f32_to_bf16(v);
-        if (KIND == TR_BF16) {
-            o[c * Rp + r] = h;
-            continue;
-        }
-        const float r1 = v - bf16_to_f32(h);
-        const bf16_t m = f32_to_bf16(r1);
-        if (KIND == TR_PLANES3) {
-            o[c * Rp + r] = h;
-            o[(C + c) * Rp + r] = m;
-            o[(2 * C + c) * Rp + r] = f32_to_bf16(r1 - bf16_to_f32(m));
+    const uint4 hv = make_uint4(h[0], h[1], h[2], h[3]), lv = make_uint4(l[0], l[1], l[2], l[3]);
+    bf16_t* o = dst + ((n / 16) * kb + blockIdx.y) * 512 + (w * 16 + n % 16) * 8;
+    stg16(o, hv);
+    stg16(o + Ep / 32 * 512, hv);
+    stg16(o + 2 * (Ep / 32) * 512, lv);
+}
+
+// dW_r = dz^T x, split over the tokens: job (split, M tile, N tile) adds up
+// (32 MB experts) x (256 columns) over its tokens into its plane of `part`;
+// the four waves hold (16 MB) x 128 each.  dz comes in three bf16 parts that
+// carry all its bits (each product with the bf16 x is then exact in the fp32
+// accumulator), so a tile of M x N moves 3 M + N values per token, least with
+// N the longer side.  Both operands of an MFMA want eight consecutive tokens
+// per lane: k_gate_backward writes dz that way, in whole fragments of 1 KiB; x
+// is row-major and is read transposed from LDS (ds_read_b64_tr_b16: a group of
+// 16 lanes reads 4 rows x 16 columns, lane i receives column i).  32-byte
+// chunk c of slab row r of x sits at c ^ f(r), f = r % 4 + 4 (r / 8 % 2), so the
+// rows that lanes 0 - 31 read lie in different banks.
+//
+// With 192 accumulators a SIMD has one wave, so nothing but the order of its
+// own instructions hides a latency.  Slabs of 32 tokens come straight into a
+// ring of three LDS buffers (DMA: staging them in registers left the compiler
+// too few, and it copied the accumulators once a slab).  In the middle of slab
+// b every wave waits for its own loads of b + 1, which have had a slab's time,
+// and meets the others: after that b + 1 may be read, and b - 1, which nobody
+// reads any more, makes room for b + 2.  The first fragments of b + 1 are read
+// under the last products of b.  XXX
+// x of a token that does not count may hold anything: its fragments are
+// masked by `live` after the read.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+struct DwArgs {
+    const bf16_t* cols;    // PlaneArgs::cols, ::live
+    const uint16_t* live;
+    const bf16_t* x;
+    float* part;
+    int64_t d;
+    int32_t T, E, Eb, Tb, ntn, mt, nsplit;
+};
+// 16 (4) bytes per lane from base + off (src) to LDS at lds + 16 (4) lane.
+// Nothing waits for these but wait_loads(), and no register is their target.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int MB>
+__global__ __launch_bounds__(256, 1) void k_dw(const DwArgs a) {
+    constexpr int NA = 6 * MB, LA = (NA + 3) / 4;           // 1 KiB blocks of dz per slab, and per wave
+    constexpr int XO = NA * 1024, LO = XO + 16384, BUF = LO + 256;  // x, live (64 bytes, four times)
+    __shared__ __attribute__((aligned(1024))) char lds[3 * BUF];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wid >> 1, wn = wid & 1;
+    // split-major job order, a contiguous stretch of it per XCD: the blocks of
+    // an XCD share the parts of dz they stream
+    const int jobs = a.ntn * a.mt * a.nsplit;
+    const int job = xcd_slot_pair(static_cast<int>(blockIdx.x), jobs, jobs);
+    if (job < 0) return;
+    const int sp = job / (a.ntn * a.mt), mt = job % a.mt;
+    const int64_t n0 = static_cast<int64_t>(job / a.mt % a.ntn) * 256;
+    const int per = (a.Tb + a.nsplit - 1) / a.nsplit;
+    const int b0 = min(a.Tb, sp * per), b1 = min(a.Tb, b0 + per);
+    const int eb0 = mt * 2 * MB;  // this tile's first block of 16 experts
+
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(lds)));
+    auto fl = [](int r) { return (r & 3) | ((r >> 1) & 4); };
+    // x: block q of a slab is its rows 2 q and 2 q + 1; lane l fills position
+    // l % 32 of row 2 q + l / 32
+    const int xrow = lane >> 5;
+    // Slab b to buffer `buf`: wave w moves blocks w, w + 4, .. of dz (block q:
+    // part q / (2 MB), experts 16 (q % (2 MB)) ..) and of x.  Past the last slab
+    // the last one is read again; past the ends of dz's blocks, of x's rows
+    // and of its columns likewise (nothing of it is stored, or its dz is 0).
+    constexpr int NL = LA + 5;  // loads per wave and slab
+    auto load = [&](int b, int buf, int k) {  // the k-th of them
+        const int bc = min(b, a.Tb - 1);
+        const uint32_t dst = lds0 + buf * BUF;
+        if (k < LA) {
+            const int q = min(wid + 4 * k, NA - 1);
+            const int64_t blk = static_cast<int64_t>(bc) * 3 * a.Eb + q / (2 * MB) * a.Eb + min(eb0 + q % (2 * MB), a.Eb - 1);
+            dma16(a.cols + blk * 512, lane * 16, dst + q * 1024);
+        } else if (k < LA + 4) {
+            const int q = wid + 4 * (k - LA), r = 2 * q + xrow;
+            const int c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);  // logical 16-byte chunk
+            const int64_t row = min(bc * 32 + r, a.T - 1), col = min(n0 + c * 8, a.d - 8);
+            dma16(a.x + row * a.d + col, dst + XO + q * 1024);
         } else {
-            o[c * 3 * Rp + r] = h;
-            o[c * 3 * Rp + Rp + r] = h;
-            o[c * 3 * Rp + 2 * Rp + r] = m;
+            dma4(a.live + bc * 32, (lane & 15) * 4, dst + LO);
         }
+    };
+    auto load_all = [&](int b, int buf) {
+#pragma unroll
+        for (int k = 0; k < NL; ++k) load(b, buf, k);
+    };
+    auto read_a = [&](int buf, int p, uint4 (&f)[MB]) {
+        const char* o = lds + buf * BUF + (p * 2 * MB + wm * MB) * 1024 + lane * 16;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) f[i] = *reinterpret_cast<const uint4*>(o + i * 1024);
+    };
+    auto read_live = [&](int buf) { return *reinterpret_cast<const uint4*>(lds + buf * BUF + LO + grp * 16); };
+    // rows 8 grp + r16 / 4 and + 4 of columns 16 j ..: 8 bytes per lane
+    auto read_x = [&](int buf, int j) {
+        uint2 h[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * grp + (r16 >> 2) + 4 * i;
+            const char* q = lds + buf * BUF + XO + r * 512 + (((wn * 8 + j) ^ fl(r)) << 5) + (r16 & 3) * 8;
+            h[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                 (__attribute__((address_space(3))) s16x4*)(q)));
+        }
+        return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+    };
+
+    f32x4 acc[MB][8];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (b0 < b1) {
+        load_all(b0, 0);
+        wait_loads();
+        __syncthreads();
+        load_all(b0 + 1, 1);
+        uint4 f[3][MB], xf[2], lm;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) read_a(0, p, f[p]);
+        xf[0] = read_x(0, 0);
+        lm = read_live(0);
+        int buf = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int next = buf == 2 ? 0 : buf + 1, third = buf == 0 ? 2 : buf - 1;
+            uint4 ln = lm;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j == 4) {
+                    wait_loads();
+                    __syncthreads();
+                }
+                xf[(j + 1) & 1] = j < 7 ? read_x(buf, j + 1) : read_x(next, 0);
+                if (j == 7) ln = read_live(next);
+                __builtin_amdgcn_sched_barrier(0);
+                const uint4 x = make_uint4(xf[j & 1].x & lm.x, xf[j & 1].y & lm.y, xf[j & 1].z & lm.z, xf[j & 1].w & lm.w);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) acc[i][j] = Mfma<bf16_t>::run(x, f[p][i], acc[i][j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (j == 7) read_a(next, p, f[p]);
+                    // the loads of b + 2 a few at a time: issued together they hold up the MFMAs behind them
+                    if (j >= 4)
+#pragma unroll
+                        for (int k = 0; k < NL; ++k)
+                            if (k * 12 / NL == (j - 4) * 3 + p) load(b + 2, third, k);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            lm = ln;
+            buf = next;
+        }
+        wait_loads();  // no load may reach the LDS after the block has left it
+    }
+    // acc[i][j] of a lane: expert 16 i + lane % 16, columns 16 j + 4 (lane / 16) .. + 3
+    float* out = a.part + sp * a.E * a.d;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int e = (eb0 + wm * MB + i) * 16 + r16;
+        if (e >= a.E) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t n = n0 + (wn * 8 + j) * 16 + grp * 4;
+            if (n < a.d)
+                *reinterpret_cast<float4*>(out + e * a.d + n) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        }
+    }
+}
+
+// Both products of a small router in one launch, on the vector ALUs: fp32
+// FMAs.  Blocks of 16 rows (tokens for dx, experts for dW_r) x 64 columns, a
+// column per lane; the four waves split the sum, and each step of it takes one
+// line of x or W_r and 16 neighbours of dz (of its rows for dW_r, of its
+// transpose for dx), the same for the whole wave.
+template <typename TX>
+__device__ __forceinline__ void small_rows(const float* __restrict__ A, int64_t lda, int n, const TX* __restrict__ B,
+                                           int64_t d, const uint8_t* mask, int wid, float (&acc)[16]) {
+    const int k0 = static_cast<int>(static_cast<int64_t>(n) * wid / 4), k1 = static_cast<int>(static_cast<int64_t>(n) * (wid + 1) / 4);
+#pragma unroll 4
+    for (int k = k0; k < k1; ++k) {
+        float b = Elem<TX>::to_f32(B[k * d]);
+        if (mask && !mask[k]) b = 0.f;
+        const float* p = A + k * lda;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = fmaf(p[i], b, acc[i]);
+    }
+}
+template <typename TX>
+__global__ __launch_bounds__(256) void k_small_products(const float* __restrict__ rows, const float* __restrict__ cols,
+                                                        int Es, int Ts, const TX* __restrict__ x,
+                                                        const float* __restrict__ W, const uint8_t* __restrict__ mask,
+                                                        int T, int E, int64_t d, int xblocks, TX* __restrict__ dx,
+                                                        float* __restrict__ dW) {
+    __shared__ float red[4][16][64];
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t ntn = d / 64;
+    const bool isx = static_cast<int>(blockIdx.x) < xblocks;
+    const int64_t b = isx ? blockIdx.x : blockIdx.x - xblocks;
+    const int64_t col = (b % ntn) * 64 + lane;
+    const int r0 = static_cast<int>(b / ntn) * 16;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    if (isx)
+        small_rows<float>(cols + r0, Ts, E, W + col, d, nullptr, wid, acc);
+    else
+        small_rows<TX>(rows + r0, Es, T, x + col, d, mask, wid, acc);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) red[wid][i][lane] = acc[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = wid * 4 + i;
+        const float v = (red[0][r][lane] + red[1][r][lane]) + (red[2][r][lane] + red[3][r][lane]);
+        if (isx) {
+            if (r0 + r < T) dx[(r0 + r) * d + col] = Elem<TX>::from_f32(v);
+        } else {
+            if (r0 + r < E) dW[(r0 + r) * d + col] = v;
+        }
+    }
+}
+
+// [R, C] fp32 -> [C, Rp], columns R .. Rp - 1 zero, and those of rows that do
+// not count (mask); 64 x 64 tiles through LDS.
+__global__ __launch_bounds__(256) void k_transpose(const float* __restrict__ src, int64_t R, int64_t C, int64_t Rp,
+                                                   const uint8_t* __restrict__ mask, float* __restrict__ dst) {
+    __shared__ float tile[64][65];
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * 64; c0 < C; c0 += static_cast<int64_t>(gridDim.y) * 64) {
+        for (int i = w; i < 64; i += 4) {
+            const int64_t r = r0 + i, c = c0 + lane;
+            tile[i][lane] = r < R && c < C && (!mask || mask[r]) ? src[r * C + c] : 0.f;
+        }
+        __syncthreads();
+        for (int i = w; i < 64; i += 4) {
+            const int64_t c = c0 + i, r = r0 + lane;
+            if (c < C && r < Rp) dst[c * Rp + r] = tile[lane][i];
+        }
+        __syncthreads();
+    }
+}
+// [R, C] fp32 -> [R, Cp], columns C .. Cp - 1 zero.
+__global__ __launch_bounds__(256) void k_pad_rows(const float* __restrict__ src, int64_t n, int C, int Cp,
+                                                  float* __restrict__ dst) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int c = static_cast<int>(i % Cp);
+        dst[i] = c < C ? src[i / Cp * C + c] : 0.f;
     }
 }
 
@@ -385,75 +787,172 @@ unsigned grid_of(int64_t threads, int64_t most) {
 
 }  // namespace
 
-int balance_chunk(int T) { return T >= 32768 ? 64 : 32; }
-int64_t balance_slots(int T, int S) { return (static_cast<int64_t>(T) + balance_chunk(T) - 1) / balance_chunk(T) + S; }
+int dw_slabs(int T) { return static_cast<int>((static_cast<int64_t>(T) + 31) / 32); }
 
-// The kernels hold 2 J2 experts per lane: the smallest that reaches E.
-#define MOE_FOR_E(E, CALL)   \
-    do {                     \
-        if ((E) <= 128)      \
-            CALL(1);         \
-        else if ((E) <= 256) \
-            CALL(2);         \
-        else if ((E) <= 384) \
-            CALL(3);         \
-        else if ((E) <= 512) \
-            CALL(4);         \
-        else if ((E) <= 896) \
-            CALL(7);         \
-        else                 \
-            CALL(8);         \
-    } while (0)
+int64_t balance_slots(int T, int S) { return (static_cast<int64_t>(T) + kChunk - 1) / kChunk + S; }
+
+// The kernels hold 2 J2 experts per lane, J2 = ceil(E / 128).
+#define MOE_FOR_E(E, CALL)             \
+    switch (((E) + 127) / 128) {       \
+        case 1: CALL(1); break;        \
+        case 2: CALL(2); break;        \
+        case 3: CALL(3); break;        \
+        case 4: CALL(4); break;        \
+        case 5: CALL(5); break;        \
+        case 6: CALL(6); break;        \
+        case 7: CALL(7); break;        \
+        case 8: CALL(8); break;        \
+        default: return hipErrorInvalidValue; \
+    }
 
 hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* idx, float alpha, float* part_p,
                                int32_t* part_c, int32_t* part_n, float* part_l, int32_t* ticket, float* loss,
                                int32_t* seq_counts, hipStream_t stream) {
     if (a.T < 1 || a.E < 1 || a.E > kMaxE || a.S < 1 || a.S > 65535) return hipErrorInvalidValue;
-    const int C = balance_chunk(a.T);
-    const dim3 grid((a.T + C - 1) / C);
-#define MOE_CALL(J2)                                                                                             \
-    hipLaunchKernelGGL(k_balance_partial<J2>, grid, dim3(256), 0, stream, a, C, z, idx, part_p, part_c, part_n, \
-                       ticket)
+    const dim3 grid((a.T + kChunk - 1) / kChunk);
+#define MOE_CALL(J2) \
+    hipLaunchKernelGGL(k_balance_partial<J2>, grid, dim3(512), 0, stream, a, z, idx, part_p, part_c, part_n, ticket)
     MOE_FOR_E(a.E, MOE_CALL);
 #undef MOE_CALL
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(k_balance_final, dim3((a.E + 63) / 64, a.S), dim3(1024), 0, stream, a, C, part_p, part_c,
+    hipLaunchKernelGGL(k_balance_final, dim3((a.E + 63) / 64, a.S), dim3(1024), 0, stream, a, part_p, part_c,
                        part_n, alpha, part_l, ticket, loss, seq_counts);
+    return hipGetLastError();
+}
+
+template <int OUT>
+static hipError_t launch_gate(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
+                              const int32_t* counts, float alpha, const float* d_loss, float* dz, const PlaneArgs& pl,
+                              int64_t tokens, hipStream_t stream) {
+    if (a.T < 1 || a.E < 1 || a.E > kMaxE || a.K > 16) return hipErrorInvalidValue;
+    const int per = 4 * toks((a.E + 127) / 128);
+    const dim3 grid(static_cast<unsigned>((tokens + per - 1) / per));
+#define MOE_CALL(J2)                                                                                                  \
+    hipLaunchKernelGGL((k_gate_backward<J2, OUT>), grid, dim3(256), 0, stream, a, z, idx, dw, scale, counts, alpha, \
+                       d_loss, dz, pl)
+    MOE_FOR_E(a.E, MOE_CALL);
+#undef MOE_CALL
     return hipGetLastError();
 }
 
 hipError_t launch_gate_backward(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
                                 const int32_t* counts, float alpha, const float* d_loss, float* dz,
                                 hipStream_t stream) {
-    if (a.T < 1 || a.E < 1 || a.E > kMaxE) return hipErrorInvalidValue;
-    const dim3 grid((a.T + 4 * kTW - 1) / (4 * kTW));
-#define MOE_CALL(J2)                                                                                               \
-    hipLaunchKernelGGL(k_gate_backward<J2>, grid, dim3(256), 0, stream, a, z, idx, dw, scale, counts, alpha, d_loss, \
-                       dz)
-    MOE_FOR_E(a.E, MOE_CALL);
-#undef MOE_CALL
+    return launch_gate<GATE_ROWS>(a, z, idx, dw, scale, counts, alpha, d_loss, dz, PlaneArgs{}, a.T, stream);
+}
+
+hipError_t launch_gate_backward_small(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
+                                      const int32_t* counts, float alpha, const float* d_loss, float* rows, float* cols,
+                                      hipStream_t stream) {
+    PlaneArgs pl{};
+    pl.rows32 = rows;
+    pl.cols32 = cols;
+    pl.Es = (a.E + 15) / 16 * 16;
+    pl.Ts = (a.T + 15) / 16 * 16;
+    return launch_gate<GATE_SMALL>(a, z, idx, dw, scale, counts, alpha, d_loss, nullptr, pl, pl.Ts, stream);
+}
+
+hipError_t launch_gate_backward_planes(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
+                                       const int32_t* counts, float alpha, const float* d_loss, uint16_t* rows, int Ep,
+                                       uint16_t* cols, uint16_t* live, hipStream_t stream) {
+    if (Ep % 64 || Ep < a.E || Ep >= a.E + 64) return hipErrorInvalidValue;
+    PlaneArgs pl{};
+    pl.rows = rows;
+    pl.cols = cols;
+    pl.live = live;
+    pl.Ep = Ep;
+    pl.Eb = (a.E + 15) / 16;
+    pl.Tb = dw_slabs(a.T);
+    return launch_gate<GATE_PLANES>(a, z, idx, dw, scale, counts, alpha, d_loss, nullptr, pl,
+                                    static_cast<int64_t>(pl.Tb) * 32, stream);
+}
+
+hipError_t launch_pack_wt(const float* W, int E, int64_t d, int Ep, uint16_t* dst, hipStream_t stream) {
+    if (d % 64 || Ep % 64) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_pack_wt, dim3(static_cast<unsigned>(d / 64), Ep / 32), dim3(256), 0, stream, W, E, d, Ep, dst);
     return hipGetLastError();
 }
 
-hipError_t launch_split_rows(const float* src, int64_t R, int C, int Cp, uint16_t* dst, hipStream_t stream) {
-    if (R <= 0) return hipSuccess;
-    hipLaunchKernelGGL(k_split_rows, dim3(grid_of(R * Cp, 8192)), dim3(256), 0, stream, src, R, C, Cp, dst);
-    return hipGetLastError();
-}
-
-hipError_t launch_transpose(TransposeKind kind, const void* src, int64_t R, int64_t C, int64_t Rp, void* dst,
-                            hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((Rp + 63) / 64), static_cast<unsigned>((C + 63) / 64));
-    if (grid.y > 65535u || Rp >= (int64_t{1} << 31)) return hipErrorInvalidValue;
-#define MOE_CALL(K) hipLaunchKernelGGL(k_transpose<K>, grid, dim3(256), 0, stream, src, R, C, Rp, dst)
-    switch (kind) {
-        case TR_F32: MOE_CALL(TR_F32); break;
-        case TR_BF16: MOE_CALL(TR_BF16); break;
-        case TR_PLANES3: MOE_CALL(TR_PLANES3); break;
-        case TR_HHL: MOE_CALL(TR_HHL); break;
+DwPlan dw_plan(int T, int E, int64_t d) {
+    DwPlan p{};
+    // M tiles of 32 MB experts, MB <= 6 (192 of a lane's registers are then
+    // accumulators, at one wave per SIMD)
+    const int rb = (E + 31) / 32;
+    p.mt = (rb + 5) / 6;
+    p.mb = (rb + p.mt - 1) / p.mt;
+    p.ntn = static_cast<int>((d + 255) / 256);
+    // one block per CU at a time: the fewest splits that fill 85% of the 256
+    // CUs over whole rounds (each split costs a pass over [E, d] more), or the
+    // fullest of the 16
+    const int64_t jobs = static_cast<int64_t>(p.mt) * p.ntn;
+    const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, (T + 31) / 32 / 4)));
+    double best = 0;
+    for (int n = 1; n <= most; ++n) {
+        const int64_t b = jobs * n, rounds = (b + 255) / 256;
+        const double full = static_cast<double>(b) / static_cast<double>(rounds * 256);
+        if (full > best) {
+            best = full;
+            p.nsplit = n;
+        }
+        if (full >= 0.85) break;
     }
+    return p;
+}
+
+hipError_t launch_dw(const DwPlan& p, const uint16_t* cols, const uint16_t* live, const void* x, int T, int E, int64_t d,
+                     float* part, hipStream_t stream) {
+    if (T < 1 || E < 1 || d < 64 || d % 8) return hipErrorInvalidValue;
+    const DwArgs a{cols, live, static_cast<const bf16_t*>(x), part, d, T, E, (E + 15) / 16, dw_slabs(T), p.ntn, p.mt,
+                   p.nsplit};
+    const int64_t jobs = static_cast<int64_t>(p.ntn) * p.mt * p.nsplit;
+    if (jobs >= (int64_t{1} << 30)) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>((jobs + 7) / 8 * 8 + 16));
+    switch (p.mb) {
+#define MOE_CALL(MB)                                                        \
+    case MB:                                                                \
+        hipLaunchKernelGGL(k_dw<MB>, grid, dim3(256), 0, stream, a); \
+        break
+        MOE_CALL(1);
+        MOE_CALL(2);
+        MOE_CALL(3);
+        MOE_CALL(4);
+        MOE_CALL(5);
+        MOE_CALL(6);
 #undef MOE_CALL
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_small_products(bool bf16, const float* rows, const float* cols, const void* x, const float* W,
+                                 const uint8_t* mask, int T, int E, int64_t d, void* dx, float* dW, hipStream_t stream) {
+    if (T < 1 || E < 1 || d % 64) return hipErrorInvalidValue;
+    const int64_t ntn = d / 64, xb = dx ? (static_cast<int64_t>(T) + 15) / 16 * ntn : 0, wb = dW ? (E + 15) / 16 * ntn : 0;
+    if (xb + wb < 1 || xb + wb >= (int64_t{1} << 31)) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(xb + wb));
+    const int Es = (E + 15) / 16 * 16, Ts = (T + 15) / 16 * 16;
+    if (bf16)
+        hipLaunchKernelGGL(k_small_products<bf16_t>, grid, dim3(256), 0, stream, rows, cols, Es, Ts,
+                           static_cast<const bf16_t*>(x), W, mask, T, E, d, static_cast<int>(xb),
+                           static_cast<bf16_t*>(dx), dW);
+    else
+        hipLaunchKernelGGL(k_small_products<float>, grid, dim3(256), 0, stream, rows, cols, Es, Ts,
+                           static_cast<const float*>(x), W, mask, T, E, d, static_cast<int>(xb),
+                           static_cast<float*>(dx), dW);
+    return hipGetLastError();
+}
+
+hipError_t launch_transpose(const float* src, int64_t R, int64_t C, int64_t Rp, const uint8_t* mask, float* dst,
+                            hipStream_t stream) {
+    if (Rp >= (int64_t{1} << 31) * 64) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>((Rp + 63) / 64), static_cast<unsigned>(std::min<int64_t>((C + 63) / 64, 65535)));
+    hipLaunchKernelGGL(k_transpose, grid, dim3(256), 0, stream, src, R, C, Rp, mask, dst);
+    return hipGetLastError();
+}
+
+hipError_t launch_pad_rows(const float* src, int64_t R, int C, int Cp, float* dst, hipStream_t stream) {
+    hipLaunchKernelGGL(k_pad_rows, dim3(grid_of(R * Cp, 8192)), dim3(256), 0, stream, src, R * Cp, C, Cp, dst);
     return hipGetLastError();
 }
 

@@ -26,7 +26,6 @@ struct SeqArgs {
 // Balance loss.  part_p / part_c / part_n hold balance_slots(T, S) partial
 // rows of E (p sums, counts, tokens); part_l one float per (sequence, 64
 // experts); ticket one int.
-int balance_chunk(int T);
 int64_t balance_slots(int T, int S);
 hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* idx, float alpha, float* part_p,
                                int32_t* part_c, int32_t* part_n, float* part_l, int32_t* ticket, float* loss,
@@ -37,15 +36,42 @@ hipError_t launch_gate_backward(const SeqArgs& a, const float* z, const int32_t*
                                 const int32_t* counts, float alpha, const float* d_loss, float* dz,
                                 hipStream_t stream);
 
-// [R, C] fp32 -> bf16 parts, row-major, columns C .. Cp - 1 zero: the row
-// [hi | lo | hi] of 3 Cp columns (hi = rne(v), lo = rne(v - hi)).
-hipError_t launch_split_rows(const float* src, int64_t R, int C, int Cp, uint16_t* dst, hipStream_t stream);
-// [R, C] -> [C, Rp], columns R .. Rp - 1 zero.  fp32 -> fp32; bf16 -> bf16;
-// fp32 -> three bf16 planes [C, Rp] with hi + mid + lo == v; fp32 -> rows
-// [hi | hi | lo] of 3 Rp columns.
-enum TransposeKind { TR_F32 = 0, TR_BF16 = 1, TR_PLANES3 = 2, TR_HHL = 3 };
-hipError_t launch_transpose(TransposeKind kind, const void* src, int64_t R, int64_t C, int64_t Rp, void* dst,
+// The same gradient for launch_small_products: rows [T, Es] and cols [Es, Ts]
+// (E and T up to whole 16s), zero past E and T.
+hipError_t launch_gate_backward_small(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
+                                      const int32_t* counts, float alpha, const float* d_loss, float* rows, float* cols,
+                                      hipStream_t stream);
+// The same gradient as operands of the two products (bf16 activations):
+// rows (nullable) [T, 3 Ep] = [hi | lo | hi], zero past E (Ep = E up to 64s);
+// cols (nullable): its parts hi, mid, lo with hi + mid + lo == dz in
+// [dw_slabs(T)][3][ceil(E/16)] blocks of 1 KiB (16 experts x 32 tokens, element
+// (r, c) at ((c / 8) 16 + r) 8 + c % 8), zero past E and T; with it live
+// [32 dw_slabs(T)]: 0xffff for the tokens that count, else 0.
+int dw_slabs(int T);
+hipError_t launch_gate_backward_planes(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
+                                       const int32_t* counts, float alpha, const float* d_loss, uint16_t* rows, int Ep,
+                                       uint16_t* cols, uint16_t* live, hipStream_t stream);
+
+// W_r [E, d] -> W_r^T [d, 3 Ep] = [hi | hi | lo] in the fragment-block layout.
+hipError_t launch_pack_wt(const float* W, int E, int64_t d, int Ep, uint16_t* dst, hipStream_t stream);
+
+// dW_r from cols and bf16 x: nsplit planes [E, d] whose sum it is.
+struct DwPlan {
+    int mb, mt, ntn, nsplit;
+};
+DwPlan dw_plan(int T, int E, int64_t d);
+hipError_t launch_dw(const DwPlan& p, const uint16_t* cols, const uint16_t* live, const void* x, int T, int E, int64_t d,
+                     float* part, hipStream_t stream);
+
+// Both products (dx, dW_r; either nullable) in fp32 on the vector ALUs.
+hipError_t launch_small_products(bool bf16, const float* rows, const float* cols, const void* x, const float* W,
+                                 const uint8_t* mask, int T, int E, int64_t d, void* dx, float* dW, hipStream_t stream);
+
+// [R, C] -> [C, Rp], columns R .. Rp - 1 and those of rows with a zero mask
+// byte zero; [R, C] -> [R, Cp], columns C .. Cp - 1 zero.
+hipError_t launch_transpose(const float* src, int64_t R, int64_t C, int64_t Rp, const uint8_t* mask, float* dst,
                             hipStream_t stream);
+hipError_t launch_pad_rows(const float* src, int64_t R, int C, int Cp, float* dst, hipStream_t stream);
 // out[i] = sum over the n planes of part[i], in plane order.
 hipError_t launch_sum_planes(const float* part, int n, int64_t stride, int64_t count, float* out, hipStream_t stream);
 

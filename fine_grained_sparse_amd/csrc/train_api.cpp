@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "../../include/moe_train.h"
 #include "launch.hpp"
@@ -15,6 +16,8 @@ using namespace moe;
 namespace {
 
 constexpr int64_t kAlign = 256;
+// T E d up to which both products run as one launch on the vector ALUs.
+const int64_t kSmallProducts = getenv("SMALLP") ? atoll(getenv("SMALLP")) : 16000000;
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -74,31 +77,46 @@ BalancePlan balance_plan(const moe_layer_desc* D, int S) {
 }
 
 struct BackPlan {
-    bool bf16;
+    bool bf16, small;
     int64_t Ep, Tp;  // E and T in whole 64-column K steps
-    TileCfg xcfg, wcfg;
-    int nsplit;
-    int64_t o_dz, o_a, o_wt, o_dzt, o_xt, o_part, total;
+    TileCfg xcfg;
+    DwPlan dw;       // bf16
+    int nsplit;      // planes of dW_r
+    int64_t o_dz, o_rows, o_wt, o_cols, o_live, o_xt, o_part, total;
 };
 BackPlan back_plan(const moe_layer_desc* D) {
     BackPlan p{};
     p.bf16 = D->act_dtype == MOE_BF16;
-    const int64_t T = D->T, E = D->E, d = D->d, es = p.bf16 ? 2 : 4;
+    const int64_t T = D->T, E = D->E, d = D->d;
+    p.small = T * E * d <= kSmallProducts;
     p.Ep = up(E, 64);
     p.Tp = up(T, 64);
-    p.xcfg = p.bf16 && T > 64 ? TILE_LARGE : TILE_SMALL;
-    p.wcfg = p.bf16 && E > 64 ? TILE_LARGE : TILE_SMALL;
-    // dW_r has few output tiles and a long K (the tokens): split K until
-    // about 512 workgroups are in flight, at least 8 K steps each
-    const int64_t wgs = cdiv(E, tile_bm(p.wcfg)) * cdiv(d, 256), ksteps = (p.bf16 ? 3 : 1) * p.Tp / 32;
-    p.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({16, cdiv(512, wgs), ksteps / 8})));
     Arena ar;
-    p.o_dz = ar.take(T * E * 4);
-    p.o_a = ar.take(p.bf16 ? T * 3 * p.Ep * 2 : T * p.Ep * 4);
-    p.o_wt = ar.take(p.bf16 ? d * 3 * p.Ep * 2 : d * p.Ep * 4);
-    p.o_dzt = ar.take(p.bf16 ? 3 * E * p.Tp * 2 : E * p.Tp * 4);
-    p.o_xt = ar.take(d * p.Tp * es);
-    p.o_part = ar.take(p.nsplit > 1 ? p.nsplit * E * d * 4 : 1);
+    if (p.small) {
+        p.o_rows = ar.take(T * up(E, 16) * 4);
+        p.o_cols = ar.take(up(E, 16) * up(T, 16) * 4);
+    } else if (p.bf16) {
+        p.xcfg = T > 64 ? TILE_WIDE : TILE_SMALL;
+        p.dw = dw_plan(D->T, D->E, d);
+        p.nsplit = p.dw.nsplit;
+        p.o_rows = ar.take(T * 3 * p.Ep * 2);
+        p.o_wt = ar.take(d * 3 * p.Ep * 2);
+        p.o_cols = ar.take(3 * cdiv(E, 16) * dw_slabs(D->T) * 1024);
+        p.o_live = ar.take(static_cast<int64_t>(dw_slabs(D->T)) * 64);
+        p.o_part = ar.take(p.nsplit > 1 ? p.nsplit * E * d * 4 : 1);
+    } else {
+        p.xcfg = TILE_SMALL;
+        // dW_r has few output tiles and a long K (the tokens): split K until
+        // about 512 workgroups are in flight, at least 8 K steps each
+        const int64_t wgs = cdiv(E, tile_bm(TILE_SMALL)) * cdiv(d, 256);
+        p.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({16, cdiv(512, wgs), p.Tp / 32 / 8})));
+        p.o_dz = ar.take(T * E * 4);
+        p.o_rows = ar.take(T * p.Ep * 4);
+        p.o_wt = ar.take(d * p.Ep * 4);
+        p.o_cols = ar.take(E * p.Tp * 4);
+        p.o_xt = ar.take(d * p.Tp * 4);
+        p.o_part = ar.take(p.nsplit > 1 ? p.nsplit * E * d * 4 : 1);
+    }
     p.total = ar.off;
     return p;
 }
@@ -211,46 +229,56 @@ moe_status moe_router_backward(const moe_layer_desc* desc, const void* x, const 
     if (!aligned16(x) || !aligned16(W_r) || !aligned16(workspace)) return MOE_ERR_ALIGN;
     const BackPlan p = back_plan(desc);
     if (workspace_bytes < static_cast<size_t>(p.total)) return MOE_ERR_WORKSPACE;
-    float* dz = at<float>(workspace, p.o_dz);
-    MOE_HIP(launch_gate_backward(seq_args(desc, balance), logits, topk_idx, d_topk_w, desc->scale, seq_counts,
-                                 balance ? balance->alpha : 0.f, d_loss, dz, s));
-    const DType dt = p.bf16 ? DT_BF16 : DT_F32;
-    if (dx) {
-        void* a = at<char>(workspace, p.o_a);
-        void* wt = at<char>(workspace, p.o_wt);
-        int64_t K = p.Ep;
-        if (p.bf16) {
-            MOE_HIP(launch_split_rows(dz, T, desc->E, static_cast<int>(p.Ep), static_cast<uint16_t*>(a), s));
-            MOE_HIP(launch_transpose(TR_HHL, W_r, E, d, p.Ep, wt, s));
-            K = 3 * p.Ep;
-        } else {  // (zero columns up to Ep: two transposes)
-            float* t = at<float>(workspace, p.o_dzt);
-            MOE_HIP(launch_transpose(TR_F32, dz, T, E, T, t, s));
-            MOE_HIP(launch_transpose(TR_F32, t, E, T, p.Ep, a, s));
-            MOE_HIP(launch_transpose(TR_F32, W_r, E, d, p.Ep, wt, s));
+    const SeqArgs sa = seq_args(desc, balance);
+    const uint8_t* mask = sa.mask;
+    const float alpha = balance ? balance->alpha : 0.f;
+    float* part = p.nsplit > 1 ? at<float>(workspace, p.o_part) : dW_r;  // (the small products need none)
+    if (p.bf16 && !p.small) {
+        uint16_t* rows = dx ? at<uint16_t>(workspace, p.o_rows) : nullptr;
+        uint16_t* cols = dW_r ? at<uint16_t>(workspace, p.o_cols) : nullptr;
+        const int Ep = static_cast<int>(p.Ep);
+        MOE_HIP(launch_gate_backward_planes(sa, logits, topk_idx, d_topk_w, desc->scale, seq_counts, alpha, d_loss, rows,
+                                            Ep, cols, at<uint16_t>(workspace, p.o_live), s));
+        if (dx) {
+            uint16_t* wt = at<uint16_t>(workspace, p.o_wt);
+            MOE_HIP(launch_pack_wt(W_r, desc->E, d, Ep, wt, s));
+            const GemmArgs g = dense(rows, 3 * p.Ep, wt, 3 * p.Ep, 3 * p.Ep, dx, d, desc->T, desc->d);
+            MOE_HIP(launch_gemm(g, DT_BF16, false, EPI_STORE, p.xcfg, static_cast<int>(cdiv(T, tile_bm(p.xcfg))),
+                                desc->d, true, s));
         }
-        const GemmArgs g = dense(a, K, wt, K, K, dx, d, desc->T, desc->d);
-        MOE_HIP(launch_gemm(g, dt, false, EPI_STORE, p.xcfg, static_cast<int>(cdiv(T, tile_bm(p.xcfg))), desc->d, false,
-                            s));
-    }
-    if (dW_r) {
-        char* dzt = at<char>(workspace, p.o_dzt);
-        char* xt = at<char>(workspace, p.o_xt);
-        MOE_HIP(launch_transpose(p.bf16 ? TR_PLANES3 : TR_F32, dz, T, E, p.Tp, dzt, s));
-        MOE_HIP(launch_transpose(p.bf16 ? TR_BF16 : TR_F32, x, T, d, p.Tp, xt, s));
-        float* c = p.nsplit > 1 ? at<float>(workspace, p.o_part) : dW_r;
-        GemmArgs g = dense(dzt, p.Tp, xt, p.Tp, p.Tp, c, d, desc->E, desc->d);
-        if (p.bf16) {
-            g.g[0].nseg = 3;
-            for (int i = 1; i < 3; ++i)
-                g.g[0].seg[i] = GemmSeg{dzt + i * E * p.Tp * 2, xt, nullptr, p.Tp, p.Tp, static_cast<int32_t>(p.Tp), 0};
+        if (dW_r) MOE_HIP(launch_dw(p.dw, cols, at<uint16_t>(workspace, p.o_live), x, desc->T, desc->E, d, part, s));
+    } else if (p.small) {
+        float* rows = at<float>(workspace, p.o_rows);
+        float* cols = at<float>(workspace, p.o_cols);
+        MOE_HIP(launch_gate_backward_small(sa, logits, topk_idx, d_topk_w, desc->scale, seq_counts, alpha, d_loss, rows,
+                                           cols, s));
+        MOE_HIP(launch_small_products(p.bf16, rows, cols, x, W_r, mask, desc->T, desc->E, d, dx, dW_r, s));
+        return MOE_OK;
+    } else {
+        float* dz = at<float>(workspace, p.o_dz);
+        MOE_HIP(launch_gate_backward(sa, logits, topk_idx, d_topk_w, desc->scale, seq_counts, alpha, d_loss, dz, s));
+        if (dx) {
+            float* rows = at<float>(workspace, p.o_rows);
+            float* wt = at<float>(workspace, p.o_wt);
+            MOE_HIP(launch_pad_rows(dz, T, desc->E, static_cast<int>(p.Ep), rows, s));
+            MOE_HIP(launch_transpose(W_r, E, d, p.Ep, nullptr, wt, s));
+            const GemmArgs g = dense(rows, p.Ep, wt, p.Ep, p.Ep, dx, d, desc->T, desc->d);
+            MOE_HIP(launch_gemm(g, DT_F32, false, EPI_STORE, p.xcfg, static_cast<int>(cdiv(T, tile_bm(p.xcfg))),
+                                desc->d, false, s));
         }
-        g.nsplit = p.nsplit;
-        g.split_stride = E * d;
-        MOE_HIP(launch_gemm(g, dt, p.bf16, EPI_STORE, p.wcfg, static_cast<int>(cdiv(E, tile_bm(p.wcfg))), desc->d,
-                            false, s));
-        if (p.nsplit > 1) MOE_HIP(launch_sum_planes(c, p.nsplit, E * d, E * d, dW_r, s));
+        if (dW_r) {
+            float* dzt = at<float>(workspace, p.o_cols);
+            float* xt = at<float>(workspace, p.o_xt);
+            MOE_HIP(launch_transpose(dz, T, E, p.Tp, nullptr, dzt, s));
+            MOE_HIP(launch_transpose(static_cast<const float*>(x), T, d, p.Tp, mask, xt, s));
+            GemmArgs g = dense(dzt, p.Tp, xt, p.Tp, p.Tp, part, d, desc->E, desc->d);
+            g.nsplit = p.nsplit;
+            g.split_stride = E * d;
+            MOE_HIP(launch_gemm(g, DT_F32, false, EPI_STORE, TILE_SMALL, static_cast<int>(cdiv(E, tile_bm(TILE_SMALL))),
+                                desc->d, false, s));
+        }
     }
+    if (dW_r && p.nsplit > 1) MOE_HIP(launch_sum_planes(part, p.nsplit, E * d, E * d, dW_r, s));
     return MOE_OK;
 }
 
