@@ -112,15 +112,18 @@ def workspace_size(layer_desc: LayerDesc, forward: bool) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return _current_raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _need(t, name, dtype=None, shape=None, device=None):
+    # the usual case in one expression: a dozen of these run before every launch
+    if (type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous() and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device.type != "cuda":
@@ -135,6 +138,15 @@ def _need(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _current_raw_stream(index):
+    """The handle of the device's current stream."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same without building a Stream object
+    _current_raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
+
+
 class Workspace:
     """Growable device byte buffers (allocated by torch, owned here), one per
     (device, stream).  A buffer is allocated while its stream is current, so
@@ -147,6 +159,10 @@ class Workspace:
         self._buf = {}
 
     def get(self, device, nbytes, stream=None):
+        if stream is None and device.index is not None:
+            buf = self._buf.get((device, _current_raw_stream(device.index)))
+            if buf is not None and buf.numel() >= nbytes:
+                return buf
         s = torch.cuda.current_stream(device) if stream is None else stream
         key = (device, s.cuda_stream)
         buf = self._buf.get(key)

@@ -684,13 +684,16 @@ __global__ __launch_bounds__(256, 1) void k_dw(const DwArgs a) {
 
 // Both products of a small router in one launch, on the vector ALUs: fp32
 // FMAs.  Blocks of 16 rows (tokens for dx, experts for dW_r) x 64 columns, a
-// column per lane; the four waves split the sum, and each step of it takes one
-// line of x or W_r and 16 neighbours of dz (of its rows for dW_r, of its
-// transpose for dx), the same for the whole wave.
+// column per lane; the 16 waves split the sum (its steps wait for memory, so
+// few of them in a row), and each step of it takes one line of x or W_r and 16
+// neighbours of dz (of its rows for dW_r, of its transpose for dx), the same
+// for the whole wave.
+constexpr int kSmallNW = 16;
 template <typename TX>
 __device__ __forceinline__ void small_rows(const float* __restrict__ A, int64_t lda, int n, const TX* __restrict__ B,
                                            int64_t d, const uint8_t* mask, int wid, float (&acc)[16]) {
-    const int k0 = static_cast<int>(static_cast<int64_t>(n) * wid / 4), k1 = static_cast<int>(static_cast<int64_t>(n) * (wid + 1) / 4);
+    const int k0 = static_cast<int>(static_cast<int64_t>(n) * wid / kSmallNW);
+    const int k1 = static_cast<int>(static_cast<int64_t>(n) * (wid + 1) / kSmallNW);
 #pragma unroll 4
     for (int k = k0; k < k1; ++k) {
         float b = Elem<TX>::to_f32(B[k * d]);
@@ -701,12 +704,12 @@ __device__ __forceinline__ void small_rows(const float* __restrict__ A, int64_t 
     }
 }
 template <typename TX>
-__global__ __launch_bounds__(256) void k_small_products(const float* __restrict__ rows, const float* __restrict__ cols,
+__global__ __launch_bounds__(64 * kSmallNW) void k_small_products(const float* __restrict__ rows, const float* __restrict__ cols,
                                                         int Es, int Ts, const TX* __restrict__ x,
                                                         const float* __restrict__ W, const uint8_t* __restrict__ mask,
                                                         int T, int E, int64_t d, int xblocks, TX* __restrict__ dx,
                                                         float* __restrict__ dW) {
-    __shared__ float red[4][16][64];
+    __shared__ float red[kSmallNW][16][64];
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ntn = d / 64;
@@ -724,15 +727,14 @@ __global__ __launch_bounds__(256) void k_small_products(const float* __restrict_
 #pragma unroll
     for (int i = 0; i < 16; ++i) red[wid][i][lane] = acc[i];
     __syncthreads();
+    static_assert(kSmallNW == 16, "a row per wave");
+    float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = wid * 4 + i;
-        const float v = (red[0][r][lane] + red[1][r][lane]) + (red[2][r][lane] + red[3][r][lane]);
-        if (isx) {
-            if (r0 + r < T) dx[(r0 + r) * d + col] = Elem<TX>::from_f32(v);
-        } else {
-            if (r0 + r < E) dW[(r0 + r) * d + col] = v;
-        }
+    for (int w = 0; w < kSmallNW; ++w) v += red[w][wid][lane];
+    if (isx) {
+        if (r0 + wid < T) dx[(r0 + wid) * d + col] = Elem<TX>::from_f32(v);
+    } else {
+        if (r0 + wid < E) dW[(r0 + wid) * d + col] = v;
     }
 }
 
@@ -933,11 +935,11 @@ hipError_t launch_small_products(bool bf16, const float* rows, const float* cols
     const dim3 grid(static_cast<unsigned>(xb + wb));
     const int Es = (E + 15) / 16 * 16, Ts = (T + 15) / 16 * 16;
     if (bf16)
-        hipLaunchKernelGGL(k_small_products<bf16_t>, grid, dim3(256), 0, stream, rows, cols, Es, Ts,
+        hipLaunchKernelGGL(k_small_products<bf16_t>, grid, dim3(64 * kSmallNW), 0, stream, rows, cols, Es, Ts,
                            static_cast<const bf16_t*>(x), W, mask, T, E, d, static_cast<int>(xb),
                            static_cast<bf16_t*>(dx), dW);
     else
-        hipLaunchKernelGGL(k_small_products<float>, grid, dim3(256), 0, stream, rows, cols, Es, Ts,
+        hipLaunchKernelGGL(k_small_products<float>, grid, dim3(64 * kSmallNW), 0, stream, rows, cols, Es, Ts,
                            static_cast<const float*>(x), W, mask, T, E, d, static_cast<int>(xb),
                            static_cast<float*>(dx), dW);
     return hipGetLastError();

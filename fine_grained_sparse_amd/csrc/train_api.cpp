@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 
 #include "../../include/moe_train.h"
 #include "launch.hpp"
@@ -16,8 +15,13 @@ using namespace moe;
 namespace {
 
 constexpr int64_t kAlign = 256;
-// T E d up to which both products run as one launch on the vector ALUs.
-const int64_t kSmallProducts = getenv("SMALLP") ? atoll(getenv("SMALLP")) : 16000000;
+// Both products as one launch on the vector ALUs up to this many tokens and
+// this T E d.  Whole passes (balance loss, gradient) against the matrix units,
+// whose operands take four launches more: bf16 43 / 55 us at 301 x 48 x 1024
+// (T x E x d), 55 / 55 at 1024 x 64 x 1024, 76 / 54 at 2048 x 32 x 512, 75 / 81
+// at 64 x 384 x 7168, 100 / 84 at 128 x 384 x 7168; fp32 41 / 58 at 77 x 20 x
+// 320, 68 / 86 at 1024 x 256 x 1024.
+constexpr int64_t kSmallT = 1024, kSmallTEd = 200000000;
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -88,7 +92,7 @@ BackPlan back_plan(const moe_layer_desc* D) {
     BackPlan p{};
     p.bf16 = D->act_dtype == MOE_BF16;
     const int64_t T = D->T, E = D->E, d = D->d;
-    p.small = T * E * d <= kSmallProducts;
+    p.small = T <= kSmallT && T * E * d <= kSmallTEd;
     p.Ep = up(E, 64);
     p.Tp = up(T, 64);
     Arena ar;

@@ -17,12 +17,15 @@ import os
 
 import torch
 
-from . import HERE, LayerDesc, MoeError, _DT, _Nothing, _default_ws, _need, _ptr, desc
+from . import HERE, LayerDesc, MoeError, _current_raw_stream, _DT, _Nothing, _default_ws, _need, _ptr, desc
 from . import lib as _moe_lib
 
 TRAIN_LIB_PATH = os.path.join(HERE, "libmoe_train.so")
 TRAIN_EXPORTS = ("moe_router_train", "moe_balance_workspace_size", "moe_balance_loss", "moe_gate_backward",
                  "moe_router_backward_workspace_size", "moe_router_backward")
+
+
+_NOTHING = _Nothing()
 
 
 class Balance(ctypes.Structure):
@@ -59,15 +62,15 @@ def train_lib():
 
 
 def _launch(dev, stream):
-    """(stream, context): the launch stream on the tensors' device, and the
+    """(handle, context): the launch stream on the tensors' device, and the
     context in which that device and, for a stream of the caller's, that
     stream are current."""
     if stream is None:
         same = dev.index == torch.cuda.current_device()
-        return torch.cuda.current_stream(dev), _Nothing() if same else torch.cuda.device(dev)
+        return _current_raw_stream(dev.index), _NOTHING if same else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return stream, torch.cuda.stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _call(name, *args):
@@ -124,9 +127,9 @@ def router_train(x, W_r, b, K, scale=2.827, *, counts=True, workspace=None, stre
         w = torch.empty((T, K), dtype=torch.float32, device=dev)
         cnt = torch.empty((E,), dtype=torch.int32, device=dev) if counts else None
         z = torch.empty((T, E), dtype=torch.float32, device=dev)
-        ws = (workspace or _default_ws).get(dev, nbytes, s)
+        ws = (workspace or _default_ws).get(dev, nbytes, stream)
         _call("moe_router_train", ctypes.byref(D), _ptr(x), _ptr(W_r), _ptr(b), _ptr(idx), _ptr(w), _ptr(cnt),
-              _ptr(z), _ptr(ws), nbytes, s.cuda_stream)
+              _ptr(z), _ptr(ws), nbytes, s)
     return idx, w, cnt, z
 
 
@@ -144,9 +147,9 @@ def balance_loss(logits, topk_idx, alpha, *, seq_offsets=None, token_mask=None, 
     with ctx:
         loss = torch.empty((), dtype=torch.float32, device=dev)
         counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-        ws = (workspace or _default_ws).get(dev, nbytes, s)
+        ws = (workspace or _default_ws).get(dev, nbytes, stream)
         _call("moe_balance_loss", ctypes.byref(D), _ptr(logits), _ptr(topk_idx), ctypes.byref(B), _ptr(loss),
-              _ptr(counts), _ptr(ws), nbytes, s.cuda_stream)
+              _ptr(counts), _ptr(ws), nbytes, s)
     return loss, counts
 
 
@@ -187,7 +190,7 @@ def gate_backward(logits, topk_idx, d_topk_w, scale=2.827, *, alpha=None, seq_co
             out = torch.empty((T, E), dtype=torch.float32, device=dev)
         _need(out, "out", torch.float32, (T, E), dev)
         _call("moe_gate_backward", ctypes.byref(D), _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
-              None if B is None else ctypes.byref(B), _ptr(seq_counts), _ptr(d_loss), _ptr(out), s.cuda_stream)
+              None if B is None else ctypes.byref(B), _ptr(seq_counts), _ptr(d_loss), _ptr(out), s)
     return out
 
 
@@ -213,10 +216,10 @@ def router_backward(x, W_r, logits, topk_idx, d_topk_w, scale=2.827, *, alpha=No
     with ctx:
         dx = torch.empty_like(x) if need_dx else None
         dW = torch.empty((E, d), dtype=torch.float32, device=dev) if need_dW else None
-        ws = (workspace or _default_ws).get(dev, nbytes, s)
+        ws = (workspace or _default_ws).get(dev, nbytes, stream)
         _call("moe_router_backward", ctypes.byref(D), _ptr(x), _ptr(W_r), _ptr(logits), _ptr(topk_idx),
               _ptr(d_topk_w), None if B is None else ctypes.byref(B), _ptr(seq_counts), _ptr(d_loss), _ptr(dx),
-              _ptr(dW), _ptr(ws), nbytes, s.cuda_stream)
+              _ptr(dW), _ptr(ws), nbytes, s)
     return dx, dW
 
 
