@@ -52,6 +52,7 @@ struct Plan {
     bool packed;                              // weights in MOE_LAYOUT_FRAG16
     bool f8;                                  // routed experts in block-scaled FP8
     bool f4;                                  // routed experts in group-scaled FP4
+    bool once;                                // ... whose experts mostly fill one tile
     bool direct, fused;                       // ... without a dispatch; down projection and combine in one
     int64_t ys;                               // element size of the experts' outputs Y
     int64_t es;                               // element size
@@ -182,6 +183,7 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
     // shapes: 12.5 -> 10.3 ms at 768 tokens with the expert switch above;
     // below 512 the two measured the same within run-to-run noise)
     p.dcfg = (p.T >= 512 && p.dt == DT_BF16) ? big : TILE_SMALL;
+    p.once = arows <= 64ll * p.E;
     p.nch = static_cast<int>(cdiv(p.T, 64));
     p.max_tiles = static_cast<int>(cdiv(p.A, p.bm) + p.E + (p.ns ? cdiv(p.T, p.bm) : 0));
 
@@ -303,7 +305,7 @@ hipError_t launch_f4(const Plan& p, const GemmArgs& args, const uint8_t* bs, con
                      const int32_t* idx, int e0, hipStream_t s) {
     const GemmArgs g = f4_args(args, bs, bsu);
     if (p.direct) return launch_fp4_direct(g, epi, idx, p.T, p.K, e0, p.E, s);
-    return launch_gemm_fp4(g, epi, p.bm, p.max_tiles, max_n, s);
+    return launch_gemm_fp4(g, epi, p.bm, p.once, p.max_tiles, max_n, s);
 }
 
 // A dense map of the latent form over the batch.

@@ -214,7 +214,9 @@ __global__ __launch_bounds__(64 * NW) void k_fp4_rows16(const GemmArgs a, const 
         }
     } else {
         Job jb;
-        if (!pick_job<BM, BNO>(a, jb)) return;
+        // (the bf16 shared pairs, four times the bytes of a routed one, first:
+        // 1040 us against 1080, 64 tokens over 384 experts and a shared one)
+        if (!pick_job<BM, BNO>(a, jb, 0x7fffffff)) return;
         gi = jb.gi;
         expert = jb.expert;
         rows = jb.rows;
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(64 * kFusedNW) void k_fp4_down_combine(const GemmAr
 // to its registers.  A code is converted once and used by MT MFMAs.  LDS row
 // r keeps its 16-byte chunk c at c ^ (r % 16), so the 16 rows that a fragment
 // read touches at one chunk lie in 16 different bank groups.
-template <typename TC, int EPI, int MT>
+template <typename TC, int EPI, int MT, bool ONCE>
 struct Fp4Tile {
     static constexpr int BM = 16 * MT, RB = 4, NJ = EPI == EPI_SWIGLU ? RB / 2 : RB;
     static constexpr int BNO = 4 * 16 * NJ;            // output columns per workgroup
@@ -409,15 +411,12 @@ struct Fp4Tile {
         const int chunk = tid & 15;
         const int wpos = (tid >> 4) * 256 + ((chunk ^ (tid >> 4)) << 4);
         uint4 xr[2][XL];
-        auto load_x = [&](int st, uint4 (&o)[XL]) {
+        auto load_x = [&](int st, int i) {
             const int off = min(st * 256 + chunk * 16, K * 2 - 16);  // (past the end; the last stage may hold 64 columns)
-#pragma unroll
-            for (int i = 0; i < XL; ++i) o[i] = ldg16(xs[i] + off);
+            return ldg16(xs[i] + off);
         };
-        auto write_x = [&](int st, const uint4 (&o)[XL]) {
-            char* b = lds + (st & 1) * STAGE + wpos;
-#pragma unroll
-            for (int i = 0; i < XL; ++i) *reinterpret_cast<uint4*>(b + i * 16 * 256) = o[i];
+        auto write_x = [&](int st, int i, const uint4& v) {
+            *reinterpret_cast<uint4*>(lds + (st & 1) * STAGE + wpos + i * 16 * 256) = v;
         };
         auto read_x = [&](int st, int c, uint4 (&x)[MT]) {  // chunk c of rows r16 + 16 i
             const char* b = lds + (st & 1) * STAGE + r16 * 256 + ((c ^ r16) << 4);
@@ -435,25 +434,35 @@ struct Fp4Tile {
             for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
         // Loads run two stages ahead: stage st issues those of st + 2 into the
-        // registers that st's own came through, and ends by writing st + 1,
-        // loaded a whole stage ago, to the other buffer.
-        auto stages = [&](auto&& body) {
-            load_x(0, xr[0]);
-            load_x(1, xr[1]);
-            write_x(0, xr[0]);
-            __syncthreads();
-            for (int st = 0; st < nst; st += 2) {
-                load_x(st + 2, xr[0]);
-                body(st, std::integral_constant<int, 0>{});
-                write_x(st + 1, xr[1]);
-                __syncthreads();
-                if (st + 1 < nst) {
-                    load_x(st + 3, xr[1]);
-                    body(st + 1, std::integral_constant<int, 1>{});
-                    write_x(st + 2, xr[0]);
-                    __syncthreads();
-                }
+        // registers that its own came through, and writes st + 1, loaded a
+        // whole stage ago, to the other buffer.  A stage has 16 steps of MT
+        // MFMAs and does a little of this after each: a burst of loads or of
+        // LDS writes holds up the MFMAs behind it.
+        auto tick = [&](int st, auto par, int k) {
+            constexpr int P = decltype(par)::value;
+#pragma unroll
+            for (int i = 0; i < XL; ++i) {
+                if (k == 1 + i) xr[P][i] = load_x(st + 2, i);
+                if (k == 8 + i) write_x(st + 1, i, xr[1 - P][i]);
             }
+        };
+        auto stages = [&](auto&& body) {
+#pragma unroll
+            for (int i = 0; i < XL; ++i) {
+                xr[0][i] = load_x(0, i);
+                xr[1][i] = load_x(1, i);
+            }
+#pragma unroll
+            for (int i = 0; i < XL; ++i) write_x(0, i, xr[0][i]);
+            __syncthreads();
+            int st = 0;
+            for (; st + 1 < nst; st += 2) {
+                body(st, std::integral_constant<int, 0>{});
+                __syncthreads();
+                body(st + 1, std::integral_constant<int, 1>{});
+                __syncthreads();
+            }
+            if (st < nst) body(st, std::integral_constant<int, 0>{});
         };
         if (jb.gi == 0) {
             const int64_t eb = static_cast<int64_t>(jb.expert) * G.b_estride;
@@ -469,16 +478,16 @@ struct Fp4Tile {
             }
             uint4 q[2][RB];
             uint32_t e[2][RB];
-            auto load_w = [&](int st, uint4 (&o)[RB], uint32_t (&oe)[RB]) {
+            auto load_w = [&](int st, int j, uint4& o, uint32_t& oe) {
                 const int k = min(st, nst - 1);
-#pragma unroll
-                for (int j = 0; j < RB; ++j) {
-                    o[j] = ldg16(w[j] + static_cast<int64_t>(k) * 1024);
-                    oe[j] = sc[j][k * 64];
-                }
+                o = ONCE ? ldg16_once(w[j] + static_cast<int64_t>(k) * 1024) : ldg16(w[j] + static_cast<int64_t>(k) * 1024);
+                oe = sc[j][k * 64];
             };
-            load_w(0, q[0], e[0]);
-            load_w(1, q[1], e[1]);
+#pragma unroll
+            for (int j = 0; j < RB; ++j) {
+                load_w(0, j, q[0][j], e[0][j]);
+                load_w(1, j, q[1][j], e[1][j]);
+            }
             stages([&](int st, auto par) {
                 constexpr int P = decltype(par)::value;
                 uint4 x[2][MT], f[2];
@@ -505,11 +514,12 @@ struct Fp4Tile {
                         __builtin_amdgcn_sched_group_barrier(0x002, (4 + MT - 1) / MT, 0);
                     }
                     __builtin_amdgcn_sched_barrier(0);
+                    tick(st, par, k);
+                    // only now, past the codes' last use: loaded earlier, they would sit in other registers
+                    // and be copied back at the loop's end, a copy that waits for every load in flight
+                    if (s == 3) load_w(st + 2, j, q[P][j], e[P][j]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                // only now, past the codes' last use: loaded earlier, they would sit in other registers
-                // and be copied back at the loop's end, a copy that waits for every load in flight
-                load_w(st + 2, q[P], e[P]);
-                __builtin_amdgcn_sched_barrier(0);
             });
         } else {
             const int nsl = K / 32;  // 32-column blocks, loaded four ahead
@@ -519,25 +529,27 @@ struct Fp4Tile {
                 w[j] = static_cast<const char*>((EPI == EPI_SWIGLU && j >= NJ) ? G.seg[0].Bu : G.seg[0].B) +
                        static_cast<int64_t>(rb[j]) * nsl * 1024 + lane * 16;
             uint4 q[4][RB];
-            auto load_w = [&](int sl, uint4 (&o)[RB]) {
-                const int64_t k = min(sl, nsl - 1);
+            auto load_w = [&](int sl, int j) { return ldg16(w[j] + static_cast<int64_t>(min(sl, nsl - 1)) * 1024); };
 #pragma unroll
-                for (int j = 0; j < RB; ++j) o[j] = ldg16(w[j] + k * 1024);
-            };
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) load_w(s, q[s]);
-            stages([&](int st, auto) {
+                for (int j = 0; j < RB; ++j) q[s][j] = load_w(s, j);
+            stages([&](int st, auto par) {
+                uint4 x[2][MT];
+                read_x(st, grp, x[0]);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    if (4 * st + s < nsl) {  // (uniform: the last stage may hold two blocks)
-                        uint4 x[MT];
-                        read_x(st, 4 * s + grp, x);
+                    if (s < 3) read_x(st, 4 * (s + 1) + grp, x[(s + 1) & 1]);
+                    const bool use = 4 * st + s < nsl;  // (uniform: the last stage may hold two blocks)
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int j = 0; j < RB; ++j) {
+                        if (use)
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) acc[j][i] = Mfma<bf16_t>::run(q[s][j], x[s & 1][i], acc[j][i]);
                         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                        for (int j = 0; j < RB; ++j)
-#pragma unroll
-                            for (int i = 0; i < MT; ++i) acc[j][i] = Mfma<bf16_t>::run(q[s][j], x[i], acc[j][i]);
-                        load_w(4 * st + s + 4, q[s]);
+                        tick(st, par, s * RB + j);
+                        q[s][j] = load_w(4 * st + s + 4, j);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
@@ -564,18 +576,21 @@ struct Fp4Tile {
 
 // A tile with fewer rows (an expert's last) runs the body of the next quarter
 // of BM.
-template <typename TC, int EPI, int MT>
+template <typename TC, int EPI, int MT, bool ONCE>
 __global__ __launch_bounds__(256, 2) void k_fp4_tile(const GemmArgs a) {
-    using Tile = Fp4Tile<TC, EPI, MT>;
+    using Tile = Fp4Tile<TC, EPI, MT, ONCE>;
     __shared__ __attribute__((aligned(1024))) char lds[2 * Tile::STAGE];
     Job jb;
-    if (!pick_job<Tile::BM, Tile::BNO>(a, jb)) return;
+    // (48 experts of 7168 x 2048 and a shared one, shared pairs first or last:
+    // 276 / 310 us at 512 tokens, which make 128 of them in the up projection;
+    // 536 / 513 at 2048, where they would fill every CU)
+    if (!pick_job<Tile::BM, Tile::BNO>(a, jb, 256)) return;
     if (jb.rows <= Tile::BM / 4)
-        Fp4Tile<TC, EPI, MT / 4>::run(a, jb, lds);
+        Fp4Tile<TC, EPI, MT / 4, ONCE>::run(a, jb, lds);
     else if (jb.rows <= Tile::BM / 2)
-        Fp4Tile<TC, EPI, MT / 2>::run(a, jb, lds);
+        Fp4Tile<TC, EPI, MT / 2, ONCE>::run(a, jb, lds);
     else if (jb.rows <= Tile::BM / 4 * 3)
-        Fp4Tile<TC, EPI, MT / 4 * 3>::run(a, jb, lds);
+        Fp4Tile<TC, EPI, MT / 4 * 3, ONCE>::run(a, jb, lds);
     else
         Tile::run(a, jb, lds);
 }
@@ -599,7 +614,7 @@ __global__ __launch_bounds__(256) void k_pack_fp4(const uint4* __restrict__ src,
 }
 
 template <typename TC, int EPI>
-hipError_t launch_t(const GemmArgs& args, int bm, int max_tiles, int max_n, hipStream_t stream) {
+hipError_t launch_t(const GemmArgs& args, int bm, bool once, int max_tiles, int max_n, hipStream_t stream) {
     const int bno = (bm == 16 ? 64 : 256) / (EPI == EPI_SWIGLU ? 2 : 1);
     GemmArgs a = args;
     a.ntn = (max_n + bno - 1) / bno;
@@ -607,8 +622,10 @@ hipError_t launch_t(const GemmArgs& args, int bm, int max_tiles, int max_n, hipS
     const dim3 grid(job_blocks(max_tiles, a.ntn));
     if (bm == 16)
         hipLaunchKernelGGL((k_fp4_rows16<TC, EPI, 4, 1, false>), grid, dim3(256), 0, stream, a, DirectArgs{});
+    else if (once)
+        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4, true>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4, false>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -632,11 +649,11 @@ bool fp4_fits(const GemmArgs& a, Epi epi) {
 // accumulators leave room for one wave per SIMD.
 int fp4_bm(int64_t rows, int E, bool shared) { return rows < (shared ? 6 : 10) * static_cast<int64_t>(E) ? 16 : 64; }
 
-hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, int max_tiles, int max_n, hipStream_t stream) {
+hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, bool once, int max_tiles, int max_n, hipStream_t stream) {
     if (max_tiles <= 0 || max_n <= 0) return hipSuccess;
     if ((bm != 16 && bm != 64) || !args.tiles || !fp4_fits(args, epi)) return hipErrorInvalidValue;
-    if (epi == EPI_SWIGLU) return launch_t<bf16_t, EPI_SWIGLU>(args, bm, max_tiles, max_n, stream);
-    return launch_t<float, EPI_STORE>(args, bm, max_tiles, max_n, stream);
+    if (epi == EPI_SWIGLU) return launch_t<bf16_t, EPI_SWIGLU>(args, bm, once, max_tiles, max_n, stream);
+    return launch_t<float, EPI_STORE>(args, bm, once, max_tiles, max_n, stream);
 }
 
 bool fp4_direct(int64_t T) { return T <= kDirectT; }

@@ -22,12 +22,26 @@ struct Job {
     int gi, expert, row0, rows, n0;
 };
 
+// xcd_slot_pair with the shared stretch of an XCD before its routed one.
+__device__ __forceinline__ int xcd_slot_pair_shared_first(int b, int total_r, int total) {
+    const int per = (total_r + 7) >> 3, per_s = (total - total_r + 7) >> 3;
+    const int slot = b >> 3, xcd = b & 7;
+    if (slot < per_s) {
+        const int lin = total_r + xcd * per_s + slot;
+        return lin < total ? lin : -1;
+    }
+    const int k = slot - per_s, lin = xcd * per + k;
+    return (k < per && lin < total_r) ? lin : -1;
+}
+
 // With a tile table, BM is the table's rows per tile (the planner builds the
 // table for the kernels that walk it), and the job comes from one load of
 // the entry at slot / ntn, whose run fields place every tile of its run;
-// the two tile counts come in one load.
+// the two tile counts come in one load.  Up to `shared_first` shared pairs go
+// before the routed ones (for launches whose shared pairs take longer: the
+// short ones then end the launch).
 template <int BM, int BNO>
-__device__ __forceinline__ bool pick_job(const GemmArgs& a, Job& jb) {
+__device__ __forceinline__ bool pick_job(const GemmArgs& a, Job& jb, int shared_first = 0) {
     int total, total_r;  // active (M, N) tile pairs, and the routed ones among them
     if (a.tiles) {
         const int2 nt = *reinterpret_cast<const int2*>(a.ntiles);
@@ -36,7 +50,9 @@ __device__ __forceinline__ bool pick_job(const GemmArgs& a, Job& jb) {
     } else {
         total = total_r = ((a.M + BM - 1) / BM) * a.ntn;
     }
-    const int lin = xcd_slot_pair(static_cast<int>(blockIdx.x), total_r, total);
+    const int b = static_cast<int>(blockIdx.x);
+    const int lin = total - total_r <= shared_first ? xcd_slot_pair_shared_first(b, total_r, total)
+                                                    : xcd_slot_pair(b, total_r, total);
     if (lin < 0) return false;
     if (a.tiles) {
         const TileInfo t0 = a.tiles[lin / a.ntn];

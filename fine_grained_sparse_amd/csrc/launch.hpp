@@ -127,11 +127,11 @@ hipError_t launch_pack_frag16_fp8(const uint8_t* src, uint8_t* dst, int64_t coun
                                   hipStream_t stream);
 
 // The projections with 4-bit routed experts (fp4.hip): C = epi(A * B^T) over
-// a tile table of bm rows per tile (fp4_bm), bf16 A; C bf16 for the SwiGLU,
+// a tile table of bm rows per tile (fp4_bm; once: most experts fill one tile at most, so their weights are read once), bf16 A; C bf16 for the SwiGLU,
 // fp32 for the plain store.  Group 0: E2M1 codes (b_estride in bytes) with
 // E8M0 scales bs / bsu per 32 columns (s_estride in bytes), both in 16 x 128
 // blocks; group 1: packed bf16.  One K segment each.
-hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, int max_tiles, int max_n, hipStream_t stream);
+hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, bool once, int max_tiles, int max_n, hipStream_t stream);
 // rows per tile for this many routed rows over E experts
 int fp4_bm(int64_t rows, int E, bool shared);
 // The same without a tile table, for batches that fp4_direct() takes: rows of

@@ -130,13 +130,16 @@ constexpr int kMaxE = 1024;
 // and the blocks' work does not depend on the sequences.  A wave takes four
 // tokens at a time, so that their rows are in flight together.
 constexpr int kChunk = 64;
-constexpr int toks(int j2) { return j2 <= 4 ? 4 : 2; }  // tokens in hand (more experts: fewer, for the registers' sake)
+// tokens in hand (more experts: fewer, for the registers' sake) and waves of a
+// block (65521 x 896: 64 us with 8 waves, 71 with 16; 16384 x 384: 15.6 / 14.0)
+constexpr int toks(int j2) { return j2 <= 4 ? 4 : 2; }
+constexpr int partial_waves(int j2) { return j2 <= 4 ? 16 : 8; }
 template <int J2>
-__global__ __launch_bounds__(512) void k_balance_partial(const SeqArgs a, const float* __restrict__ z,
+__global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(const SeqArgs a, const float* __restrict__ z,
                                                          const int32_t* __restrict__ idx, float* __restrict__ part_p,
                                                          int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
                                                          int32_t* __restrict__ ticket) {
-    constexpr int NW = 8, kTok = toks(J2);
+    constexpr int NW = partial_waves(J2), kTok = toks(J2);
     __shared__ float sp[NW][J2 * 128];
     __shared__ int hist[kMaxE];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -191,8 +194,10 @@ __global__ __launch_bounds__(512) void k_balance_partial(const SeqArgs a, const 
         }
         __syncthreads();
         for (int e = tid; e < a.E; e += 64 * NW) {
-            part_p[slot * a.E + e] = ((sp[0][e] + sp[1][e]) + (sp[2][e] + sp[3][e])) +
-                                     ((sp[4][e] + sp[5][e]) + (sp[6][e] + sp[7][e]));
+            float p = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) p += sp[w][e];
+            part_p[slot * a.E + e] = p;
             part_c[slot * a.E + e] = hist[e];
         }
         __syncthreads();
@@ -245,8 +250,14 @@ __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const f
             const float f = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.K) * nf) / nf : 0.f;
             __hip_atomic_store(part_l + static_cast<int64_t>(q) * gridDim.x + blockIdx.x, l * f, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
+            // The share is written through to memory and read from there (agent-
+            // scope atomics); all that has to be in order is this one store before
+            // the ticket, and an acquire-release ticket would write back and
+            // invalidate the whole L2 in every block.
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             const int total = static_cast<int>(gridDim.x * gridDim.y);
-            last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
+            last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
         }
     }
     __syncthreads();
@@ -813,7 +824,8 @@ hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* 
     if (a.T < 1 || a.E < 1 || a.E > kMaxE || a.S < 1 || a.S > 65535) return hipErrorInvalidValue;
     const dim3 grid((a.T + kChunk - 1) / kChunk);
 #define MOE_CALL(J2) \
-    hipLaunchKernelGGL(k_balance_partial<J2>, grid, dim3(512), 0, stream, a, z, idx, part_p, part_c, part_n, ticket)
+    hipLaunchKernelGGL(k_balance_partial<J2>, grid, dim3(64 * partial_waves(J2)), 0, stream, a, z, idx, part_p, part_c, \
+                       part_n, ticket)
     MOE_FOR_E(a.E, MOE_CALL);
 #undef MOE_CALL
     const hipError_t err = hipGetLastError();
