@@ -15,6 +15,7 @@ MoE" sections 2-3; lilting.ch K3 essay for the latent form):
 with SwiGLU experts f(v) = W_down (silu(W_gate v) * (W_up v)).
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -190,6 +191,23 @@ class _Nothing:
         return False
 
 
+def _on_device(fn):
+    """Runs fn(first, ...) with the device of its first tensor current (where
+    its launches and default workspaces belong), whatever the caller's is."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        t = first.get("W_gate") if isinstance(first, dict) else first
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            if stream is not None and stream.device != t.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+            if t.device.index != torch.cuda.current_device():
+                with torch.cuda.device(t.device):
+                    return fn(first, *args, stream=stream, **kw)
+        return fn(first, *args, stream=stream, **kw)
+    return call
+
+
+@_on_device
 def router(x, W_r, b, K, scale=2.827, *, counts=True, workspace=None, stream=None,
            n_group=1, topk_group=1):
     """moe_router: returns (topk_idx int32 [T,K], topk_w fp32 [T,K],
@@ -281,6 +299,7 @@ def _weights_desc(weights, T, d, E, K, scale, dt, dev, n_shared, n_group=1, topk
     return D, W
 
 
+@_on_device
 def bias_update(counts, b, gamma=1e-3, *, stream=None):
     """moe_bias_update: b (fp32 [E], in place) += gamma * sgn(mean - counts)
     from the per-expert selection counts (int32 [E]) of one or more
@@ -295,6 +314,7 @@ def bias_update(counts, b, gamma=1e-3, *, stream=None):
     return b
 
 
+@_on_device
 def bias_quantile(x, W_r, K, *, out=None, workspace=None, stream=None):
     """moe_bias_quantile: the Quantile Balancing bias of a batch (fp32 [E]):
     b_e = mean(theta) - theta_e with theta_e the n-th largest router score of
@@ -322,6 +342,7 @@ def bias_quantile(x, W_r, K, *, out=None, workspace=None, stream=None):
     return b
 
 
+@_on_device
 def pack_weights(weights, *, n_shared=None, stream=None):
     """moe_pack_weights: row-major weights (bf16, or FP8 or FP4 routed experts
     with bf16 shared / latent maps) -> a new dict of tensors of the same
@@ -383,6 +404,7 @@ def _forward_call(x, W_r, b, weights, K, scale, n_shared, out, return_routing, s
     return D, W, out, routing, outs
 
 
+@_on_device
 def forward(x, W_r, b, weights, K, scale=2.827, *, n_shared=None, out=None,
             return_routing=False, workspace=None, stream=None, stage_events=None,
             n_group=1, topk_group=1):
@@ -421,6 +443,7 @@ def slice_workspace_size(layer_desc: LayerDesc, e0: int, E_total: int) -> int:
     return int(lib().moe_slice_workspace_size(ctypes.byref(layer_desc), e0, E_total))
 
 
+@_on_device
 def forward_slice(x, topk_idx, topk_w, weights, e0, E_total, *, n_shared=None, out=None,
                   return_dispatch=False, workspace=None, stream=None):
     """moe_forward_slice: one GPU's share of an expert-parallel layer.
@@ -465,6 +488,7 @@ def forward_slice(x, topk_idx, topk_w, weights, e0, E_total, *, n_shared=None, o
     return (out, disp) if return_dispatch else out
 
 
+@_on_device
 def forward_noalloc(x, W_r, b, weights, K, scale=2.827, *, n_shared=None, out=None,
                     return_routing=False, stream=None, n_group=1, topk_group=1):
     """moe_forward_noalloc: forward() with the library's fixed scratch array

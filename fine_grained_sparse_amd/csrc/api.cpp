@@ -178,7 +178,7 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
         const int64_t nt = std::max<int64_t>(cdiv(std::max(p.F, p.Fsh), 256), cdiv(p.din, 512));
         if (mt * nt < 128) p.ecfg = TILE_NARROW;
     }
-    p.bm = p.f4 ? fp4_bm(arows, p.E, p.ns > 0) : tile_bm(p.ecfg);
+    p.bm = p.f4 ? fp4_bm(arows, p.E, p.F, p.ns > 0) : tile_bm(p.ecfg);
     // dense maps of the latent form: 128-row tiles from 512 tokens (K3
     // shapes: 12.5 -> 10.3 ms at 768 tokens with the expert switch above;
     // below 512 the two measured the same within run-to-run noise)

@@ -639,15 +639,20 @@ bool fp4_fits(const GemmArgs& a, Epi epi) {
 
 }  // namespace
 
-// 64-row tiles from 10 rows per expert, or from 6 when shared experts, whose
-// every 16 tokens would be another pass over their weights, ride along.
-// Measured on 7168-wide layers (16-row against 64-row tiles): 48 of 384
-// experts alone 202 against 238 us at 5.3 rows, 219 / 245 at 8, 249 / 253 at
-// 10.7, 310 / 260 at 16, 2070 / 528 at 43 (with a shared one); all 384 experts
-// and a shared one 1592 / 1617 us at 5.3 rows, 2060 / 1679 at 10.7.  128-row
+// 64-row tiles from 8 rows per expert, or from 4 when shared experts, whose
+// every 16 tokens would be another pass over their weights, ride along; where
+// the 64-row tiles of the up projection are fewer than the CUs, from 16.
+// Measured (16-row against 64-row tiles), 7168 x 2048: 48 of 384 experts alone
+// 202 / 212 us at 5.3 rows, 218 / 219 at 8, 255 / 225 at 10.7, 324 / 235 at 16;
+// 384 experts and a shared one 1337 / 1318 us at 2.7 rows, 1495 / 1418 at 4,
+// 1613 / 1460 at 5.3, 2090 / 1599 at 10.7; 48 experts of 1024 x 256 and a shared
+// one (96 tiles) 33 / 36 us at 5.3, 32 / 40 at 10.7, 53 / 48 at 21.  128-row
 // tiles lost to 64-row ones even at 341 rows (1.40 against 1.35 ms): their
 // accumulators leave room for one wave per SIMD.
-int fp4_bm(int64_t rows, int E, bool shared) { return rows < (shared ? 6 : 10) * static_cast<int64_t>(E) ? 16 : 64; }
+int fp4_bm(int64_t rows, int E, int F, bool shared) {
+    const bool few = static_cast<int64_t>(E) * ((F + 127) / 128) < 256;
+    return rows < (few ? 16 : shared ? 4 : 8) * static_cast<int64_t>(E) ? 16 : 64;
+}
 
 hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, bool once, int max_tiles, int max_n, hipStream_t stream) {
     if (max_tiles <= 0 || max_n <= 0) return hipSuccess;

@@ -132,8 +132,8 @@ hipError_t launch_pack_frag16_fp8(const uint8_t* src, uint8_t* dst, int64_t coun
 // E8M0 scales bs / bsu per 32 columns (s_estride in bytes), both in 16 x 128
 // blocks; group 1: packed bf16.  One K segment each.
 hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, bool once, int max_tiles, int max_n, hipStream_t stream);
-// rows per tile for this many routed rows over E experts
-int fp4_bm(int64_t rows, int E, bool shared);
+// rows per tile for this many routed rows over E experts of width F
+int fp4_bm(int64_t rows, int E, int F, bool shared);
 // The same without a tile table, for batches that fp4_direct() takes: rows of
 // C are assignments a = t K + k (group 1: tokens), whose experts the kernel
 // finds in idx (ids outside e0 .. e0 + E - 1: their rows are not written).

@@ -127,19 +127,24 @@ constexpr int kMaxE = 1024;
 // meets, the sums of p and the counts over their common tokens go to partial
 // row c + q: along the ascending sequences c + q grows with every (chunk,
 // sequence) pair that meets, so the rows are distinct and at most chunks + S,
-// and the blocks' work does not depend on the sequences.  A wave takes four
-// tokens at a time, so that their rows are in flight together.
+// and the blocks' work does not depend on the sequences.  A wave takes up to
+// four tokens at a time, so that their rows are in flight together.  Bound by
+// reading z: 235 MB (65521 x 896) in 56 us, 4.2 TB/s; 16384 x 384, which the
+// caches hold, takes 14 us, mostly the latency of one round.
 constexpr int kChunk = 64;
-// tokens in hand (more experts: fewer, for the registers' sake) and waves of a
-// block (65521 x 896: 64 us with 8 waves, 71 with 16; 16384 x 384: 15.6 / 14.0)
+// Tokens in hand (more experts: fewer, for the registers' sake; 65521 x 896:
+// k_balance_partial 56 us with one, 64 with two, 69 with four, which suit the
+// gradient) and waves of a block (65521 x 896: 64 us with 8 waves, 71 with 16;
+// 16384 x 384: 15.6 / 14.0).
 constexpr int toks(int j2) { return j2 <= 4 ? 4 : 2; }
+constexpr int partial_toks(int j2) { return j2 <= 4 ? 4 : 1; }
 constexpr int partial_waves(int j2) { return j2 <= 4 ? 16 : 8; }
 template <int J2>
 __global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(const SeqArgs a, const float* __restrict__ z,
                                                          const int32_t* __restrict__ idx, float* __restrict__ part_p,
                                                          int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
                                                          int32_t* __restrict__ ticket) {
-    constexpr int NW = partial_waves(J2), kTok = toks(J2);
+    constexpr int NW = partial_waves(J2), kTok = partial_toks(J2);
     __shared__ float sp[NW][J2 * 128];
     __shared__ int hist[kMaxE];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -283,9 +288,8 @@ struct PlaneArgs {
     int32_t Es, Ts;          // E and T in whole 16s
     bf16_t* rows;   // [T][3 Ep]: hi | lo | hi of a token's row, zero past E
     bf16_t* cols;   // [Tb][3][Eb] blocks of 16 experts x 32 tokens of its parts hi, mid, lo (hi + mid + lo == dz):
-                    // element (r, c) of a block at ((c / 8) 16 + r) 8 + c % 8, zero past E and T.  (What a slab of
-                    // tokens reads lies together: blocks a power of two apart, as with the tokens fastest, met in
-                    // the same memory channels and k_dw took 548 us for XXX at 16384 tokens.)
+                    // element (r, c) of a block at ((c / 8) 16 + r) 8 + c % 8, zero past E and T; a slab of tokens
+                    // lies together
     uint16_t* live; // [32 Tb]: 0xffff for the tokens that count, else 0
     int32_t Ep, Eb, Tb;
 };
@@ -295,7 +299,10 @@ enum GateOut { GATE_ROWS = 0, GATE_SMALL = 1, GATE_PLANES = 2 };
 // A wave takes a few consecutive tokens.  The gate term touches only the K
 // chosen experts of each: lane 16 u + k computes token u's slot k, and the
 // values reach the lanes that own the experts through a row in LDS that is
-// zero between tokens.
+// zero between tokens.  Bound by its one reading of z and writing of dz: 470 MB
+// (65521 x 896) in 95 us, 4.9 TB/s, a large copy's rate here.  (Rows whose
+// every lane asked whether its pair lies inside took 146 us, those with four
+// tokens in hand at 14 pairs a lane 225: 193 registers, two waves per SIMD.)
 template <int J2, int OUT>
 __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const float* __restrict__ z,
                                                        const int32_t* __restrict__ idx, const float* __restrict__ dw,
@@ -330,8 +337,10 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
         const Sigm s = sigm(ok ? z[static_cast<int64_t>(t) * a.E + e] : 0.f);
         const float g = ok ? dw[i] : 0.f, sc = ok ? s.s : 0.f;
         const float den = row16_sum(sc) + 1e-20f;
-        const float mean = row16_sum(g * sc) / den;
-        gv = scale / den * (g - mean) * (s.s * s.c);
+        // g - mean in two passes: with few or alike g the first mean leaves only
+        // its rounding error, which the second removes (K = 1 has no gradient)
+        const float dev = g - row16_sum(g * sc) / den;
+        gv = scale / den * (dev - row16_sum(ok ? dev * sc : 0.f) / den) * (s.s * s.c);
         ge = ok ? e : -1;
     }
 
@@ -537,7 +546,14 @@ __global__ __launch_bounds__(256) void k_pack_wt(const float* __restrict__ W, in
 // b every wave waits for its own loads of b + 1, which have had a slab's time,
 // and meets the others: after that b + 1 may be read, and b - 1, which nobody
 // reads any more, makes room for b + 2.  The first fragments of b + 1 are read
-// under the last products of b.  XXX
+// under the last products of b.  Between them the loads go out one or two at a
+// time: a burst of them holds up the MFMAs behind it.
+// 16384 x 384 x 7168 (T x E x d): 270 GFLOP of partial products in 246 us from
+// rest, 278 back to back (1.1 and 0.97 PFLOP/s; 87% of the CUs have a block,
+// whose matrix pipes are then 61% busy).  On the way there: 507 us with 384 x
+// 128 tiles and dz straight into registers, 559 with both operands through LDS
+// one slab ahead, 359 with three buffers and register staging, 316 with the
+// loads by DMA in one burst.
 // x of a token that does not count may hold anything: its fragments are
 // masked by `live` after the read.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -551,14 +567,15 @@ struct DwArgs {
 };
 // 16 (4) bytes per lane from base + off (src) to LDS at lds + 16 (4) lane.
 // Nothing waits for these but wait_loads(), and no register is their target.
+// (A write of m0 needs a wait state before a load to LDS reads it.)
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 

@@ -10,9 +10,13 @@ library declared in include/moe_train.h (formulas and limits there).
 
 Like the package's other entry points these only check and marshal arguments,
 allocate outputs and workspaces on the launch stream, and enqueue HIP
-kernels; there is no fallback.
+kernels; there is no fallback.  A call that is captured into a graph should be
+given a Workspace of its own, used once before the capture: the default one
+may replace its buffer when a larger call comes, and graphs that share a
+buffer must not run at the same time.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -71,6 +75,23 @@ def _launch(dev, stream):
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _balance_bytes(T, E, K, S):
+    nbytes = int(train_lib().moe_balance_workspace_size(ctypes.byref(desc(T=T, d=64, E=E, K=K)), S))
+    if nbytes == 0:
+        raise MoeError("moe_balance_workspace_size", 2)
+    return nbytes
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_bytes(T, d, E, K, act_dtype):
+    D = desc(T=T, d=d, E=E, K=K, act_dtype=act_dtype)
+    nbytes = int(train_lib().moe_router_backward_workspace_size(ctypes.byref(D)))
+    if nbytes == 0:
+        raise MoeError("moe_router_backward_workspace_size", 2)
+    return nbytes
 
 
 def _call(name, *args):
@@ -140,9 +161,7 @@ def balance_loss(logits, topk_idx, alpha, *, seq_offsets=None, token_mask=None, 
     T, E, K, dev = _logits(logits, topk_idx)
     S, B = _balance(T, dev, alpha, seq_offsets, token_mask)
     D = desc(T=T, d=64, E=E, K=K)
-    nbytes = int(train_lib().moe_balance_workspace_size(ctypes.byref(D), S))
-    if nbytes == 0:
-        raise MoeError("moe_balance_workspace_size", 2)
+    nbytes = _balance_bytes(T, E, K, S)
     s, ctx = _launch(dev, stream)
     with ctx:
         loss = torch.empty((), dtype=torch.float32, device=dev)
@@ -209,9 +228,7 @@ def router_backward(x, W_r, logits, topk_idx, d_topk_w, scale=2.827, *, alpha=No
         raise ValueError("neither dx nor dW_r is wanted")
     B = _grads(T, E, K, dev, d_topk_w, d_loss, alpha, seq_counts, seq_offsets, token_mask)
     D = desc(T=T, d=d, E=E, K=K, scale=scale, act_dtype=_DT[x.dtype])
-    nbytes = int(train_lib().moe_router_backward_workspace_size(ctypes.byref(D)))
-    if nbytes == 0:
-        raise MoeError("moe_router_backward_workspace_size", 2)
+    nbytes = _backward_bytes(T, d, E, K, _DT[x.dtype])
     s, ctx = _launch(dev, stream)
     with ctx:
         dx = torch.empty_like(x) if need_dx else None

@@ -258,7 +258,8 @@ moe_status moe_forward_slice(const moe_layer_desc *desc,
  * but its scratch is a fixed array of MOE_NOALLOC_SCRATCH_BYTES (128 MiB)
  * that the library holds on each GPU it runs on until the process ends, so
  * no workspace is passed and nothing is allocated.  Enough for the K2 layer
- * up to T = 512 tokens and the K3 latent layer at T = 256; a descriptor
+ * up to T = 512 tokens and the K3 latent layer at T = 256 (352 and 224 with
+ * FP4 experts, whose outputs are kept in fp32); a descriptor
  * needing more (moe_workspace_size(desc, 1) > MOE_NOALLOC_SCRATCH_BYTES)
  * returns MOE_ERR_SCRATCH with nothing enqueued.  The array of the current
  * device is used (its address is resolved on the first call on that

@@ -68,7 +68,7 @@ moe_status moe_router_train(const moe_layer_desc *desc, const void *x,
 
 /* The balance loss.  Uses T, E and K of the descriptor.
  *   logits [T, E] fp32, topk_idx [T, K] int32 (distinct ids 0 .. E - 1 in a
- *   token; other ids are skipped)
+ *   token; other ids are counted nowhere, and an id twice counts twice)
  *   -> loss [1] fp32, seq_counts [S, E] int32 (c_qi; their sum over q is a
  *   load that moe_bias_update takes).
  * Workspace of at least moe_balance_workspace_size(desc, S) bytes (0: an

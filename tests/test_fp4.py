@@ -405,3 +405,31 @@ def test_python_refusals():
     with pytest.raises((TypeError, ValueError)):
         moe.forward_slice(x, idx, wt, {k: v for k, v in p.items() if k != "W_down_scale"}, 0, 2)
     assert moe.forward_slice(x[:0], idx[:0], wt[:0], p, 0, 2).shape == (0, 256)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 12, 40, 1400])
+def test_experts_past_32bit_offsets(T):
+    # 300 experts of 2048 x 7168: 2.2e9 bytes of codes per matrix; the tokens choose among the ends
+    E, F, d, K = 300, 2048, 7168, 2
+    _log(f"[gpu] fp4 past 32-bit weight offsets T={T}")
+    r = np.random.default_rng(T)
+    pick = np.array([0, 146, 298, 299], dtype=np.int32)
+    idx = torch.from_numpy(np.stack([np.sort(r.permutation(pick)[:K]) for _ in range(T)])).to(DEV)
+    x, idx, wt, w = _layer(71, T, d, E, E, K, F, idx=idx)
+    out = _run(x, idx, wt, w, 0, E, 0)
+    torch.cuda.synchronize()
+    some = torch.arange(0, T, max(1, T // 40), device=DEV)
+    _check(f"offsets T={T}", out[some], *_reference(x[some], idx[some], wt[some], w, 0))
+
+
+@pytest.mark.gpu
+def test_rows_past_32bit_offsets():
+    # 160000 assignment rows of 7168 fp32 outputs (4.6e9 bytes); a sample of the tokens, the last among them
+    T, d, E, K, F = 40000, 7168, 5, 4, 128
+    _log("[gpu] fp4 past 32-bit row offsets")
+    x, idx, wt, w = _layer(72, T, d, E, E, K, F)
+    out = _run(x, idx, wt, w, 0, E, 0)
+    torch.cuda.synchronize()
+    some = torch.cat((torch.arange(0, T, 997, device=DEV), torch.arange(T - 40, T, device=DEV)))
+    _check("row offsets", out[some], *_reference(x[some], idx[some], wt[some], w, 0))

@@ -530,3 +530,98 @@ def test_python_refusals():
         with pytest.raises((TypeError, ValueError, moe.MoeError)):
             f()
             _log(f"case {i} was accepted")
+
+
+@pytest.mark.gpu
+def test_one_expert_per_token_has_no_gate_gradient():
+    # K = 1: w is the scale whatever the score.  g - mean leaves at most 3 e |g|, its second pass 3 e of that
+    z, idx, dw, off, _ = _make(51, 200, 70, 1, 2)
+    gz, gi, gw = _dev(z, idx, dw)
+    d = moe.gate_backward(gz, gi, gw, 2.827).double().cpu().numpy()
+    assert (np.abs(d) <= 16 * E32 * E32 * 2.827 * np.abs(dw).astype(np.float64) + 1e-19).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt,T,E,d", [("bf16", 90, 40, 128), ("f32", 90, 40, 128), ("bf16", 1500, 100, 256),
+                                      ("f32", 1500, 100, 256)])
+def test_masked_tokens_leave_the_weights_gradient_alone(dt, T, E, d):
+    # x, logits, ids and gate gradients of padding may hold anything: the results are those of a clean batch
+    z, idx, dw, off, mask = _make(53, T, E, 4, 3, 0.3)
+    r = np.random.default_rng(8)
+    x = torch.from_numpy(r.normal(0, 1, (T, d)).astype(np.float32)).to(DEV)
+    x = x.bfloat16() if dt == "bf16" else x
+    W = torch.from_numpy(r.normal(0, 1, (E, d)).astype(np.float32)).to(DEV)
+    gz, gi, gw, go, gm = _dev(z, idx, dw, off, mask)
+    dead = (gm == 0).nonzero().flatten()
+    outs = []
+    for dirty in (False, True):
+        if dirty:
+            x, gz, gi, gw = x.clone(), gz.clone(), gi.clone(), gw.clone()
+            x[dead[0]], x[dead[1], 5], x[dead[-1]] = float("nan"), float("inf"), float("-inf")
+            gz[dead], gi[dead], gw[dead] = float("nan"), 1 << 30, float("inf")
+        l, c = moe.balance_loss(gz, gi, 0.1, seq_offsets=go, token_mask=gm)
+        outs.append((l, c, *moe.router_backward(x, W, gz, gi, gw, alpha=0.1, seq_counts=c, seq_offsets=go,
+                                                token_mask=gm)))
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.isfinite(outs[1][3]).all() and (outs[1][2][dead] == 0).all()
+
+
+@pytest.mark.gpu
+def test_logits_past_32bit_offsets():
+    # 2.2 million tokens x 1000 experts: 2.2e9 logits, 8.8e9 bytes; the last tokens' rows and the counts
+    T, E, K, S = 2_200_000, 1000, 2, 3
+    _log("[gpu] train past 32-bit offsets")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    z = torch.randn(T, E, device=DEV, generator=g)
+    idx = torch.randint(0, E // 2, (T, K), device=DEV, dtype=torch.int32, generator=g)
+    idx[:, 1] += E // 2
+    off = torch.tensor([0, 5, 1_000_001, T], dtype=torch.int32, device=DEV)
+    l, c = moe.balance_loss(z, idx, 1.0, seq_offsets=off)
+    d = moe.gate_backward(z, idx, None, alpha=1.0, seq_counts=c, seq_offsets=off)
+    torch.cuda.synchronize()
+    want, o = 0.0, off.tolist()
+    for q in range(S):
+        f = torch.bincount(idx[o[q]:o[q + 1]].flatten().long(), minlength=E)
+        assert torch.equal(c[q], f.int())
+        p = torch.zeros(E, dtype=torch.float64, device=DEV)
+        for a in range(o[q], o[q + 1], 200_000):
+            s = torch.sigmoid(z[a:min(a + 200_000, o[q + 1])].double())
+            p += (s / s.sum(1, keepdim=True)).sum(0)
+        n = o[q + 1] - o[q]
+        want += (f.double() * E / (K * n) * p / n).sum().item() / S
+    # sums 16 + 34376 / 16 deep over the chunks
+    assert abs(l.item() - want) <= (160 + T / 256) * E32 * want
+    s = torch.sigmoid(z[-50:].double())
+    tot = s.sum(1, keepdim=True)
+    n = T - o[2]
+    a = c[2].double() * E / (K * n * n) / S
+    ref = (a - (a * s).sum(1, keepdim=True) / tot) / tot * s * (1 - s)
+    tol = 128 * E32 * (a + (a * s).sum(1, keepdim=True) / tot) / tot * s * (1 - s) + 1e-38
+    assert ((d[-50:].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    # the same calls on two streams with their default workspaces, against each alone
+    args = []
+    for seed in (61, 62):
+        z, idx, dw, off, mask = _make(seed, 3000, 200, 4, 5, 0.1)
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        args.append((torch.randn(3000, 256, device=DEV, generator=g).bfloat16(),
+                     torch.randn(200, 256, device=DEV, generator=g), *_dev(z, idx, dw, off, mask)))
+
+    def step(x, W, z, idx, dw, off, mask, stream=None):
+        l, c = moe.balance_loss(z, idx, 0.1, seq_offsets=off, token_mask=mask, stream=stream)
+        return (l, c, *moe.router_backward(x, W, z, idx, dw, alpha=0.1, seq_counts=c, seq_offsets=off,
+                                           token_mask=mask, stream=stream))
+    alone = [step(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    for _ in range(5):
+        both = [step(*a, stream=s) for a, s in zip(args, streams)]
+        torch.cuda.synchronize()
+        for x, y in zip(alone, both):
+            for u, v in zip(x, y):
+                assert torch.equal(u, v)
