@@ -318,10 +318,11 @@ hipError_t launch_dense(const Plan& p, const GemmArgs& g, int n, hipStream_t s) 
 hipError_t combine(const Plan& p, const void* Y, const void* ysh, const int32_t* idx, int e0, const int32_t* pos,
                    const float* w, int N, void* out, hipStream_t s) {
     if (p.fused) return hipSuccess;  // the down projection did it
-    if (p.direct)
-        return launch_combine_direct(static_cast<const float*>(Y), N, static_cast<const float*>(ysh), idx, e0, p.E, w,
-                                     p.T, p.K, N, static_cast<uint16_t*>(out), N, s);
-    return launch_combine(p.dt, p.f4, Y, N, ysh, pos, w, p.T, p.K, N, out, N, s);
+    if (p.f4)
+        return launch_combine_f32(static_cast<const float*>(Y), N, static_cast<const float*>(ysh),
+                                  p.direct ? nullptr : pos, idx, e0, p.E, w, p.T, p.K, N, static_cast<uint16_t*>(out), N,
+                                  s);
+    return launch_combine(p.dt, Y, N, ysh, pos, w, p.T, p.K, N, out, N, s);
 }
 
 hipError_t record(void* const* ev, int i, hipStream_t s) {

@@ -246,8 +246,8 @@ __device__ __forceinline__ void unpack8_once(const bf16_t* p, float (&o)[8]) {
 }
 __device__ __forceinline__ void unpack8_once(const float* p, float (&o)[8]) { unpack8(p, o); }
 
-template <typename TY, typename T>
-__global__ __launch_bounds__(256) void k_combine(const TY* __restrict__ Y, int64_t ldy, const TY* __restrict__ Ysh,
+template <typename T>
+__global__ __launch_bounds__(256) void k_combine(const T* __restrict__ Y, int64_t ldy, const T* __restrict__ Ysh,
                                                  const int32_t* __restrict__ pos, const float* __restrict__ w, int K,
                                                  int N, T* __restrict__ out, int64_t ldo) {
     const int t = blockIdx.x;
@@ -275,45 +275,59 @@ __global__ __launch_bounds__(256) void k_combine(const TY* __restrict__ Y, int64
 constexpr int64_t kSmallA = 4096;      // assignments of k_dispatch_small
 constexpr int kSmallLds = 128 * 1024;  // and its LDS (12 bytes per chunk and expert), of the 160 KiB
 
-// The combine of a direct launch: few tokens, so the columns of a token are
-// spread over blocks of one wave and every row a thread needs is asked for
-// before the first is used (one after the other, at one token, took 12 us).
-constexpr int kDirectK = 16;
-__global__ __launch_bounds__(64) void k_combine_direct(const float* __restrict__ Y, int64_t ldy,
-                                                       const float* __restrict__ Ysh, const int32_t* __restrict__ idx,
-                                                       int e0, int E, const float* __restrict__ w, int K, int N,
-                                                       bf16_t* __restrict__ out, int64_t ldo) {
-    const int t = blockIdx.y, c = (blockIdx.x * 64 + threadIdx.x) * 4;
+// The combine of fp32 outputs (FP4 layers): four columns of a token per
+// thread, and every row it needs is asked for before the first is used (one
+// after the other, as above, took 12 us at one token, 10.6 at 256).  Row of
+// slot a = t K + k: pos[a], or with pos NULL a itself where idx[a] is one of
+// e0 .. e0 + E - 1; -1 (none) is skipped.
+template <int KM>
+__global__ __launch_bounds__(64) void k_combine_f32(const float* __restrict__ Y, int64_t ldy,
+                                                    const float* __restrict__ Ysh, const int32_t* __restrict__ pos,
+                                                    const int32_t* __restrict__ idx, int e0, int E,
+                                                    const float* __restrict__ w, int K, int N,
+                                                    bf16_t* __restrict__ out, int64_t ldo) {
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    const int64_t t = blockIdx.x;
+    const int c = (blockIdx.y * 64 + threadIdx.x) * 4;
     if (c >= N) return;
-    float4 v[kDirectK];
-    float wk[kDirectK];
+    f4 v[KM];
+    float wk[KM];
 #pragma unroll
-    for (int k = 0; k < kDirectK; ++k) {
-        const int64_t a = static_cast<int64_t>(t) * K + k;
-        const bool use = k < K && static_cast<unsigned>(idx[k < K ? a : 0] - e0) < static_cast<unsigned>(E);
-        wk[k] = use ? w[a] : 0.f;
-        v[k] = use ? *reinterpret_cast<const float4*>(Y + a * ldy + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < KM; ++k) {
+        v[k] = f4{0.f, 0.f, 0.f, 0.f};
+        wk[k] = 0.f;
+        if (k < K) {
+            const int64_t a = t * K + k;
+            const int64_t row = pos ? pos[a] : (static_cast<unsigned>(idx[a] - e0) < static_cast<unsigned>(E) ? a : -1);
+            if (row >= 0) {  // (uniform)
+                wk[k] = w[a];
+                v[k] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(Y + row * ldy + c));
+            }
+        }
     }
-    float4 s = Ysh ? *reinterpret_cast<const float4*>(Ysh + t * ldy + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    f4 s = Ysh ? __builtin_nontemporal_load(reinterpret_cast<const f4*>(Ysh + t * ldy + c)) : f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kDirectK; ++k) {
-        s.x += wk[k] * v[k].x;
-        s.y += wk[k] * v[k].y;
-        s.z += wk[k] * v[k].z;
-        s.w += wk[k] * v[k].w;
-    }
+    for (int k = 0; k < KM; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = fmaf(wk[k], v[k][i], s[i]);
     *reinterpret_cast<uint2*>(out + t * ldo + c) =
-        make_uint2(f32_to_bf16(s.x) | (static_cast<uint32_t>(f32_to_bf16(s.y)) << 16),
-                   f32_to_bf16(s.z) | (static_cast<uint32_t>(f32_to_bf16(s.w)) << 16));
+        make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
+                   f32_to_bf16(s[2]) | (static_cast<uint32_t>(f32_to_bf16(s[3])) << 16));
 }
 
 }  // namespace
 
-hipError_t launch_combine_direct(const float* Y, int64_t ldy, const float* Yshared, const int32_t* idx, int e0, int E,
-                                 const float* w, int T, int K, int N, uint16_t* out, int64_t ldo, hipStream_t stream) {
-    if (T < 1 || K > kDirectK || N % 4) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_combine_direct, dim3((N / 4 + 63) / 64, T), dim3(64), 0, stream, Y, ldy, Yshared, idx, e0, E,
-                       w, K, N, out, ldo);
+hipError_t launch_combine_f32(const float* Y, int64_t ldy, const float* Yshared, const int32_t* pos,
+                              const int32_t* idx, int e0, int E, const float* w, int T, int K, int N, uint16_t* out,
+                              int64_t ldo, hipStream_t stream) {
+    if (T < 1 || K < 1 || K > 16 || N % 4 || (N / 4 + 63) / 64 > 65535) return hipErrorInvalidValue;
+    const dim3 grid(T, (N / 4 + 63) / 64);
+    if (K <= 8)
+        hipLaunchKernelGGL(k_combine_f32<8>, grid, dim3(64), 0, stream, Y, ldy, Yshared, pos, idx, e0, E, w, K, N, out,
+                           ldo);
+    else
+        hipLaunchKernelGGL(k_combine_f32<16>, grid, dim3(64), 0, stream, Y, ldy, Yshared, pos, idx, e0, E, w, K, N, out,
+                           ldo);
     return hipGetLastError();
 }
 
@@ -353,17 +367,14 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int 
     return hipGetLastError();
 }
 
-hipError_t launch_combine(DType dt, bool y_f32, const void* Y, int64_t ldy, const void* Yshared, const int32_t* pos, const float* w,
+hipError_t launch_combine(DType dt, const void* Y, int64_t ldy, const void* Yshared, const int32_t* pos, const float* w,
                           int T, int K, int N, void* out, int64_t ldo, hipStream_t stream) {
     if (T <= 0) return hipSuccess;
     if (dt == DT_F32)
-        hipLaunchKernelGGL((k_combine<float, float>), dim3(T), dim3(256), 0, stream, static_cast<const float*>(Y), ldy,
+        hipLaunchKernelGGL(k_combine<float>, dim3(T), dim3(256), 0, stream, static_cast<const float*>(Y), ldy,
                            static_cast<const float*>(Yshared), pos, w, K, N, static_cast<float*>(out), ldo);
-    else if (y_f32)
-        hipLaunchKernelGGL((k_combine<float, bf16_t>), dim3(T), dim3(256), 0, stream, static_cast<const float*>(Y), ldy,
-                           static_cast<const float*>(Yshared), pos, w, K, N, static_cast<bf16_t*>(out), ldo);
     else
-        hipLaunchKernelGGL((k_combine<bf16_t, bf16_t>), dim3(T), dim3(256), 0, stream, static_cast<const bf16_t*>(Y), ldy,
+        hipLaunchKernelGGL(k_combine<bf16_t>, dim3(T), dim3(256), 0, stream, static_cast<const bf16_t*>(Y), ldy,
                            static_cast<const bf16_t*>(Yshared), pos, w, K, N, static_cast<bf16_t*>(out), ldo);
     return hipGetLastError();
 }

@@ -210,14 +210,14 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int 
                            hipStream_t stream);
 
 // out[t] = (Yshared ? Yshared[t] : 0) + sum_k w[t,k] * Y[pos[t,k]], over
-// the slots with pos >= 0; y_f32: Y and Yshared in fp32 under a bf16 out.
-// launch_combine_direct: pos[t,k] = t K + k where idx[t,k] is one of e0 ..
-// e0 + E - 1, -1 elsewhere.
-hipError_t launch_combine(DType dt, bool y_f32, const void* Y, int64_t ldy,
+// the slots with pos >= 0.  launch_combine_f32: fp32 Y and Yshared, bf16 out; pos
+// NULL: pos[t,k] = t K + k where idx[t,k] is one of e0 .. e0 + E - 1, -1 elsewhere.
+hipError_t launch_combine(DType dt, const void* Y, int64_t ldy,
                           const void* Yshared, const int32_t* pos,
                           const float* w, int T, int K, int N, void* out,
                           int64_t ldo, hipStream_t stream);
-hipError_t launch_combine_direct(const float* Y, int64_t ldy, const float* Yshared, const int32_t* idx, int e0, int E,
-                                 const float* w, int T, int K, int N, uint16_t* out, int64_t ldo, hipStream_t stream);
+hipError_t launch_combine_f32(const float* Y, int64_t ldy, const float* Yshared, const int32_t* pos,
+                              const int32_t* idx, int e0, int E, const float* w, int T, int K, int N, uint16_t* out,
+                              int64_t ldo, hipStream_t stream);
 
 }  // namespace moe
