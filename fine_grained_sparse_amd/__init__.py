@@ -16,6 +16,7 @@ with SwiGLU experts f(v) = W_down (silu(W_gate v) * (W_up v)).
 """
 import ctypes
 import functools
+import inspect
 import os
 
 import torch
@@ -192,18 +193,23 @@ class _Nothing:
 
 
 def _on_device(fn):
-    """Runs fn(first, ...) with the device of its first tensor current (where
+    """Runs fn with the device of its first argument's tensors current (where
     its launches and default workspaces belong), whatever the caller's is."""
+    first_name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        t = first.get("W_gate") if isinstance(first, dict) else first
+    def call(*args, **kw):
+        t = args[0] if args else kw.get(first_name)
+        if isinstance(t, dict):
+            t = t.get("W_gate")
         if isinstance(t, torch.Tensor) and t.is_cuda:
+            stream = kw.get("stream")
             if stream is not None and stream.device != t.device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
             if t.device.index != torch.cuda.current_device():
                 with torch.cuda.device(t.device):
-                    return fn(first, *args, stream=stream, **kw)
-        return fn(first, *args, stream=stream, **kw)
+                    return fn(*args, **kw)
+        return fn(*args, **kw)
     return call
 
 

@@ -45,6 +45,23 @@ def test_train_library_exports_what_its_header_declares():
         assert hasattr(train.train_lib(), n)
 
 
+def test_entry_points_take_their_first_argument_by_name():
+    # every argument by its name; CPU tensors get as far as the check that refuses them
+    x, W, b = torch.zeros(2, 64), torch.zeros(8, 64), torch.zeros(8)
+    w = {"W_gate": torch.zeros(8, 32, 64), "W_up": torch.zeros(8, 32, 64), "W_down": torch.zeros(8, 64, 32)}
+    idx, tw = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+    for f in (lambda: moe.router(x=x, W_r=W, b=b, K=2),
+              lambda: moe.router_train(x=x, W_r=W, b=b, K=2),
+              lambda: moe.forward(x=x, W_r=W, b=b, weights=w, K=2),
+              lambda: moe.forward_noalloc(x=x, W_r=W, b=b, weights=w, K=2),
+              lambda: moe.forward_slice(x=x, topk_idx=idx, topk_w=tw, weights=w, e0=0, E_total=8),
+              lambda: moe.bias_update(counts=idx[0], b=b),
+              lambda: moe.bias_quantile(x=x, W_r=W, K=2),
+              lambda: moe.balance_loss(logits=b[None], topk_idx=idx[:1], alpha=1.0)):
+        with pytest.raises(ValueError, match="device|GPU|cuda|CUDA"):
+            f()
+
+
 def _bal(S=2, off=FAKE, mask=None, alpha=1e-3):
     return train.Balance(S, off, mask, alpha)
 
