@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(cons
 // rows in turn, their sums meet in LDS in wave order; the counts go out, and
 // the block's share of the loss goes to part_l.  The last block to finish
 // adds the shares up in a fixed order: a launch of its own for that would cost
-// more than this kernel.  Latency-bound: 3.4 us at 128 x 32, 7.8 at 16384 x 384 x
+// more than this kernel.  Latency-bound: 4 us at 128 x 32, 7.8 at 16384 x 384 x
 // 4 sequences, 12.7 at 65521 x 896 x 37 (8 MB of partial rows).
 __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const float* __restrict__ part_p,
                                                         const int32_t* __restrict__ part_c,
@@ -504,7 +504,7 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
 // fragment-block layout of 16 x 32, its rows [hi | hi | lo]: with dz's hi | lo |
 // hi a plain K = 3 Ep product gives the three terms that 16 bits of either
 // side need.  A wave reads 64 columns of eight rows and writes their 16-byte
-// pieces.  27 MB (384 x 7168) in 9 to 10 us.
+// pieces.  27 MB (384 x 7168) in 6 to 7 us.
 __global__ __launch_bounds__(256) void k_pack_wt(const float* __restrict__ W, int E, int64_t d, int Ep,
                                                  bf16_t* __restrict__ dst) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
