@@ -123,6 +123,50 @@ __device__ __forceinline__ int seq_of(const SeqArgs& a, int t) {
 
 constexpr int kMaxE = 1024;
 
+// This wave's share of the sums of p over tokens lo .. hi - 1 of one sequence,
+// kTok tokens at a time for each of the block's NW waves.
+template <int J2, int NW, int kTok>
+__device__ __forceinline__ void score_sums(const SeqArgs& a, const float* __restrict__ z, int lo, int hi, int wid, int lane,
+                                           float (&acc)[2 * J2]) {
+#pragma unroll
+    for (int j = 0; j < 2 * J2; ++j) acc[j] = 0.f;
+    for (int t = lo + wid * kTok; t < hi; t += NW * kTok) {
+        float v[kTok][2 * J2], sum[kTok];
+        bool live[kTok];
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+            const int tu = min(t + u, hi - 1);
+            live[u] = t + u < hi && (!a.mask || a.mask[tu]);
+            load_row<J2>(z + static_cast<int64_t>(tu) * a.E, lane, a.E, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+            sum[u] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) {
+                v[u][j] = in_row<J2>(j, lane, a.E) ? sigm(v[u][j]).s : 0.f;
+                sum[u] += v[u][j];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) {
+            const float inv = live[u] ? 1.f / (wave_sum(sum[u]) + 1e-20f) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * J2; ++j) acc[j] = fmaf(v[u][j], inv, acc[j]);
+        }
+    }
+}
+
+// The selections of each expert by the tokens that count, added to hist.
+template <int NW>
+__device__ __forceinline__ void count_choices(const SeqArgs& a, const int32_t* __restrict__ idx, int lo, int hi, int tid,
+                                              int* hist) {
+    for (int i = tid; i < (hi - lo) * a.K; i += 64 * NW) {
+        const unsigned e = static_cast<unsigned>(idx[static_cast<int64_t>(lo) * a.K + i]);
+        if (e < static_cast<unsigned>(a.E) && (!a.mask || a.mask[lo + i / a.K])) atomicAdd(&hist[e], 1);
+    }
+}
+
 // One block per chunk of 64 tokens.  For every sequence q that the chunk c
 // meets, the sums of p and the counts over their common tokens go to partial
 // row c + q: along the ascending sequences c + q grows with every (chunk,
@@ -157,38 +201,9 @@ __global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(cons
         const int64_t slot = c + q;
         for (int e = tid; e < a.E; e += 64 * NW) hist[e] = 0;
         float acc[2 * J2];
-#pragma unroll
-        for (int j = 0; j < 2 * J2; ++j) acc[j] = 0.f;
-        for (int t = lo + wid * kTok; t < hi; t += NW * kTok) {
-            float v[kTok][2 * J2], sum[kTok];
-            bool live[kTok];
-#pragma unroll
-            for (int u = 0; u < kTok; ++u) {
-                const int tu = min(t + u, hi - 1);
-                live[u] = t + u < hi && (!a.mask || a.mask[tu]);
-                load_row<J2>(z + static_cast<int64_t>(tu) * a.E, lane, a.E, v[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kTok; ++u) {
-                sum[u] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 2 * J2; ++j) {
-                    v[u][j] = in_row<J2>(j, lane, a.E) ? sigm(v[u][j]).s : 0.f;
-                    sum[u] += v[u][j];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kTok; ++u) {
-                const float inv = live[u] ? 1.f / (wave_sum(sum[u]) + 1e-20f) : 0.f;
-#pragma unroll
-                for (int j = 0; j < 2 * J2; ++j) acc[j] = fmaf(v[u][j], inv, acc[j]);
-            }
-        }
+        score_sums<J2, NW, kTok>(a, z, lo, hi, wid, lane, acc);
         __syncthreads();
-        for (int i = tid; i < (hi - lo) * a.K; i += 64 * NW) {
-            const unsigned e = static_cast<unsigned>(idx[static_cast<int64_t>(lo) * a.K + i]);
-            if (e < static_cast<unsigned>(a.E) && (!a.mask || a.mask[lo + i / a.K])) atomicAdd(&hist[e], 1);
-        }
+        count_choices<NW>(a, idx, lo, hi, tid, hist);
 #pragma unroll
         for (int j = 0; j < J2; ++j)
             *reinterpret_cast<float2*>(&sp[wid][j * 128 + lane * 2]) = make_float2(acc[2 * j], acc[2 * j + 1]);
@@ -282,6 +297,62 @@ __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const f
         for (int w = 0; w < 16; ++w) t += sp[0][w];
         *loss = t * (alpha / static_cast<float>(a.S));
     }
+}
+
+// The whole loss of a small batch in one block: no partial rows, no second
+// launch, but 2 us for every 64 tokens and every sequence, in a row.  One block
+// against two launches, replayed from a graph: 6.4 / 8.0 us at 128 x 32 (T x E),
+// 8.1 / 9.3 at 128 x 256, 11.0 / 11.3 at 128 x 512, 10.3 / 14.0 at 64 x 128 in four
+// sequences, but 11.9 / 9.7 at 301 x 48 in two and 20 / 10 at 256 x 32 in eight; a
+// call of the binding takes 3 us less.
+constexpr int kSmallT = 128, kSmallS = 4, kSmallJ2 = 4;  // (J2: its sums fill 32 of the 64 KiB of LDS)
+template <int J2>
+__global__ __launch_bounds__(1024) void k_balance_small(const SeqArgs a, const float* __restrict__ z,
+                                                        const int32_t* __restrict__ idx, float alpha,
+                                                        float* __restrict__ loss, int32_t* __restrict__ seq_counts) {
+    constexpr int NW = 16;
+    __shared__ float sp[NW][J2 * 128], red[NW];
+    __shared__ int hist[J2 * 128], sn;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    float total = 0.f;
+    for (int q = 0; q < a.S; ++q) {
+        const int lo = seq_lo(a, q), hi = seq_hi(a, q);
+        if (tid < a.E) hist[tid] = 0;
+        if (tid == 0) sn = 0;
+        float acc[2 * J2];
+        score_sums<J2, NW, partial_toks(J2)>(a, z, lo, hi, wid, lane, acc);
+#pragma unroll
+        for (int j = 0; j < J2; ++j)
+            *reinterpret_cast<float2*>(&sp[wid][j * 128 + lane * 2]) = make_float2(acc[2 * j], acc[2 * j + 1]);
+        __syncthreads();
+        count_choices<NW>(a, idx, lo, hi, tid, hist);
+        for (int t = lo + wid * 64; t < hi; t += 64 * NW) {
+            const uint64_t live = __ballot(t + lane < hi && (!a.mask || a.mask[t + lane]));
+            if (lane == 0) atomicAdd(&sn, __popcll(live));
+        }
+        __syncthreads();
+        float l = 0.f;
+        if (tid < a.E) {
+            float p = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) p += sp[w][tid];
+            const int cnt = hist[tid];
+            seq_counts[static_cast<int64_t>(q) * a.E + tid] = cnt;
+            l = p * static_cast<float>(cnt);
+        }
+        l = wave_sum(l);
+        if (lane == 0) red[wid] = l;
+        __syncthreads();
+        if (tid == 0) {
+            const int n = sn;
+            const float nf = static_cast<float>(n);
+            float t = 0.f;
+            for (int w = 0; w < NW; ++w) t += red[w];
+            total += n > 0 ? t * (static_cast<float>(a.E) / (static_cast<float>(a.K) * nf) / nf) : 0.f;
+        }
+    }
+    if (tid == 0) *loss = total * (alpha / static_cast<float>(a.S));
 }
 
 // Where k_gate_backward leaves dz as the two products' operands instead.
@@ -846,6 +917,18 @@ hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* 
                                int32_t* part_c, int32_t* part_n, float* part_l, int32_t* ticket, float* loss,
                                int32_t* seq_counts, hipStream_t stream) {
     if (a.T < 1 || a.E < 1 || a.E > kMaxE || a.S < 1 || a.S > 65535) return hipErrorInvalidValue;
+    const int j2 = (a.E + 127) / 128;
+    if (a.T <= kSmallT && a.S <= kSmallS && j2 <= kSmallJ2) {
+#define MOE_CALL(J2) hipLaunchKernelGGL(k_balance_small<J2>, dim3(1), dim3(1024), 0, stream, a, z, idx, alpha, loss, seq_counts)
+        switch (j2) {
+            case 1: MOE_CALL(1); break;
+            case 2: MOE_CALL(2); break;
+            case 3: MOE_CALL(3); break;
+            default: MOE_CALL(4); break;
+        }
+#undef MOE_CALL
+        return hipGetLastError();
+    }
     const dim3 grid((a.T + kChunk - 1) / kChunk);
 #define MOE_CALL(J2) \
     hipLaunchKernelGGL(k_balance_partial<J2>, grid, dim3(64 * partial_waves(J2)), 0, stream, a, z, idx, part_p, part_c, \

@@ -77,25 +77,33 @@ def _launch(dev, stream):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
+# The descriptors (which no call writes) and workspace sizes of the shapes in
+# use: building them anew takes a quarter of a small call's host time.
 @functools.lru_cache(maxsize=256)
-def _balance_bytes(T, E, K, S):
-    nbytes = int(train_lib().moe_balance_workspace_size(ctypes.byref(desc(T=T, d=64, E=E, K=K)), S))
+def _balance_plan(T, E, K, S):
+    D = ctypes.byref(desc(T=T, d=64, E=E, K=K))
+    nbytes = int(train_lib().moe_balance_workspace_size(D, S))
     if nbytes == 0:
         raise MoeError("moe_balance_workspace_size", 2)
-    return nbytes
+    return D, nbytes
 
 
 @functools.lru_cache(maxsize=256)
-def _backward_bytes(T, d, E, K, act_dtype):
-    D = desc(T=T, d=d, E=E, K=K, act_dtype=act_dtype)
-    nbytes = int(train_lib().moe_router_backward_workspace_size(ctypes.byref(D)))
+def _gate_desc(T, E, K, scale):
+    return ctypes.byref(desc(T=T, d=64, E=E, K=K, scale=scale))
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_plan(T, d, E, K, scale, act_dtype):
+    D = ctypes.byref(desc(T=T, d=d, E=E, K=K, scale=scale, act_dtype=act_dtype))
+    nbytes = int(train_lib().moe_router_backward_workspace_size(D))
     if nbytes == 0:
         raise MoeError("moe_router_backward_workspace_size", 2)
-    return nbytes
+    return D, nbytes
 
 
 def _call(name, *args):
-    rc = getattr(train_lib(), name)(*args)
+    rc = getattr(_lib or train_lib(), name)(*args)
     if rc:
         raise MoeError(name, rc)
 
@@ -160,15 +168,14 @@ def balance_loss(logits, topk_idx, alpha, *, seq_offsets=None, token_mask=None, 
     (default: one); token_mask, uint8 or bool [T], is zero for padding."""
     T, E, K, dev = _logits(logits, topk_idx)
     S, B = _balance(T, dev, alpha, seq_offsets, token_mask)
-    D = desc(T=T, d=64, E=E, K=K)
-    nbytes = _balance_bytes(T, E, K, S)
+    D, nbytes = _balance_plan(T, E, K, S)
     s, ctx = _launch(dev, stream)
     with ctx:
         loss = torch.empty((), dtype=torch.float32, device=dev)
         counts = torch.empty((S, E), dtype=torch.int32, device=dev)
         ws = (workspace or _default_ws).get(dev, nbytes, stream)
-        _call("moe_balance_loss", ctypes.byref(D), _ptr(logits), _ptr(topk_idx), ctypes.byref(B), _ptr(loss),
-              _ptr(counts), _ptr(ws), nbytes, s)
+        _call("moe_balance_loss", D, _ptr(logits), _ptr(topk_idx), ctypes.byref(B), _ptr(loss), _ptr(counts), _ptr(ws),
+              nbytes, s)
     return loss, counts
 
 
@@ -202,13 +209,14 @@ def gate_backward(logits, topk_idx, d_topk_w, scale=2.827, *, alpha=None, seq_co
     gradient at the loss, is 1 by default)."""
     T, E, K, dev = _logits(logits, topk_idx)
     B = _grads(T, E, K, dev, d_topk_w, d_loss, alpha, seq_counts, seq_offsets, token_mask)
-    D = desc(T=T, d=64, E=E, K=K, scale=scale)
+    D = _gate_desc(T, E, K, scale)
     s, ctx = _launch(dev, stream)
     with ctx:
         if out is None:
             out = torch.empty((T, E), dtype=torch.float32, device=dev)
-        _need(out, "out", torch.float32, (T, E), dev)
-        _call("moe_gate_backward", ctypes.byref(D), _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
+        else:
+            _need(out, "out", torch.float32, (T, E), dev)
+        _call("moe_gate_backward", D, _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w),
               None if B is None else ctypes.byref(B), _ptr(seq_counts), _ptr(d_loss), _ptr(out), s)
     return out
 
@@ -227,14 +235,13 @@ def router_backward(x, W_r, logits, topk_idx, d_topk_w, scale=2.827, *, alpha=No
     if not (need_dx or need_dW):
         raise ValueError("neither dx nor dW_r is wanted")
     B = _grads(T, E, K, dev, d_topk_w, d_loss, alpha, seq_counts, seq_offsets, token_mask)
-    D = desc(T=T, d=d, E=E, K=K, scale=scale, act_dtype=_DT[x.dtype])
-    nbytes = _backward_bytes(T, d, E, K, _DT[x.dtype])
+    D, nbytes = _backward_plan(T, d, E, K, scale, _DT[x.dtype])
     s, ctx = _launch(dev, stream)
     with ctx:
         dx = torch.empty_like(x) if need_dx else None
         dW = torch.empty((E, d), dtype=torch.float32, device=dev) if need_dW else None
         ws = (workspace or _default_ws).get(dev, nbytes, stream)
-        _call("moe_router_backward", ctypes.byref(D), _ptr(x), _ptr(W_r), _ptr(logits), _ptr(topk_idx),
+        _call("moe_router_backward", D, _ptr(x), _ptr(W_r), _ptr(logits), _ptr(topk_idx),
               _ptr(d_topk_w), None if B is None else ctypes.byref(B), _ptr(seq_counts), _ptr(d_loss), _ptr(dx),
               _ptr(dW), _ptr(ws), nbytes, s)
     return dx, dW

@@ -276,6 +276,17 @@ def test_loss_counts_and_logit_gradient(case):
     assert torch.equal(moe.gate_backward(gz, gi, gw, scale, **kw), both)
 
 
+# on either side of the limits of the loss in one block: 128 tokens, 4 sequences, 512 experts
+EDGES = [(128, 512, 16, 4, 0.2, True), (129, 512, 16, 4, 0.2, True), (128, 512, 16, 5, 0.2, True),
+         (128, 513, 16, 4, 0.2, True), (127, 385, 7, 3, 0.9, False), (2, 511, 3, 4, 0.0, False), (65, 100, 10, 4, 0.5, True)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", EDGES, ids=lambda c: "x".join(map(str, c)))
+def test_loss_of_small_batches(case):
+    test_loss_counts_and_logit_gradient(case)
+
+
 @pytest.mark.gpu
 def test_gradient_against_differences():
     # central differences of the float64 loss along random directions, step h: the truncation is
