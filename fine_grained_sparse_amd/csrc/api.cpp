@@ -216,12 +216,12 @@ Plan make_plan(const moe_layer_desc* D, bool forward, int E_total = 0) {
         p.o_pos = take(p.A * 4);
         p.o_tiles = take(static_cast<int64_t>(p.max_tiles) * sizeof(TileInfo));
         p.o_ntiles = take(8);
-        if (p.dl) p.o_xlat = take(T * p.dl * p.es);
+        if (p.dl) p.o_xlat = take(T * p.dl * p.es * (p.f4 ? 2 : 1));
         p.o_H = take(p.A * p.F * p.es);
         if (p.ns) p.o_Hs = take(T * p.Fsh * p.es);
         const int64_t yrows = p.A + ((p.ns && !p.dl) ? T : 0);
         p.o_Y = take(yrows * p.din * p.ys);
-        if (p.dl) p.o_R = take(T * p.dl * p.es);
+        if (p.dl) p.o_R = take(T * p.dl * p.es * (p.f4 ? 2 : 1));
     }
     p.total = off;
     return p;
@@ -307,13 +307,27 @@ GemmArgs f4_args(GemmArgs g, const uint8_t* bs, const uint8_t* bsu) {
 hipError_t launch_f4(const Plan& p, const GemmArgs& args, const uint8_t* bs, const uint8_t* bsu, Epi epi, int max_n,
                      const int32_t* idx, int e0, hipStream_t s) {
     const GemmArgs g = f4_args(args, bs, bsu);
-    if (p.direct) return launch_fp4_direct(g, epi, idx, p.T, p.K, e0, p.E, s);
-    return launch_gemm_fp4(g, epi, p.bm, p.once, p.max_tiles, max_n, s);
+    const bool two = p.dl && epi == EPI_SWIGLU;
+    if (p.direct) return launch_fp4_direct(g, epi, two, idx, p.T, p.K, e0, p.E, s);
+    return launch_gemm_fp4(g, epi, two, p.bm, p.once, p.max_tiles, max_n, s);
 }
 
-// A dense map of the latent form over the batch.
-hipError_t launch_dense(const Plan& p, const GemmArgs& g, int n, hipStream_t s) {
-    if (p.f4 && p.T <= kDenseRows16T) return launch_dense_rows16(g, s);
+// A dense map of the latent form over the batch.  x_lat and R of FP4 layers
+// are kept in two bf16 parts (a row is its upper parts, then the rest: 16
+// bits), which the next product takes both: one bf16 each would cost as much
+// accuracy as all else in the layer (3.8e-3 against 2.3e-3, norm-wise).
+// two: C is x_lat, and fp32 scratch of its size is at tmp.
+hipError_t launch_dense(const Plan& p, const GemmArgs& g, int n, bool two, float* tmp, hipStream_t s) {
+    if (p.f4 && p.T <= kDenseRows16T) return launch_dense_rows16(g, two ? n : 0, s);
+    if (two) {
+        GemmArgs f = g;
+        f.g[0].C = tmp;
+        f.g[0].ldc = n;
+        const hipError_t err = launch_gemm(f, p.dt, true, EPI_STORE, p.dcfg, static_cast<int>(cdiv(p.T, tile_bm(p.dcfg))),
+                                           n, p.packed, s);
+        if (err != hipSuccess) return err;
+        return launch_two_parts(tmp, p.T, n, static_cast<uint16_t*>(g.g[0].C), s);
+    }
     return launch_gemm(g, p.dt, false, EPI_STORE, p.dcfg, static_cast<int>(cdiv(p.T, tile_bm(p.dcfg))), n, p.packed, s);
 }
 
@@ -323,8 +337,8 @@ hipError_t combine(const Plan& p, const void* Y, const void* ysh, const int32_t*
     if (p.fused) return hipSuccess;  // the down projection did it
     if (p.f4)
         return launch_combine_f32(static_cast<const float*>(Y), N, static_cast<const float*>(ysh),
-                                  p.direct ? nullptr : pos, idx, e0, p.E, w, p.T, p.K, N, static_cast<uint16_t*>(out), N,
-                                  s);
+                                  p.direct ? nullptr : pos, idx, e0, p.E, w, p.T, p.K, N, static_cast<uint16_t*>(out),
+                                  p.dl ? 2 * N : N, p.dl ? N : 0, s);
     return launch_combine(p.dt, Y, N, ysh, pos, w, p.T, p.K, N, out, N, s);
 }
 
@@ -365,9 +379,9 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         g.g[0].nseg = 1;
         g.g[0].N = p.dl;
         g.g[0].C = xlat;
-        g.g[0].ldc = p.dl;
+        g.g[0].ldc = p.f4 ? 2 * p.dl : p.dl;
         g.M = p.T;
-        MOE_HIP(launch_dense(p, g, p.dl, s));
+        MOE_HIP(launch_dense(p, g, p.dl, p.f4, reinterpret_cast<float*>(Y), s));  // (Y comes later)
         xin = xlat;
     }
     MOE_HIP(record(ev, MOE_EV_LATENT, s));
@@ -376,7 +390,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
     {
         GemmArgs g = gemm_args();
         GemmGroup& R0 = g.g[0];
-        R0.seg[0] = GemmSeg{xin, W->W_gate, W->W_up, p.din, p.din, p.din, 0};
+        R0.seg[0] = GemmSeg{xin, W->W_gate, W->W_up, p.f4 && latent ? 2 * p.din : p.din, p.din, p.din, 0};
         R0.nseg = 1;
         R0.N = p.F;
         R0.b_estride = static_cast<int64_t>(p.F) * p.din;
@@ -425,7 +439,7 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
         if (p.fused) {
             g = f4_args(g, W->W_down_scale, nullptr);
             MOE_HIP(launch_fp4_down_combine(g, idx, w, p.T, p.K, e0, p.E, static_cast<uint16_t*>(latent ? R : out),
-                                            p.din, s));
+                                            latent ? 2 * p.din : p.din, latent ? p.din : 0, s));
         } else if (p.f4)
             MOE_HIP(launch_f4(p, g, W->W_down_scale, nullptr, EPI_STORE, p.din, idx, e0, s));
         else if (p.f8)
@@ -446,13 +460,20 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
     GemmGroup& G = g.g[0];
     int ns = 0;
     if (p.ns) G.seg[ns++] = GemmSeg{Hs, W->Ws_down, nullptr, p.Fsh, p.Fsh, p.Fsh, 0};
-    G.seg[ns++] = GemmSeg{R, W->W_lat_up, nullptr, p.dl, p.dl, p.dl, 0};
+    if (p.f4 && p.T <= kDenseRows16T) {
+        G.seg[ns++] = GemmSeg{R, W->W_lat_up, nullptr, 2 * p.dl, p.dl, p.dl, 1};
+    } else if (p.f4) {
+        G.seg[ns++] = GemmSeg{R, W->W_lat_up, nullptr, 2 * p.dl, p.dl, p.dl, 0};
+        G.seg[ns++] = GemmSeg{R + p.dl * p.es, W->W_lat_up, nullptr, 2 * p.dl, p.dl, p.dl, 0};
+    } else {
+        G.seg[ns++] = GemmSeg{R, W->W_lat_up, nullptr, p.dl, p.dl, p.dl, 0};
+    }
     G.nseg = ns;
     G.N = p.d;
     G.C = out;
     G.ldc = p.d;
     g.M = p.T;
-    MOE_HIP(launch_dense(p, g, p.d, s));
+    MOE_HIP(launch_dense(p, g, p.d, false, nullptr, s));
     MOE_HIP(record(ev, MOE_EV_END, s));
     return MOE_OK;
 }

@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64) void k_combine_f32(const float* __restrict__ Y,
                                                     const float* __restrict__ Ysh, const int32_t* __restrict__ pos,
                                                     const int32_t* __restrict__ idx, int e0, int E,
                                                     const float* __restrict__ w, int K, int N,
-                                                    bf16_t* __restrict__ out, int64_t ldo) {
+                                                    bf16_t* __restrict__ out, int64_t ldo, int64_t lo) {
     typedef float f4 __attribute__((ext_vector_type(4)));
     const int64_t t = blockIdx.x;
     const int c = (blockIdx.y * 64 + threadIdx.x) * 4;
@@ -310,24 +310,32 @@ __global__ __launch_bounds__(64) void k_combine_f32(const float* __restrict__ Y,
     for (int k = 0; k < KM; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = fmaf(wk[k], v[k][i], s[i]);
-    *reinterpret_cast<uint2*>(out + t * ldo + c) =
-        make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
-                   f32_to_bf16(s[2]) | (static_cast<uint32_t>(f32_to_bf16(s[3])) << 16));
+    auto store = [&](int64_t at) {
+        *reinterpret_cast<uint2*>(out + t * ldo + c + at) =
+            make_uint2(f32_to_bf16(s[0]) | (static_cast<uint32_t>(f32_to_bf16(s[1])) << 16),
+                       f32_to_bf16(s[2]) | (static_cast<uint32_t>(f32_to_bf16(s[3])) << 16));
+    };
+    store(0);
+    if (lo) {  // the second part: what the first leaves
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] -= bf16_to_f32(f32_to_bf16(s[i]));
+        store(lo);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_combine_f32(const float* Y, int64_t ldy, const float* Yshared, const int32_t* pos,
                               const int32_t* idx, int e0, int E, const float* w, int T, int K, int N, uint16_t* out,
-                              int64_t ldo, hipStream_t stream) {
+                              int64_t ldo, int64_t lo, hipStream_t stream) {
     if (T < 1 || K < 1 || K > 16 || N % 4 || (N / 4 + 63) / 64 > 65535) return hipErrorInvalidValue;
     const dim3 grid(T, (N / 4 + 63) / 64);
     if (K <= 8)
         hipLaunchKernelGGL(k_combine_f32<8>, grid, dim3(64), 0, stream, Y, ldy, Yshared, pos, idx, e0, E, w, K, N, out,
-                           ldo);
+                           ldo, lo);
     else
         hipLaunchKernelGGL(k_combine_f32<16>, grid, dim3(64), 0, stream, Y, ldy, Yshared, pos, idx, e0, E, w, K, N, out,
-                           ldo);
+                           ldo, lo);
     return hipGetLastError();
 }
 

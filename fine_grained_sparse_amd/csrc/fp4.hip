@@ -55,50 +55,69 @@ __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// v as two bf16 parts, hi at p and the rest at p + lo (16 of v's bits; lo 0: hi alone).
+__device__ __forceinline__ void store_parts(bf16_t* p, int64_t lo, const float (&v)[4]) {
+    store4(p, v);
+    if (!lo) return;
+    float r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = v[i] - bf16_to_f32(f32_to_bf16(v[i]));
+    store4(p + lo, r);
+}
+
 // ---- few rows: weights streamed once, K split over the waves of a workgroup
 
 // acc[j] += (row block j of the weights) * (activation rows), over the
 // 128-column blocks k0, k0 + step, .. < kend.  w[j] / sc[j]: this lane's place
 // in block 0 of row block j; x: this lane's row at column 32 (lane / 16).
 // Everything comes straight from memory to the registers of the one wave that
-// uses it, the next block's loads in flight while a block is used.
+// uses it, the next block's loads in flight while a block is used.  TWO: the
+// activations come in two parts, the second xlo bytes behind the first, and
+// every weight meets both.
 // D blocks are in flight.  D = 1 leaves the registers for more waves, which
 // then hide each other's latency: better where a wave has few blocks.
-template <int RB>
+template <int RB, bool TWO>
 struct Fp4Load {
-    uint4 q[RB], x[4];
+    uint4 q[RB], x[TWO ? 8 : 4];
     uint32_t e[RB];
 };
-template <int RB, int D>
+template <int RB, int D, bool TWO = false>
 __device__ __forceinline__ void fp4_stream(f32x4 (&acc)[RB], const char* const (&w)[RB], const uint8_t* const (&sc)[RB],
-                                           const char* x, int k0, int step, int kend) {
+                                           const char* x, int k0, int step, int kend, int64_t xlo = 0) {
     if (k0 >= kend) return;
-    auto load = [&](Fp4Load<RB>& l, int k) {
+    auto load = [&](Fp4Load<RB, TWO>& l, int k) {
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
             l.q[j] = ldg16_once(w[j] + static_cast<int64_t>(k) * 1024);
             l.e[j] = sc[j][k * 64];
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) l.x[s] = ldg16(x + static_cast<int64_t>(k) * 256 + s * 16);
+        for (int s = 0; s < 4; ++s) {
+            l.x[s] = ldg16(x + static_cast<int64_t>(k) * 256 + s * 16);
+            if constexpr (TWO) l.x[4 + s] = ldg16(x + xlo + static_cast<int64_t>(k) * 256 + s * 16);
+        }
     };
-    auto use = [&](const Fp4Load<RB>& l) {
+    auto use = [&](const Fp4Load<RB, TWO>& l) {
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
             const float scale = __uint_as_float(l.e[j] << 23);
             const uint32_t c[4] = {l.q[j].x, l.q[j].y, l.q[j].z, l.q[j].w};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) acc[j] = Mfma<bf16_t>::run(fp4x8_to_bf16(c[s], scale), l.x[s], acc[j]);
+            for (int s = 0; s < 4; ++s) {
+                const uint4 f = fp4x8_to_bf16(c[s], scale);
+                acc[j] = Mfma<bf16_t>::run(f, l.x[s], acc[j]);
+                if constexpr (TWO) acc[j] = Mfma<bf16_t>::run(f, l.x[4 + s], acc[j]);
+            }
         }
     };
     if constexpr (D == 1) {
         for (int k = k0; k < kend; k += step) {
-            Fp4Load<RB> l;
+            Fp4Load<RB, TWO> l;
             load(l, k);
             use(l);
         }
     } else {
-        Fp4Load<RB> l[D];
+        Fp4Load<RB, TWO> l[D];
 #pragma unroll
         for (int u = 0; u < D; ++u)
             if (k0 + u * step < kend) load(l[u], k0 + u * step);
@@ -116,16 +135,17 @@ __device__ __forceinline__ void fp4_stream(f32x4 (&acc)[RB], const char* const (
 }
 // The same for packed bf16 weights, over 32-column blocks, U in flight; x at column
 // 8 (lane / 16).
-template <int RB, int U>
+template <int RB, int U, bool TWO = false>
 __device__ __forceinline__ void bf16_stream(f32x4 (&acc)[RB], const char* const (&w)[RB], const char* x, int k0, int step,
-                                            int kend) {
+                                            int kend, int64_t xlo = 0) {
     if (k0 >= kend) return;
-    uint4 q[U][RB], xv[U];
+    uint4 q[U][RB], xv[U], xl[TWO ? U : 1];
     auto load = [&](int u, int k) {
         if (k >= kend) return;  // (uniform)
 #pragma unroll
         for (int j = 0; j < RB; ++j) q[u][j] = ldg16_once(w[j] + static_cast<int64_t>(k) * 1024);
         xv[u] = ldg16(x + static_cast<int64_t>(k) * 64);
+        if constexpr (TWO) xl[u] = ldg16(x + xlo + static_cast<int64_t>(k) * 64);
     };
 #pragma unroll
     for (int u = 0; u < U; ++u) load(u, k0 + u * step);
@@ -135,7 +155,10 @@ __device__ __forceinline__ void bf16_stream(f32x4 (&acc)[RB], const char* const 
             __builtin_amdgcn_sched_barrier(0);
             if (k + u * step < kend) {
 #pragma unroll
-                for (int j = 0; j < RB; ++j) acc[j] = Mfma<bf16_t>::run(q[u][j], xv[u], acc[j]);
+                for (int j = 0; j < RB; ++j) {
+                    acc[j] = Mfma<bf16_t>::run(q[u][j], xv[u], acc[j]);
+                    if constexpr (TWO) acc[j] = Mfma<bf16_t>::run(q[u][j], xl[u], acc[j]);
+                }
                 load(u, k + (U + u) * step);
             }
         }
@@ -197,7 +220,8 @@ __device__ __forceinline__ int direct_rows(const DirectArgs& d, int a, int* rows
 // 6.0 to 6.5 TB/s, where a large copy reaches 4.7; 256 tokens over 48 experts
 // up 115 to 128 us and down 67 to 70 for 0.75 and 0.37 GB, 5.3 to 6.5 TB/s; one
 // token's up, 184 MB, 30 us.
-template <typename TC, int EPI, int NW, int D, bool DIRECT>
+// TWO: the routed experts' activation rows hold two parts, K columns each.
+template <typename TC, int EPI, int NW, int D, bool DIRECT, bool TWO>
 __global__ __launch_bounds__(64 * NW) void k_fp4_rows16(const GemmArgs a, const DirectArgs dir) {
     constexpr int BM = 16, RB = 4, NJ = EPI == EPI_SWIGLU ? RB / 2 : RB, BNO = 16 * NJ;
     __shared__ f32x4 red[NW][RB][64];
@@ -258,7 +282,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp4_rows16(const GemmArgs a, const 
             w[j] = static_cast<const char*>(up ? G.seg[0].Bu : G.seg[0].B) + eb + blk * 1024 + lane * 16;
             sc[j] = (up ? G.bsu : G.bs) + es + blk * 64 + lane;
         }
-        fp4_stream<RB, D>(acc, w, sc, x + grp * 64, wid, NW, kb);
+        fp4_stream<RB, D, TWO>(acc, w, sc, x + grp * 64, wid, NW, kb, K * 2);
     } else {
         constexpr int RS = DIRECT ? RB / 2 : RB, NS = EPI == EPI_SWIGLU ? RS / 2 : RS;
         const char* w[RS];
@@ -302,10 +326,10 @@ __global__ __launch_bounds__(64 * NW) void k_fp4_rows16(const GemmArgs a, const 
 }
 
 // Dense maps of a few rows (the latent form's): C = A B^T over up to two K
-// segments of packed bf16, 16 rows x 32 columns per workgroup, K split over
-// the waves as above.
+// segments of packed bf16 (their rows of A in one or two parts), 16 rows x 32 columns per workgroup, K split over
+// the waves as above.  lo: C is written in two parts, that far apart.
 constexpr int kDenseNW = 8;
-__global__ __launch_bounds__(64 * kDenseNW) void k_dense_rows16(const GemmArgs a) {
+__global__ __launch_bounds__(64 * kDenseNW) void k_dense_rows16(const GemmArgs a, int64_t lo) {
     constexpr int RB = 2;
     __shared__ f32x4 red[kDenseNW][RB][64];
     const GemmGroup& G = a.g[0];
@@ -323,7 +347,11 @@ __global__ __launch_bounds__(64 * kDenseNW) void k_dense_rows16(const GemmArgs a
 #pragma unroll
         for (int j = 0; j < RB; ++j)
             w[j] = static_cast<const char*>(S.B) + static_cast<int64_t>(min(n0 / 16 + j, G.N / 16 - 1)) * kb * 1024 + lane * 16;
-        bf16_stream<RB, 4>(acc, w, static_cast<const char*>(S.A) + row * S.lda * 2 + grp * 16, wid, kDenseNW, kb);
+        const char* x = static_cast<const char*>(S.A) + row * S.lda * 2 + grp * 16;
+        if (S.two)
+            bf16_stream<RB, 4, true>(acc, w, x, wid, kDenseNW, kb, S.K * 2);
+        else
+            bf16_stream<RB, 4>(acc, w, x, wid, kDenseNW, kb);
     }
 #pragma unroll
     for (int j = 0; j < RB; ++j) red[wid][j][lane] = acc[j];
@@ -335,7 +363,7 @@ __global__ __launch_bounds__(64 * kDenseNW) void k_dense_rows16(const GemmArgs a
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += red[w][wid][lane][j];
     const int col = n0 + wid * 16 + grp * 4;
-    if (row0 + r16 < a.M && col < G.N) store4(static_cast<bf16_t*>(G.C) + row * G.ldc + col, v);
+    if (row0 + r16 < a.M && col < G.N) store_parts(static_cast<bf16_t*>(G.C) + row * G.ldc + col, lo, v);
 }
 
 // Down projection and combine of a single token in one: block (n, t) forms
@@ -350,7 +378,7 @@ __global__ __launch_bounds__(64 * kDenseNW) void k_dense_rows16(const GemmArgs a
 constexpr int kFusedNW = 8;
 __global__ __launch_bounds__(64 * kFusedNW) void k_fp4_down_combine(const GemmArgs a, const DirectArgs d,
                                                                    const float* __restrict__ wt,
-                                                                   bf16_t* __restrict__ out, int64_t ldo) {
+                                                                   bf16_t* __restrict__ out, int64_t ldo, int64_t lo) {
     __shared__ f32x4 red[kFusedNW][64];
     const int lane = threadIdx.x & 63, grp = lane >> 4;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -389,7 +417,7 @@ __global__ __launch_bounds__(64 * kFusedNW) void k_fp4_down_combine(const GemmAr
     for (int w = 0; w < kFusedNW; ++w)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += red[w][lane][j];
-    store4(out + t * ldo + n * 16 + grp * 4, v);
+    store_parts(out + t * ldo + n * 16 + grp * 4, lo, v);
 }
 
 // Many rows: BM = 16 MT activation rows x 256 weight rows per workgroup
@@ -400,11 +428,13 @@ __global__ __launch_bounds__(64 * kFusedNW) void k_fp4_down_combine(const GemmAr
 // straight to its registers.  A code is converted once and used by MT MFMAs.
 // LDS row r keeps its 16-byte chunk c at c ^ (r % 16), so the 16 rows that a
 // fragment read touches at one chunk lie in 16 different bank groups.
+// TWO (rows of two parts, K columns each): every K block takes two stages, one
+// for either part, and its weights come through the caches twice.
 // Measured, 2048 tokens over 48 of 384 experts of 7168 x 2048 and a shared one
 // (43 rows an expert): up 296 to 322 us, down 168 to 182 us, 361 GFLOP together
 // at 0.72 to 0.78 PFLOP/s (a large bf16 product of the library: 1.37) while
 // 1.2 GB stream past.
-template <typename TC, int EPI, int MT, bool ONCE>
+template <typename TC, int EPI, int MT, bool ONCE, bool TWO>
 struct Fp4Tile {
     static constexpr int BM = 16 * MT, RB = 4, NJ = EPI == EPI_SWIGLU ? RB / 2 : RB;
     static constexpr int BNO = 4 * 16 * NJ;            // output columns per workgroup
@@ -416,7 +446,8 @@ struct Fp4Tile {
         const int tid = threadIdx.x, lane = tid & 63;
         const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int r16 = lane & 15, grp = lane >> 4;
-        const int K = G.seg[0].K, nst = (K + 127) / 128;
+        const int K = G.seg[0].K, kb = (K + 127) / 128;
+        const int two = TWO && jb.gi == 0 ? 1 : 0, nst = kb << two;  // stage st: K block st >> two, part st & two
 
         // this thread's pieces of a stage: row (tid / 16) + 16 i, chunk tid % 16
         const char* xs[XL];
@@ -431,7 +462,8 @@ struct Fp4Tile {
         const int wpos = (tid >> 4) * 256 + ((chunk ^ (tid >> 4)) << 4);
         uint4 xr[2][XL];
         auto load_x = [&](int st, int i) {
-            const int off = min(st * 256 + chunk * 16, K * 2 - 16);  // (past the end; the last stage may hold 64 columns)
+            int off = min((st >> two) * 256 + chunk * 16, K * 2 - 16);  // (past the end; the last stage may hold 64 columns)
+            if (TWO) off += (st & two) * K * 2;
             return ldg16(xs[i] + off);
         };
         auto write_x = [&](int st, int i, const uint4& v) {
@@ -492,13 +524,13 @@ struct Fp4Tile {
             for (int j = 0; j < RB; ++j) {
                 const bool up = EPI == EPI_SWIGLU && j >= NJ;
                 w[j] = static_cast<const char*>(up ? G.seg[0].Bu : G.seg[0].B) + eb +
-                       static_cast<int64_t>(rb[j]) * nst * 1024 + lane * 16;
-                sc[j] = (up ? G.bsu : G.bs) + es + static_cast<int64_t>(rb[j]) * nst * 64 + lane;
+                       static_cast<int64_t>(rb[j]) * kb * 1024 + lane * 16;
+                sc[j] = (up ? G.bsu : G.bs) + es + static_cast<int64_t>(rb[j]) * kb * 64 + lane;
             }
             uint4 q[2][RB];
             uint32_t e[2][RB];
             auto load_w = [&](int st, int j, uint4& o, uint32_t& oe) {
-                const int k = min(st, nst - 1);
+                const int k = min(st, nst - 1) >> two;
                 o = ONCE ? ldg16_once(w[j] + static_cast<int64_t>(k) * 1024) : ldg16(w[j] + static_cast<int64_t>(k) * 1024);
                 oe = sc[j][k * 64];
             };
@@ -595,9 +627,9 @@ struct Fp4Tile {
 
 // A tile with fewer rows (an expert's last) runs the body of the next quarter
 // of BM.
-template <typename TC, int EPI, int MT, bool ONCE>
+template <typename TC, int EPI, int MT, bool ONCE, bool TWO>
 __global__ __launch_bounds__(256, 2) void k_fp4_tile(const GemmArgs a) {
-    using Tile = Fp4Tile<TC, EPI, MT, ONCE>;
+    using Tile = Fp4Tile<TC, EPI, MT, ONCE, TWO>;
     __shared__ __attribute__((aligned(1024))) char lds[2 * Tile::STAGE];
     Job jb;
     // (48 experts of 7168 x 2048 and a shared one, shared pairs first or last:
@@ -605,11 +637,11 @@ __global__ __launch_bounds__(256, 2) void k_fp4_tile(const GemmArgs a) {
     // 536 / 513 at 2048, where they would fill every CU)
     if (!pick_job<Tile::BM, Tile::BNO>(a, jb, 256)) return;
     if (jb.rows <= Tile::BM / 4)
-        Fp4Tile<TC, EPI, MT / 4, ONCE>::run(a, jb, lds);
+        Fp4Tile<TC, EPI, MT / 4, ONCE, TWO>::run(a, jb, lds);
     else if (jb.rows <= Tile::BM / 2)
-        Fp4Tile<TC, EPI, MT / 2, ONCE>::run(a, jb, lds);
+        Fp4Tile<TC, EPI, MT / 2, ONCE, TWO>::run(a, jb, lds);
     else if (jb.rows <= Tile::BM / 4 * 3)
-        Fp4Tile<TC, EPI, MT / 4 * 3, ONCE>::run(a, jb, lds);
+        Fp4Tile<TC, EPI, MT / 4 * 3, ONCE, TWO>::run(a, jb, lds);
     else
         Tile::run(a, jb, lds);
 }
@@ -632,7 +664,18 @@ __global__ __launch_bounds__(256) void k_pack_fp4(const uint4* __restrict__ src,
     }
 }
 
-template <typename TC, int EPI>
+// fp32 [rows, n] -> bf16 [rows, 2 n]: a row's upper parts, then what they leave.
+__global__ __launch_bounds__(256) void k_two_parts(const float4* __restrict__ src, int64_t pieces, int n,
+                                                   bf16_t* __restrict__ dst) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const float4 f = src[i];
+        const float v[4] = {f.x, f.y, f.z, f.w};
+        const int64_t r = i / (n / 4), c = i % (n / 4) * 4;
+        store_parts(dst + r * 2 * n + c, n, v);
+    }
+}
+
+template <typename TC, int EPI, bool TWO>
 hipError_t launch_t(const GemmArgs& args, int bm, bool once, int max_tiles, int max_n, hipStream_t stream) {
     const int bno = (bm == 16 ? 64 : 256) / (EPI == EPI_SWIGLU ? 2 : 1);
     GemmArgs a = args;
@@ -640,18 +683,19 @@ hipError_t launch_t(const GemmArgs& args, int bm, bool once, int max_tiles, int 
     if (static_cast<int64_t>(max_tiles) * a.ntn >= (int64_t{1} << 31) - 64) return hipErrorInvalidValue;
     const dim3 grid(job_blocks(max_tiles, a.ntn));
     if (bm == 16)
-        hipLaunchKernelGGL((k_fp4_rows16<TC, EPI, 4, 1, false>), grid, dim3(256), 0, stream, a, DirectArgs{});
-    else if (once)
-        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4, true>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_fp4_rows16<TC, EPI, 4, 1, false, TWO>), grid, dim3(256), 0, stream, a, DirectArgs{});
+    else if (once && !TWO)
+        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4, !TWO, TWO>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4, false>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_fp4_tile<TC, EPI, 4, false, TWO>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
 // One K segment per group; the routed matrices in whole 16 x 128 blocks, the
 // shared ones in whole 16 x 32 blocks and 64-column steps.
-bool fp4_fits(const GemmArgs& a, Epi epi) {
+bool fp4_fits(const GemmArgs& a, Epi epi, bool two) {
     const GemmGroup &R = a.g[0], &S = a.g[1];
+    if (two && (epi != EPI_SWIGLU || R.seg[0].lda < 2ll * R.seg[0].K)) return false;
     return a.nsplit == 1 && R.nseg == 1 && R.N > 0 && R.N % 16 == 0 && R.seg[0].K > 0 && R.seg[0].K % 128 == 0 && R.bs &&
            (epi != EPI_SWIGLU || R.bsu) && (!S.N || (S.nseg == 1 && S.N % 16 == 0 && S.seg[0].K % 64 == 0));
 }
@@ -673,48 +717,63 @@ int fp4_bm(int64_t rows, int E, int F, bool shared) {
     return rows < (few ? 16 : shared ? 4 : 8) * static_cast<int64_t>(E) ? 16 : 64;
 }
 
-hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, bool once, int max_tiles, int max_n, hipStream_t stream) {
+hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, bool two, int bm, bool once, int max_tiles, int max_n,
+                           hipStream_t stream) {
     if (max_tiles <= 0 || max_n <= 0) return hipSuccess;
-    if ((bm != 16 && bm != 64) || !args.tiles || !fp4_fits(args, epi)) return hipErrorInvalidValue;
-    if (epi == EPI_SWIGLU) return launch_t<bf16_t, EPI_SWIGLU>(args, bm, once, max_tiles, max_n, stream);
-    return launch_t<float, EPI_STORE>(args, bm, once, max_tiles, max_n, stream);
+    if ((bm != 16 && bm != 64) || !args.tiles || !fp4_fits(args, epi, two)) return hipErrorInvalidValue;
+    if (two) return launch_t<bf16_t, EPI_SWIGLU, true>(args, bm, once, max_tiles, max_n, stream);
+    if (epi == EPI_SWIGLU) return launch_t<bf16_t, EPI_SWIGLU, false>(args, bm, once, max_tiles, max_n, stream);
+    return launch_t<float, EPI_STORE, false>(args, bm, once, max_tiles, max_n, stream);
 }
 
 bool fp4_direct(int64_t T) { return T <= kDirectT; }
 bool fp4_fused(int64_t T) { return T == 1; }
 
-hipError_t launch_fp4_direct(const GemmArgs& args, Epi epi, const int32_t* idx, int T, int K, int e0, int E,
+hipError_t launch_fp4_direct(const GemmArgs& args, Epi epi, bool two, const int32_t* idx, int T, int K, int e0, int E,
                              hipStream_t stream) {
-    if (T < 1 || T > kDirectT || K < 1 || K > kDirectA / kDirectT || !fp4_fits(args, epi)) return hipErrorInvalidValue;
+    if (T < 1 || T > kDirectT || K < 1 || K > kDirectA / kDirectT || !fp4_fits(args, epi, two)) return hipErrorInvalidValue;
     const int bno = epi == EPI_SWIGLU ? 32 : 64;
     GemmArgs a = args;
     a.ntn = (a.g[0].N + bno - 1) / bno;
     const int nsh = a.g[1].N ? (a.g[1].N + bno / 2 - 1) / (bno / 2) : 0;
     const DirectArgs d{idx, T * K, K, e0, E, nsh, epi == EPI_SWIGLU ? 0 : 1};
     const dim3 grid(static_cast<unsigned>(nsh + T * K * a.ntn));
-    if (epi == EPI_SWIGLU)
-        hipLaunchKernelGGL((k_fp4_rows16<bf16_t, EPI_SWIGLU, 8, 2, true>), grid, dim3(512), 0, stream, a, d);
+    // (two parts: one block of K in flight leaves two workgroups to a CU; two in
+    // flight took 99 us against 96 at 8 tokens, 132 / 128 at 16, 50 / 52 at one)
+    if (two)
+        hipLaunchKernelGGL((k_fp4_rows16<bf16_t, EPI_SWIGLU, 8, 1, true, true>), grid, dim3(512), 0, stream, a, d);
+    else if (epi == EPI_SWIGLU)
+        hipLaunchKernelGGL((k_fp4_rows16<bf16_t, EPI_SWIGLU, 8, 2, true, false>), grid, dim3(512), 0, stream, a, d);
     else
-        hipLaunchKernelGGL((k_fp4_rows16<float, EPI_STORE, 4, 1, true>), grid, dim3(256), 0, stream, a, d);
+        hipLaunchKernelGGL((k_fp4_rows16<float, EPI_STORE, 4, 1, true, false>), grid, dim3(256), 0, stream, a, d);
     return hipGetLastError();
 }
 
 hipError_t launch_fp4_down_combine(const GemmArgs& args, const int32_t* idx, const float* w, int T, int K, int e0, int E,
-                                   uint16_t* out, int64_t ldo, hipStream_t stream) {
-    if (T < 1 || K < 1 || !fp4_fits(args, EPI_STORE) || (args.g[1].N && args.g[1].N != args.g[0].N))
+                                   uint16_t* out, int64_t ldo, int64_t lo, hipStream_t stream) {
+    if (T < 1 || K < 1 || !fp4_fits(args, EPI_STORE, false) || (args.g[1].N && args.g[1].N != args.g[0].N))
         return hipErrorInvalidValue;
     const DirectArgs d{idx, T * K, K, e0, E, 0, 1};
     hipLaunchKernelGGL(k_fp4_down_combine, dim3(args.g[0].N / 16, T), dim3(64 * kFusedNW), 0, stream, args, d, w, out,
-                       ldo);
+                       ldo, lo);
     return hipGetLastError();
 }
 
-hipError_t launch_dense_rows16(const GemmArgs& a, hipStream_t stream) {
+hipError_t launch_dense_rows16(const GemmArgs& a, int64_t lo, hipStream_t stream) {
     const GemmGroup& G = a.g[0];
     if (a.nsplit != 1 || a.M < 1 || G.nseg < 1 || G.nseg > 2 || G.N < 16 || G.N % 16) return hipErrorInvalidValue;
     for (int i = 0; i < G.nseg; ++i)
-        if (G.seg[i].K < 32 || G.seg[i].K % 32) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_dense_rows16, dim3((G.N + 31) / 32, (a.M + 15) / 16), dim3(64 * kDenseNW), 0, stream, a);
+        if (G.seg[i].K < 32 || G.seg[i].K % 32 || (G.seg[i].two && G.seg[i].lda < 2ll * G.seg[i].K))
+            return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_dense_rows16, dim3((G.N + 31) / 32, (a.M + 15) / 16), dim3(64 * kDenseNW), 0, stream, a, lo);
+    return hipGetLastError();
+}
+
+hipError_t launch_two_parts(const float* src, int64_t rows, int n, uint16_t* dst, hipStream_t stream) {
+    if (rows < 1 || n < 4 || n % 4) return hipErrorInvalidValue;
+    const int64_t pieces = rows * (n / 4), blocks = (pieces + 255) / 256;
+    hipLaunchKernelGGL(k_two_parts, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream,
+                       reinterpret_cast<const float4*>(src), pieces, n, dst);
     return hipGetLastError();
 }
 

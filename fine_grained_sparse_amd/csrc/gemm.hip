@@ -1233,10 +1233,7 @@ hipError_t launch_gemm(const GemmArgs& args, DType dt, bool out_f32, Epi epi, Ti
         if (epi == EPI_SWIGLU) return launch_t<float, float, EPI_SWIGLU>(args, cfg, max_tiles, max_n, packed, stream);
         return launch_t<float, float, EPI_STORE>(args, cfg, max_tiles, max_n, packed, stream);
     }
-    if (out_f32) {
-        if (packed) return hipErrorInvalidValue;  // fp32 output: the router, on row-major planes
-        return launch_t<bf16_t, float, EPI_STORE>(args, cfg, max_tiles, max_n, false, stream);
-    }
+    if (out_f32) return launch_t<bf16_t, float, EPI_STORE>(args, cfg, max_tiles, max_n, packed, stream);
     if (epi == EPI_SWIGLU) return launch_t<bf16_t, bf16_t, EPI_SWIGLU>(args, cfg, max_tiles, max_n, packed, stream);
     return launch_t<bf16_t, bf16_t, EPI_STORE>(args, cfg, max_tiles, max_n, packed, stream);
 }

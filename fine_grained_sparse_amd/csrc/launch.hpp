@@ -32,7 +32,7 @@ struct GemmSeg {
     const void* Bu;
     int64_t lda, ldb;
     int32_t K;
-    int32_t pad_;
+    int32_t two;  // launch_dense_rows16: a row of A holds two parts of K columns, whose sum B meets
 };
 
 // A family of tiles sharing operands: the routed experts (B offset by
@@ -127,29 +127,37 @@ hipError_t launch_pack_frag16_fp8(const uint8_t* src, uint8_t* dst, int64_t coun
                                   hipStream_t stream);
 
 // The projections with 4-bit routed experts (fp4.hip): C = epi(A * B^T) over
-// a tile table of bm rows per tile (fp4_bm; once: most experts fill one tile at most, so their weights are read once), bf16 A; C bf16 for the SwiGLU,
-// fp32 for the plain store.  Group 0: E2M1 codes (b_estride in bytes) with
+// a tile table of bm rows per tile (fp4_bm; once: most experts fill one tile at
+// most, so their weights are read once), bf16 A; C bf16 for the SwiGLU, fp32
+// for the plain store.  two (SwiGLU): group 0's rows of A hold two parts of K
+// columns each, whose sum the weights meet.  Group 0: E2M1 codes (b_estride in bytes) with
 // E8M0 scales bs / bsu per 32 columns (s_estride in bytes), both in 16 x 128
 // blocks; group 1: packed bf16.  One K segment each.
-hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, int bm, bool once, int max_tiles, int max_n, hipStream_t stream);
+hipError_t launch_gemm_fp4(const GemmArgs& args, Epi epi, bool two, int bm, bool once, int max_tiles, int max_n,
+                           hipStream_t stream);
 // rows per tile for this many routed rows over E experts of width F
 int fp4_bm(int64_t rows, int E, int F, bool shared);
 // The same without a tile table, for batches that fp4_direct() takes: rows of
 // C are assignments a = t K + k (group 1: tokens), whose experts the kernel
 // finds in idx (ids outside e0 .. e0 + E - 1: their rows are not written).
 bool fp4_direct(int64_t T);
-hipError_t launch_fp4_direct(const GemmArgs& args, Epi epi, const int32_t* idx, int T, int K, int e0, int E,
+hipError_t launch_fp4_direct(const GemmArgs& args, Epi epi, bool two, const int32_t* idx, int T, int K, int e0, int E,
                              hipStream_t stream);
 // The down projection (group 0: H rows by assignment, group 1: the shared
 // experts) and the combine in one launch, for the batches of fp4_fused():
-// out[t] = shared + sum_k w[t,k] W_down[idx[t,k] - e0] H[t K + k].
+// out[t] = shared + sum_k w[t,k] W_down[idx[t,k] - e0] H[t K + k], in two
+// bf16 parts, lo elements apart, if lo is not 0.
 bool fp4_fused(int64_t T);
 hipError_t launch_fp4_down_combine(const GemmArgs& args, const int32_t* idx, const float* w, int T, int K, int e0, int E,
-                                   uint16_t* out, int64_t ldo, hipStream_t stream);
+                                   uint16_t* out, int64_t ldo, int64_t lo, hipStream_t stream);
 
-// C = A B^T for a few rows: bf16 A and C, packed bf16 B, one or two K segments
-// (group 0, no tile table).
-hipError_t launch_dense_rows16(const GemmArgs& args, hipStream_t stream);
+// C = A B^T for a few rows: bf16 A and C (two parts, lo elements apart, if lo
+// is not 0), packed bf16 B, one or two K segments (group 0, no tile table).
+hipError_t launch_dense_rows16(const GemmArgs& args, int64_t lo, hipStream_t stream);
+
+// fp32 [rows, n] -> two bf16 parts [rows, 2 n]: row r's upper parts at 2 n r, what
+// they leave at 2 n r + n.
+hipError_t launch_two_parts(const float* src, int64_t rows, int n, uint16_t* dst, hipStream_t stream);
 
 // Row-major E2M1 codes [rows, cols / 2] and scales [rows, cols / 32] (count
 // matrices each, consecutive) -> 16 x 128 blocks: lane l of a block holds the
@@ -210,7 +218,8 @@ hipError_t launch_dispatch(const int32_t* idx, int T, int E, int e0, int K, int 
                            hipStream_t stream);
 
 // out[t] = (Yshared ? Yshared[t] : 0) + sum_k w[t,k] * Y[pos[t,k]], over
-// the slots with pos >= 0.  launch_combine_f32: fp32 Y and Yshared, bf16 out; pos
+// the slots with pos >= 0.  launch_combine_f32: fp32 Y and Yshared, bf16 out (two
+// parts, lo elements apart, if lo is not 0); pos
 // NULL: pos[t,k] = t K + k where idx[t,k] is one of e0 .. e0 + E - 1, -1 elsewhere.
 hipError_t launch_combine(DType dt, const void* Y, int64_t ldy,
                           const void* Yshared, const int32_t* pos,
@@ -218,6 +227,6 @@ hipError_t launch_combine(DType dt, const void* Y, int64_t ldy,
                           int64_t ldo, hipStream_t stream);
 hipError_t launch_combine_f32(const float* Y, int64_t ldy, const float* Yshared, const int32_t* pos,
                               const int32_t* idx, int e0, int E, const float* w, int T, int K, int N, uint16_t* out,
-                              int64_t ldo, hipStream_t stream);
+                              int64_t ldo, int64_t lo, hipStream_t stream);
 
 }  // namespace moe

@@ -148,7 +148,8 @@ typedef enum { MOE_LAYOUT_ROWS = 0, MOE_LAYOUT_FRAG16 = 1 } moe_weight_layout;
  * aligned like the matrices and repacked with them, so that element (r, c)
  * is code(r, c) * 2^(s[r][c/32] - 127), exact in bf16 in the same range and
  * under the same limit.  The experts' outputs are then kept in fp32 until
- * the combine (H and x_lat are rounded to bf16).                            */
+ * the combine, x_lat and the latent sum R in two bf16 parts (16 bits); H is
+ * rounded to bf16.                                                          */
 typedef struct {
     const void *W_gate, *W_up, *W_down;
     const void *Ws_gate, *Ws_up, *Ws_down;

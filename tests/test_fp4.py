@@ -228,6 +228,24 @@ def test_random_slices(seed):
     _check(f"random {seed}", out, *_reference(x, idx, wt, w, e0))
 
 
+# (T, d, ns): one kernel for down and combine, direct, tables with 16-row tiles, dense maps by the GEMM tiles, 64-row tiles
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,ns", [(1, 448, 0), (9, 448, 0), (60, 448, 1), (130, 320, 0), (200, 448, 1), (530, 448, 0),
+                                    (600, 448, 2)])
+def test_latent_roundings(T, d, ns):
+    # Of the latent form's values only H and the output are rounded to bf16; x_lat and R keep 16 bits.  With random
+    # signs each rounding of at most u relative is at most u / sqrt(3) rms, so two of them give u sqrt(2 / 3); x_lat and
+    # R in bf16 would add more than as much again (x_lat enters H through both of its factors).
+    _log(f"[gpu] fp4 latent roundings T={T} d={d} ns={ns}")
+    x, idx, wt, w = _layer(31, T, d, 6, 6, 3, 256, ns, 64 if ns else 0, 640)
+    out = _run(x, idx, wt, w, 0, 6, ns)
+    torch.cuda.synchronize()
+    ref, tol = _reference(x, idx, wt, w, 0)
+    _check(f"latent {T}", out, ref, tol)
+    rel = ((out.double() - ref).norm() / ref.norm()).item()
+    assert rel <= U * (2 / 3) ** 0.5, rel
+
+
 @pytest.mark.gpu
 def test_pack_is_the_documented_permutation():
     _, _, _, w = _layer(3, 1, 384, 3, 3, 1, 256, 1, 128, 0)
