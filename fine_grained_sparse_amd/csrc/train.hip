@@ -228,8 +228,8 @@ __global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(cons
 // rows in turn, their sums meet in LDS in wave order; the counts go out, and
 // the block's share of the loss goes to part_l.  The last block to finish
 // adds the shares up in a fixed order: a launch of its own for that would cost
-// more than this kernel.  Latency-bound: 4 us at 128 x 32, 7.8 at 16384 x 384 x
-// 4 sequences, 12.7 at 65521 x 896 x 37 (8 MB of partial rows).
+// more than this kernel.  Latency-bound: 7.8 us at 16384 x 384 x 4
+// sequences, 12.7 at 65521 x 896 x 37 (8 MB of partial rows).
 __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const float* __restrict__ part_p,
                                                         const int32_t* __restrict__ part_c,
                                                         const int32_t* __restrict__ part_n, float alpha,
