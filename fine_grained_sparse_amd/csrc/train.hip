@@ -355,6 +355,86 @@ __global__ __launch_bounds__(1024) void k_balance_small(const SeqArgs a, const f
     if (tid == 0) *loss = total * (alpha / static_cast<float>(a.S));
 }
 
+// n_q, for the gradient: the number of tokens of a sequence that count, and not
+// that of its choices over K, as a token may hold ids that no count has.
+// Without a mask it is the sequence's length; with one its bytes are counted:
+// by each block of the gradient for the sequences of its own tokens, or, for
+// many tokens, once by k_seq_tokens, which leaves n_q (as float) at q's first
+// token and at the first token of each of the gradient's waves.  The gradient
+// unmasked / counting in its blocks / with k_seq_tokens, in us: 15 / 16.6 / 20 at
+// 16384 x 384 in four sequences, 98 / 116 / 110 at 65521 x 896 in 37 and
+// 104 / 136 / 111 in one, 328 / 2327 / 435 at 1048576 x 128 (of which k_seq_tokens 50).
+constexpr int kSeqTokensT = 32768;
+
+// This wave's share (of its block's NW) of the tokens that count among lo ..
+// hi - 1: the mask in whole 16-byte pieces, single bytes at both ends.
+template <int NW>
+__device__ __forceinline__ int live_share(const uint8_t* mask, int lo, int hi, int tid) {
+    const int p0 = lo / 16 + (lo % 16 != 0), p1 = hi / 16;  // pieces that lie inside
+    int n = 0;
+    if (p0 < p1) {
+#pragma unroll 4
+        for (int p = p0 + tid; p < p1; p += 64 * NW) {
+            const uint4 v = *reinterpret_cast<const uint4*>(mask + static_cast<int64_t>(p) * 16);
+            const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // the bytes that are not zero
+                n += __popc((d[i] | ((d[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u);
+        }
+        if (tid < 16) {
+            if (lo + tid < p0 * 16) n += mask[lo + tid] != 0;
+            if (p1 * 16 + tid < hi) n += mask[p1 * 16 + tid] != 0;
+        }
+    } else if (lo + tid < hi) {  // (30 tokens at most)
+        n = mask[lo + tid] != 0;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) n += __shfl_xor(n, o);
+    return n;
+}
+
+// One block per 1024 tokens, a token per thread.  The part of a sequence that
+// lies in the block comes from a running count of the block's mask bytes, what
+// the first and the last token's sequences hold outside of it from reading
+// that.  Latency: 6 us at 65521 tokens (six steps of the search, two reads).
+__global__ __launch_bounds__(1024) void k_seq_tokens(const SeqArgs a, int tok, float* __restrict__ n_tok, int64_t stride) {
+    __shared__ int upto[1025], wave_n[16], outer[2], ends[4];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const int b0 = blockIdx.x * 1024, b1 = min(a.T, b0 + 1024), t = b0 + tid;
+    const uint64_t live = __ballot(t < b1 && a.mask[t < b1 ? t : b0]);
+    int l = 0, h = a.S;  // the first sequence that ends after t
+    while (l < h) {
+        const int m = (l + h) >> 1;
+        if (seq_hi(a, m) > t)
+            h = m;
+        else
+            l = m + 1;
+    }
+    int lo = 0, hi = 0;  // t's sequence (none: 0, 0)
+    if (t < b1 && l < a.S && seq_lo(a, l) <= t) {
+        lo = seq_lo(a, l);
+        hi = seq_hi(a, l);
+    }
+    if (lane == 0) wave_n[wid] = __popcll(live);
+    if (tid < 2) outer[tid] = 0;
+    if (tid == 0) ends[0] = lo, ends[1] = hi;
+    if (t == b1 - 1) ends[2] = lo, ends[3] = hi;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < wid; ++w) before += wave_n[w];
+    upto[tid] = before + __popcll(live & ((1ull << lane) - 1));
+    if (tid == 1023) upto[1024] = before + __popcll(live);
+    const int lo0 = ends[0], hi0 = ends[1], lo1 = ends[2], hi1 = ends[3];
+    int n = live_share<16>(a.mask, lo0, min(hi0, b0), tid);
+    if (lane == 0) atomicAdd(&outer[0], n);
+    n = live_share<16>(a.mask, b1, max(hi1, b1), tid);
+    if (lane == 0) atomicAdd(&outer[1], n);
+    __syncthreads();
+    if (lo >= hi || (t % tok && t != lo)) return;  // (a wave of the gradient asks for no other)
+    n = upto[min(hi, b1) - b0] - upto[max(lo, b0) - b0] + (lo < b0 ? outer[0] : 0) + (hi > b1 ? outer[1] : 0);
+    n_tok[t * stride] = static_cast<float>(n);
+}
+
 // Where k_gate_backward leaves dz as the two products' operands instead.
 struct PlaneArgs {
     float *rows32, *cols32;  // (small products) dz as [T][Es] and as [Es][Ts], zero past E and T
@@ -372,7 +452,8 @@ enum GateOut { GATE_ROWS = 0, GATE_SMALL = 1, GATE_PLANES = 2 };
 // A wave takes a few consecutive tokens.  The gate term touches only the K
 // chosen experts of each: lane 16 u + k computes token u's slot k, and the
 // values reach the lanes that own the experts through a row in LDS that is
-// zero between tokens.  Bound by its one reading of z and writing of dz: 470 MB
+// zero between tokens.  n_tok may lie in dz: a wave reads it at its own tokens,
+// before it writes them.  Bound by its one reading of z and writing of dz: 470 MB
 // (65521 x 896) in 95 us, 4.9 TB/s, a large copy's rate here.  (Rows whose
 // every lane asked whether its pair lies inside took 146 us, those with four
 // tokens in hand at 14 pairs a lane 225: 193 registers, two waves per SIMD.)
@@ -380,14 +461,27 @@ template <int J2, int OUT>
 __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const float* __restrict__ z,
                                                        const int32_t* __restrict__ idx, const float* __restrict__ dw,
                                                        float scale, const int32_t* __restrict__ counts, float alpha,
-                                                       const float* __restrict__ d_loss, float* __restrict__ dz,
-                                                       const PlaneArgs pl) {
+                                                       const float* __restrict__ d_loss, float* dz,
+                                                       const PlaneArgs pl, const float* n_tok, int64_t n_stride) {
     constexpr int kTok = toks(J2);
     __shared__ float rows[4][J2 * 128];
+    __shared__ int n_at[4 * kTok];  // n_q, at the first of the block's tokens that is in q
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float* row = rows[wid];
-    const int t0 = (blockIdx.x * 4 + wid) * kTok;
+    const int b0 = blockIdx.x * 4 * kTok, t0 = b0 + wid * kTok;
+    if (counts && a.mask && !n_tok) {
+        const int b1 = min(a.T, b0 + 4 * kTok);
+        if (threadIdx.x < 4 * kTok) n_at[threadIdx.x] = 0;
+        __syncthreads();
+        for (int q = b0 < b1 ? seq_of(a, b0) : a.S; q < a.S && seq_lo(a, q) < b1; ++q) {
+            const int lo = seq_lo(a, q), hi = seq_hi(a, q);
+            if (lo >= hi) continue;
+            const int n = live_share<4>(a.mask, lo, hi, threadIdx.x);
+            if (lane == 0) atomicAdd(&n_at[max(lo, b0) - b0], n);
+        }
+        __syncthreads();
+    }
     if (OUT == GATE_ROWS && t0 >= a.T) return;
 
     bool live[kTok];
@@ -424,6 +518,7 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
         for (int j = 0; j < 2 * J2; ++j) d[u][j] = 0.f;
     if (counts && t0 < a.T) {
         float s[kTok][2 * J2], inv[kTok];
+        const float n_first = n_tok ? n_tok[t0 * n_stride] : 0.f;
 #pragma unroll
         for (int u = 0; u < kTok; ++u) load_row<J2>(z + static_cast<int64_t>(min(t0 + u, a.T - 1)) * a.E, lane, a.E, s[u]);
 #pragma unroll
@@ -445,14 +540,12 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
             const int qlo = seq_lo(a, q), qhi = seq_hi(a, q);
             if (qlo >= qhi) continue;
             const int32_t* cr = counts + static_cast<int64_t>(q) * a.E;
-            float co[2 * J2], total = 0.f;  // a_q of this lane's experts
+            float co[2 * J2];  // a_q of this lane's experts
 #pragma unroll
-            for (int j = 0; j < 2 * J2; ++j) {
+            for (int j = 0; j < 2 * J2; ++j)
                 co[j] = in_row<J2>(j, lane, a.E) ? static_cast<float>(cr[(j >> 1) * 128 + lane * 2 + (j & 1)]) : 0.f;
-                total += co[j];
-            }
-            // K n_q is the sum of the counts
-            const float n = wave_sum(total) / static_cast<float>(a.K);
+            const float n = n_tok ? (qlo <= t0 ? n_first : n_tok[qlo * n_stride])
+                                  : static_cast<float>(a.mask ? n_at[max(qlo, b0) - b0] : qhi - qlo);
             const float g = alpha * (d_loss ? *d_loss : 1.f) / static_cast<float>(a.S);
             const float f = n > 0.f ? g * (static_cast<float>(a.E) / (static_cast<float>(a.K) * n) / n) : 0.f;
 #pragma unroll
@@ -945,13 +1038,19 @@ hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* 
 template <int OUT>
 static hipError_t launch_gate(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
                               const int32_t* counts, float alpha, const float* d_loss, float* dz, const PlaneArgs& pl,
-                              int64_t tokens, hipStream_t stream) {
+                              int64_t tokens, float* n_tok, int64_t n_stride, hipStream_t stream) {
     if (a.T < 1 || a.E < 1 || a.E > kMaxE || a.K > 16) return hipErrorInvalidValue;
-    const int per = 4 * toks((a.E + 127) / 128);
+    const int tok = toks((a.E + 127) / 128), per = 4 * tok;
+    if (!counts || !a.mask || a.T <= kSeqTokensT) n_tok = nullptr;
+    if (n_tok) {
+        hipLaunchKernelGGL(k_seq_tokens, dim3((a.T + 1023) / 1024), dim3(1024), 0, stream, a, tok, n_tok, n_stride);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
     const dim3 grid(static_cast<unsigned>((tokens + per - 1) / per));
 #define MOE_CALL(J2)                                                                                                  \
     hipLaunchKernelGGL((k_gate_backward<J2, OUT>), grid, dim3(256), 0, stream, a, z, idx, dw, scale, counts, alpha, \
-                       d_loss, dz, pl)
+                       d_loss, dz, pl, n_tok, n_stride)
     MOE_FOR_E(a.E, MOE_CALL);
 #undef MOE_CALL
     return hipGetLastError();
@@ -960,7 +1059,11 @@ static hipError_t launch_gate(const SeqArgs& a, const float* z, const int32_t* i
 hipError_t launch_gate_backward(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
                                 const int32_t* counts, float alpha, const float* d_loss, float* dz,
                                 hipStream_t stream) {
-    return launch_gate<GATE_ROWS>(a, z, idx, dw, scale, counts, alpha, d_loss, dz, PlaneArgs{}, a.T, stream);
+    // dz itself takes n_q at each token's first logit, unless z may be the same memory
+    const uintptr_t o = reinterpret_cast<uintptr_t>(dz), i = reinterpret_cast<uintptr_t>(z);
+    const uintptr_t bytes = static_cast<uintptr_t>(a.T) * a.E * 4;
+    float* n_tok = o < i + bytes && i < o + bytes ? nullptr : dz;
+    return launch_gate<GATE_ROWS>(a, z, idx, dw, scale, counts, alpha, d_loss, dz, PlaneArgs{}, a.T, n_tok, a.E, stream);
 }
 
 hipError_t launch_gate_backward_small(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
@@ -971,12 +1074,12 @@ hipError_t launch_gate_backward_small(const SeqArgs& a, const float* z, const in
     pl.cols32 = cols;
     pl.Es = (a.E + 15) / 16 * 16;
     pl.Ts = (a.T + 15) / 16 * 16;
-    return launch_gate<GATE_SMALL>(a, z, idx, dw, scale, counts, alpha, d_loss, nullptr, pl, pl.Ts, stream);
+    return launch_gate<GATE_SMALL>(a, z, idx, dw, scale, counts, alpha, d_loss, nullptr, pl, pl.Ts, nullptr, 0, stream);
 }
 
 hipError_t launch_gate_backward_planes(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
                                        const int32_t* counts, float alpha, const float* d_loss, uint16_t* rows, int Ep,
-                                       uint16_t* cols, uint16_t* live, hipStream_t stream) {
+                                       uint16_t* cols, uint16_t* live, float* n_tok, hipStream_t stream) {
     if (Ep % 64 || Ep < a.E || Ep >= a.E + 64) return hipErrorInvalidValue;
     PlaneArgs pl{};
     pl.rows = rows;
@@ -986,7 +1089,7 @@ hipError_t launch_gate_backward_planes(const SeqArgs& a, const float* z, const i
     pl.Eb = (a.E + 15) / 16;
     pl.Tb = dw_slabs(a.T);
     return launch_gate<GATE_PLANES>(a, z, idx, dw, scale, counts, alpha, d_loss, nullptr, pl,
-                                    static_cast<int64_t>(pl.Tb) * 32, stream);
+                                    static_cast<int64_t>(pl.Tb) * 32, n_tok, 1, stream);
 }
 
 hipError_t launch_pack_wt(const float* W, int E, int64_t d, int Ep, uint16_t* dst, hipStream_t stream) {

@@ -46,11 +46,11 @@ hipError_t launch_gate_backward_small(const SeqArgs& a, const float* z, const in
 // cols (nullable): its parts hi, mid, lo with hi + mid + lo == dz in
 // [dw_slabs(T)][3][ceil(E/16)] blocks of 1 KiB (16 experts x 32 tokens, element
 // (r, c) at ((c / 8) 16 + r) 8 + c % 8), zero past E and T; with it live
-// [32 dw_slabs(T)]: 0xffff for the tokens that count, else 0.
+// [32 dw_slabs(T)]: 0xffff for the tokens that count, else 0.  n_tok: scratch of T floats.
 int dw_slabs(int T);
 hipError_t launch_gate_backward_planes(const SeqArgs& a, const float* z, const int32_t* idx, const float* dw, float scale,
                                        const int32_t* counts, float alpha, const float* d_loss, uint16_t* rows, int Ep,
-                                       uint16_t* cols, uint16_t* live, hipStream_t stream);
+                                       uint16_t* cols, uint16_t* live, float* n_tok, hipStream_t stream);
 
 // W_r [E, d] -> W_r^T [d, 3 Ep] = [hi | hi | lo] in the fragment-block layout.
 hipError_t launch_pack_wt(const float* W, int E, int64_t d, int Ep, uint16_t* dst, hipStream_t stream);

@@ -86,7 +86,7 @@ struct BackPlan {
     TileCfg xcfg;
     DwPlan dw;       // bf16
     int nsplit;      // planes of dW_r
-    int64_t o_dz, o_rows, o_wt, o_cols, o_live, o_xt, o_part, total;
+    int64_t o_dz, o_rows, o_wt, o_cols, o_live, o_ntok, o_xt, o_part, total;
 };
 BackPlan back_plan(const moe_layer_desc* D) {
     BackPlan p{};
@@ -107,6 +107,7 @@ BackPlan back_plan(const moe_layer_desc* D) {
         p.o_wt = ar.take(d * 3 * p.Ep * 2);
         p.o_cols = ar.take(3 * cdiv(E, 16) * dw_slabs(D->T) * 1024);
         p.o_live = ar.take(static_cast<int64_t>(dw_slabs(D->T)) * 64);
+        p.o_ntok = ar.take(T * 4);
         p.o_part = ar.take(p.nsplit > 1 ? p.nsplit * E * d * 4 : 1);
     } else {
         p.xcfg = TILE_SMALL;
@@ -242,7 +243,7 @@ moe_status moe_router_backward(const moe_layer_desc* desc, const void* x, const 
         uint16_t* cols = dW_r ? at<uint16_t>(workspace, p.o_cols) : nullptr;
         const int Ep = static_cast<int>(p.Ep);
         MOE_HIP(launch_gate_backward_planes(sa, logits, topk_idx, d_topk_w, desc->scale, seq_counts, alpha, d_loss, rows,
-                                            Ep, cols, at<uint16_t>(workspace, p.o_live), s));
+                                            Ep, cols, at<uint16_t>(workspace, p.o_live), at<float>(workspace, p.o_ntok), s));
         if (dx) {
             uint16_t* wt = at<uint16_t>(workspace, p.o_wt);
             MOE_HIP(launch_pack_wt(W_r, desc->E, d, Ep, wt, s));

@@ -68,7 +68,8 @@ moe_status moe_router_train(const moe_layer_desc *desc, const void *x,
 
 /* The balance loss.  Uses T, E and K of the descriptor.
  *   logits [T, E] fp32, topk_idx [T, K] int32 (distinct ids 0 .. E - 1 in a
- *   token; other ids are counted nowhere, and an id twice counts twice)
+ *   token; other ids are counted nowhere, and an id twice counts twice; n_q
+ *   counts tokens, whatever their ids)
  *   -> loss [1] fp32, seq_counts [S, E] int32 (c_qi; their sum over q is a
  *   load that moe_bias_update takes).
  * Workspace of at least moe_balance_workspace_size(desc, S) bytes (0: an
@@ -86,7 +87,7 @@ moe_status moe_balance_loss(const moe_layer_desc *desc, const float *logits,
  *   balance given then still masks tokens); d_loss [1] fp32: the gradient at
  *   the loss, NULL for 1.
  *   At least one of d_topk_w and seq_counts is given.
- *   -> d_logits [T, E] fp32.                                                 */
+ *   -> d_logits [T, E] fp32, which may be the logits' own memory.            */
 moe_status moe_gate_backward(const moe_layer_desc *desc, const float *logits,
                              const int32_t *topk_idx, const float *d_topk_w,
                              const moe_balance *balance,

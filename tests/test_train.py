@@ -653,3 +653,89 @@ def test_two_streams_at_once():
         for x, y in zip(alone, both):
             for u, v in zip(x, y):
                 assert torch.equal(u, v)
+
+
+def _foreign(seed, T, E, K, S, masked, outside, share):
+    """_make with a share of the slots holding ids that no expert has, and a sequence with no others."""
+    z, idx, dw, off, mask = _make(seed, T, E, K, S, masked, outside)
+    r = np.random.default_rng(seed + 1)
+    bad = r.choice(np.array([-1, E, E + 7, 1 << 30, -(1 << 31)], dtype=np.int64), idx.shape).astype(np.int32)
+    idx = np.where(r.random(idx.shape) < share, bad, idx).astype(np.int32)
+    if S > 2:
+        idx[off[1]:off[2]] = -1
+    return z, idx, dw, off, mask
+
+
+def _balance64(z, idx, off, mask, alpha):
+    """The balance loss, its counts, its gradient at the logits and that one's tolerance, in float64 from the definition:
+    n_q are the tokens that count, whatever ids they hold."""
+    T, E = z.shape
+    K, S = idx.shape[1], len(off) - 1
+    Z, I = torch.from_numpy(z).double(), torch.from_numpy(idx).long()
+    s = torch.sigmoid(Z)
+    tot = s.sum(1, keepdim=True) + 1e-20
+    live = torch.ones(T, dtype=torch.bool) if mask is None else torch.from_numpy(mask) != 0
+    loss, counts = 0.0, torch.zeros(S, E, dtype=torch.int32)
+    dz, tol = torch.zeros_like(Z), torch.zeros_like(Z)
+    for q in range(S):
+        t = torch.arange(int(off[q]), int(off[q + 1]))
+        t = t[live[t]]
+        if not len(t):
+            continue
+        ids = I[t].flatten()
+        counts[q] = torch.bincount(ids[(ids >= 0) & (ids < E)], minlength=E).int()
+        a = alpha / S * E * counts[q].double() / (K * len(t) ** 2)
+        p = s[t] / tot[t]
+        loss += (p @ a).sum().item()
+        mean = (p @ a)[:, None]
+        sc = s[t] * torch.sigmoid(-Z[t]) / tot[t]
+        dz[t], tol[t] = sc * (a - mean), 128 * E32 * sc * (a + mean)
+    return loss, counts, dz, tol + 1e-38
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,K,S,masked,outside,share", [
+    (1, 8, 2, 1, 0.0, False, 0.6), (9, 33, 4, 1, 0.4, False, 0.5), (100, 64, 5, 3, 0.0, True, 0.5),
+    (128, 512, 16, 4, 0.3, False, 0.25), (129, 70, 3, 5, 0.3, True, 1.0), (700, 385, 8, 30, 0.2, False, 0.1),
+    (3001, 1024, 16, 7, 0.1, True, 0.5), (5000, 96, 6, 1, 0.5, False, 0.3), (32768, 20, 3, 40, 0.2, True, 0.5),
+    (32769, 20, 3, 40, 0.2, True, 0.5), (40000, 20, 3, 3, 0.05, True, 0.5), (50001, 129, 4, 5000, 0.3, False, 0.3),
+    (70000, 12, 2, 60000, 0.3, True, 0.1), (200000, 600, 5, 1, 0.01, True, 0.9)])
+def test_foreign_ids_leave_loss_and_gradient_one(T, E, K, S, masked, outside, share):
+    _log(f"[gpu] foreign ids T={T} E={E} K={K} S={S} masked={masked} share={share}")
+    z, idx, dw, off, mask = _foreign(71, T, E, K, S, masked, outside, share)
+    loss, counts, dz, tol = _balance64(z, idx, off, mask, 0.4)
+    gz, gi, _, go, gm = _dev(z, idx, dw, off, mask)
+    l, c = moe.balance_loss(gz, gi, 0.4, seq_offsets=go, token_mask=gm)
+    d = moe.gate_backward(gz, gi, None, alpha=0.4, seq_counts=c, seq_offsets=go, token_mask=gm)
+    torch.cuda.synchronize()
+    assert torch.equal(c.cpu(), counts)
+    assert abs(l.item() - loss) <= (160 + T / 256) * E32 * abs(loss)
+    assert ((d.cpu().double() - dz).abs() <= tol).all()
+    same = moe.gate_backward(gz, gi, None, alpha=0.4, seq_counts=c, seq_offsets=go, token_mask=gm, out=gz)
+    assert same is gz and torch.equal(same, d)   # (in place: a token's row needs no other's)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,E,dt", [(50, 128, 40, "bf16"), (50, 128, 40, "f32"), (1500, 256, 100, "bf16"),
+                                      (1500, 256, 100, "f32"), (33001, 64, 40, "bf16"), (33001, 64, 40, "f32")])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+def test_foreign_ids_in_the_router_backward(T, d, E, dt, masked):
+    # dx and dW_r are the products of gate_backward's dz, whichever route they take
+    z, idx, dw, off, mask = _foreign(73, T, E, 4, 3, masked, True, 0.5)
+    loss, counts, dz, tz = _balance64(z, idx, off, mask, 0.4)
+    r = np.random.default_rng(3)
+    x = torch.from_numpy(r.normal(0, 1, (T, d)).astype(np.float32))
+    x = x.bfloat16() if dt == "bf16" else x
+    W = torch.from_numpy((r.normal(0, 1, (E, d)) / d ** 0.5).astype(np.float32))
+    gz, gi, _, go, gm = _dev(z, idx, dw, off, mask)
+    dx, dW = moe.router_backward(x.to(DEV), W.to(DEV), gz, gi, None, alpha=0.4, seq_counts=counts.to(DEV),
+                                 seq_offsets=go, token_mask=gm)
+    torch.cuda.synchronize()
+    X, Wd, a = x.double(), W.double(), dz.abs()
+    # the bounds of test_router_backward
+    ref, refw = dz @ Wd, dz.T @ X
+    tol = (a @ Wd.abs()) * ((3 * 2.0 ** -16 if dt == "bf16" else 0.0) + 3 * (E + 64) * E32) + tz @ Wd.abs()
+    tol = tol + (U if dt == "bf16" else E32) * (ref.abs() + tol) + 1e-38
+    tolw = (a.T @ X.abs()) * 3 * (T + 64) * E32 + tz.T @ X.abs() + 1e-38
+    assert ((dx.cpu().double() - ref).abs() <= tol).all()
+    assert ((dW.cpu().double() - refw).abs() <= tolw).all()
