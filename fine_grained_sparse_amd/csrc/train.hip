@@ -452,13 +452,14 @@ enum GateOut { GATE_ROWS = 0, GATE_SMALL = 1, GATE_PLANES = 2 };
 // A wave takes a few consecutive tokens.  The gate term touches only the K
 // chosen experts of each: lane 16 u + k computes token u's slot k, and the
 // values reach the lanes that own the experts through a row in LDS that is
-// zero between tokens.  n_tok may lie in dz: a wave reads it at its own tokens,
-// before it writes them.  Bound by its one reading of z and writing of dz: 470 MB
-// (65521 x 896) in 95 us, 4.9 TB/s, a large copy's rate here.  (Rows whose
-// every lane asked whether its pair lies inside took 146 us, those with four
-// tokens in hand at 14 pairs a lane 225: 193 registers, two waves per SIMD.)
+// zero between tokens.  dz may be z's memory, and n_tok lie in dz: a wave reads
+// both at its own tokens only, before it writes them.  Bound by its one reading
+// of z and writing of dz: 470 MB (65521 x 896) in 95 us, 4.9 TB/s, a large
+// copy's rate here.  (Rows whose every lane asked whether its pair lies inside
+// took 146 us, those with four tokens in hand at 14 pairs a lane 225: 193
+// registers, two waves per SIMD.)
 template <int J2, int OUT>
-__global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const float* __restrict__ z,
+__global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const float* z,
                                                        const int32_t* __restrict__ idx, const float* __restrict__ dw,
                                                        float scale, const int32_t* __restrict__ counts, float alpha,
                                                        const float* __restrict__ d_loss, float* dz,
