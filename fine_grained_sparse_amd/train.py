@@ -209,7 +209,7 @@ def gate_backward(logits, topk_idx, d_topk_w, scale=2.827, *, alpha=None, seq_co
     gradient at the loss, is 1 by default)."""
     T, E, K, dev = _logits(logits, topk_idx)
     B = _grads(T, E, K, dev, d_topk_w, d_loss, alpha, seq_counts, seq_offsets, token_mask)
-    D = _gate_desc(T, E, K, scale)
+    D = _gate_desc(T, E, K, float(scale))  # (a tensor would be kept by what it is, not by its value)
     s, ctx = _launch(dev, stream)
     with ctx:
         if out is None:
@@ -235,7 +235,7 @@ def router_backward(x, W_r, logits, topk_idx, d_topk_w, scale=2.827, *, alpha=No
     if not (need_dx or need_dW):
         raise ValueError("neither dx nor dW_r is wanted")
     B = _grads(T, E, K, dev, d_topk_w, d_loss, alpha, seq_counts, seq_offsets, token_mask)
-    D, nbytes = _backward_plan(T, d, E, K, scale, _DT[x.dtype])
+    D, nbytes = _backward_plan(T, d, E, K, float(scale), _DT[x.dtype])
     s, ctx = _launch(dev, stream)
     with ctx:
         dx = torch.empty_like(x) if need_dx else None

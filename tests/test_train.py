@@ -739,3 +739,17 @@ def test_foreign_ids_in_the_router_backward(T, d, E, dt, masked):
     tolw = (a.T @ X.abs()) * 3 * (T + 64) * E32 + tz.T @ X.abs() + 1e-38
     assert ((dx.cpu().double() - ref).abs() <= tol).all()
     assert ((dW.cpu().double() - refw).abs() <= tolw).all()
+
+
+@pytest.mark.gpu
+def test_scale_is_read_anew_each_call():
+    # a scale that is a tensor or an array and changes between two calls of one shape
+    z, idx, dw, off, mask = _make(81, 30, 12, 3, 1)
+    gz, gi, gw = _dev(z, idx, dw)
+    x, W = torch.randn(30, 64, device=DEV), torch.randn(12, 64, device=DEV)
+    for s in (torch.tensor(2.0), np.array(2.0, dtype=np.float32)):
+        for v in (2.0, 0.5):
+            s[...] = v
+            assert torch.equal(moe.gate_backward(gz, gi, gw, s), moe.gate_backward(gz, gi, gw, v))
+            for a, b in zip(moe.router_backward(x, W, gz, gi, gw, s), moe.router_backward(x, W, gz, gi, gw, v)):
+                assert torch.equal(a, b)
