@@ -505,10 +505,11 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
         const Sigm s = sigm(ok ? z[static_cast<int64_t>(t) * a.E + e] : 0.f);
         const float g = ok ? dw[i] : 0.f, sc = ok ? s.s : 0.f;
         const float den = row16_sum(sc) + 1e-20f;
-        // g - mean in two passes: with few or alike g the first mean leaves only
-        // its rounding error, which the second removes (K = 1 has no gradient)
-        const float dev = g - row16_sum(g * sc) / den;
-        gv = scale / den * (dev - row16_sum(ok ? dev * sc : 0.f) / den) * (s.s * s.c);
+        // g - mean in two passes: with few or alike g the first mean leaves little
+        // but its rounding error, which the second removes.  sum dev s is mean 1e-20
+        // without one (den holds 1e-20 more than the scores), not 0.
+        const float mean = row16_sum(g * sc) / den, dev = g - mean;
+        gv = scale / den * (dev - (row16_sum(ok ? dev * sc : 0.f) - mean * 1e-20f) / den) * (s.s * s.c);
         ge = ok ? e : -1;
     }
 

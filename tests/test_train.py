@@ -753,3 +753,28 @@ def test_scale_is_read_anew_each_call():
             assert torch.equal(moe.gate_backward(gz, gi, gw, s), moe.gate_backward(gz, gi, gw, v))
             for a, b in zip(moe.router_backward(x, W, gz, gi, gw, s), moe.router_backward(x, W, gz, gi, gw, v)):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [1, 2, 3, 8, 16])
+def test_gate_gradient_where_the_guard_counts(K):
+    # chosen scores about as small as the 1e-20 of D: dw_k - sum_j dw_j s_j / D is then dw's own size even for equal
+    # dw or K = 1.  The bound is the module's gate term, with D as the formula has it
+    T, E, scale = 400, 40, 2.827
+    r = np.random.default_rng(91)
+    z = (r.uniform(-50, -36, (T, 1)) + r.uniform(-1, 1, (T, E))).astype(np.float32)
+    z[::5] = r.uniform(-80, -30, (T // 5, E))
+    idx = np.argsort(r.random((T, E)), axis=1)[:, :K].astype(np.int32)
+    dw = r.normal(0, 1, (T, K)).astype(np.float32)
+    dw[1::3] = 0.75
+    gz, gi, gw = _dev(z, idx, dw)
+    got = moe.gate_backward(gz, gi, gw, scale).cpu().double()
+    Z, I, g = torch.from_numpy(z).double(), torch.from_numpy(idx).long(), torch.from_numpy(dw).double()
+    s = torch.sigmoid(Z).gather(1, I)
+    sc = s * torch.sigmoid(-Z).gather(1, I)
+    D = s.sum(1, keepdim=True) + 1e-20
+    ref = torch.zeros_like(Z).scatter_(1, I, scale / D * (g - (g * s).sum(1, keepdim=True) / D) * sc)
+    tol = torch.zeros_like(Z).scatter_(1, I, scale / D * (g.abs() + (g.abs() * s).sum(1, keepdim=True) / D) * sc)
+    worst = ((got - ref).abs() / (128 * E32 * tol + 1e-36)).max().item()
+    _log(f"[gpu] guard K={K}: worst element {worst:.3f} of the tolerance")
+    assert worst <= 1.0
