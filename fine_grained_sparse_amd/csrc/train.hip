@@ -18,13 +18,14 @@ namespace {
 // sigmoid with the hardware exp2 and reciprocal: e = exp(-z) = 2^p 2^r with
 // p = -z log2(e) rounded and r its rounding error, so that e carries about
 // one ulp at any z.  Returns s and 1 - s = e s (no cancellation near s = 1).
-// Logits past +-87 are held there (s is 1.6e-38 or 1).
+// Logits past +-87 are held there (s is 1.6e-38 or 1); a NaN stays one (the
+// maximum and minimum that pass it on cost what the others do).
 struct Sigm {
     float s, c;
 };
 __device__ __forceinline__ Sigm sigm(float z) {
     constexpr float kL = 1.44269502f, kLlo = 1.92596303e-8f, kLn2 = 0.693147181f;
-    const float m = -fminf(fmaxf(z, -87.f), 87.f);
+    const float m = -__builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -87.f), 87.f);
     const float p = m * kL;
     const float r = fmaf(m, kLlo, fmaf(m, kL, -p));
     float e = __builtin_amdgcn_exp2f(p);
@@ -33,6 +34,13 @@ __device__ __forceinline__ Sigm sigm(float z) {
     o.s = __builtin_amdgcn_rcpf(1.f + e);
     o.c = e * o.s;
     return o;
+}
+
+// v before it is rounded to bf16, which adds to v's bits and would carry a NaN
+// of many set bits over into a number.
+__device__ __forceinline__ float plain_nan(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return __uint_as_float((u & 0x7fffffffu) > 0x7f800000u ? 0x7fc00000u : u);
 }
 
 // Sums over the 16 lanes of a row, and over the wave, in every lane: lane
@@ -150,7 +158,8 @@ __device__ __forceinline__ void score_sums(const SeqArgs& a, const float* __rest
         }
 #pragma unroll
         for (int u = 0; u < kTok; ++u) {
-            const float inv = live[u] ? 1.f / (wave_sum(sum[u]) + 1e-20f) : 0.f;
+            if (!live[u]) continue;  // (uniform; its scores may be NaN)
+            const float inv = 1.f / (wave_sum(sum[u]) + 1e-20f);
 #pragma unroll
             for (int j = 0; j < 2 * J2; ++j) acc[j] = fmaf(v[u][j], inv, acc[j]);
         }
@@ -617,8 +626,9 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
         for (int u = 0; u < kTok; ++u)
 #pragma unroll
             for (int j = 0; j < 2 * J2; ++j) {
-                hi[u][j] = f32_to_bf16(d[u][j]);
-                const float r = d[u][j] - bf16_to_f32(hi[u][j]);
+                const float v = plain_nan(d[u][j]);
+                hi[u][j] = f32_to_bf16(v);
+                const float r = v - bf16_to_f32(hi[u][j]);
                 mid[u][j] = f32_to_bf16(r);
                 lo[u][j] = f32_to_bf16(r - bf16_to_f32(mid[u][j]));
             }
@@ -931,7 +941,7 @@ __global__ __launch_bounds__(64 * kSmallNW) void k_small_products(const float* _
 #pragma unroll
     for (int w = 0; w < kSmallNW; ++w) v += red[w][wid][lane];
     if (isx) {
-        if (r0 + wid < T) dx[(r0 + wid) * d + col] = Elem<TX>::from_f32(v);
+        if (r0 + wid < T) dx[(r0 + wid) * d + col] = Elem<TX>::from_f32(plain_nan(v));
     } else {
         if (r0 + wid < E) dW[(r0 + wid) * d + col] = v;
     }

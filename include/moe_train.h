@@ -28,8 +28,10 @@
  * allocated; concurrent calls, and captured graphs that may run at the same
  * time, need distinct workspaces.  Results do not depend on timing: the same
  * call gives the same bits.  T == 0 is a no-op but for loss (0), seq_counts
- * (zeros) and dW_r (zeros).  NaN and infinite logits are unsupported, but in
- * tokens that do not count (see moe_balance) they are harmless.
+ * (zeros) and dW_r (zeros).  A NaN logit of a token that counts (see
+ * moe_balance) makes the loss NaN, and that token's gradient as far as it
+ * depends on the logit; in tokens that do not count it is harmless.  Logits past
+ * +-87, infinite ones too, are held there.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

@@ -778,3 +778,44 @@ def test_gate_gradient_where_the_guard_counts(K):
     worst = ((got - ref).abs() / (128 * E32 * tol + 1e-36)).max().item()
     _log(f"[gpu] guard K={K}: worst element {worst:.3f} of the tolerance")
     assert worst <= 1.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [0x7fc00000, 0xffffffff])
+@pytest.mark.parametrize("T,E,S", [(20, 16, 1), (128, 300, 3), (400, 70, 3), (1300, 900, 2)])
+def test_a_nan_logit_shows(T, E, S, bits):
+    # of a token that counts: in the loss and in that token's gradient, and nowhere else
+    z, idx, dw, off, mask = _make(97, T, E, 4, S, 0.2)
+    alive, dead = np.flatnonzero(mask), np.flatnonzero(mask == 0)
+    t = int(alive[len(alive) // 2])
+    e = int(np.setdiff1d(np.arange(E), idx[t])[-1])     # not a chosen one
+    nan = np.array(bits, dtype=np.uint32).view(np.float32)
+    bad = z.copy()
+    bad[t, e] = nan
+    bad[dead[0]] = nan
+    gz, gi, gw, go, gm = _dev(z, idx, dw, off, mask)
+    gb = torch.from_numpy(bad).to(DEV)
+    kw = dict(seq_offsets=go, token_mask=gm)
+    l, c = moe.balance_loss(gz, gi, 0.3, **kw)
+    lb, cb = moe.balance_loss(gb, gi, 0.3, **kw)
+    assert torch.isfinite(l) and torch.isnan(lb) and torch.equal(c, cb)
+    d = moe.gate_backward(gz, gi, gw, alpha=0.3, seq_counts=c, **kw)
+    db = moe.gate_backward(gb, gi, gw, alpha=0.3, seq_counts=c, **kw)
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[t] = False
+    assert torch.isnan(db[t]).all() and torch.equal(db[keep], d[keep])
+    for dt, d in ((torch.float32, 64), (torch.bfloat16, 64), (torch.bfloat16, 12800)):   # (every route)
+        x, W = torch.ones(T, d, dtype=dt, device=DEV), torch.ones(E, d, device=DEV)
+        (dx, _), (dxb, dWb) = (moe.router_backward(x, W, v, gi, gw, alpha=0.3, seq_counts=c, **kw) for v in (gz, gb))
+        assert torch.isnan(dxb[t]).all() and torch.equal(dxb[keep], dx[keep]) and torch.isnan(dWb).all()
+    # the gate's weights see the chosen logits only
+    g, gbad = (moe.gate_backward(v, gi, gw, **kw) for v in (gz, gb))
+    assert torch.equal(g, gbad)
+    gb[t, int(idx[t, 0])] = float("nan")
+    gbad = moe.gate_backward(gb, gi, gw, **kw)
+    assert torch.isnan(gbad[t, torch.from_numpy(idx[t]).long().to(DEV)]).all() and torch.equal(gbad[keep], g[keep])
+    # infinite logits are held at the ends
+    inf, held = z.copy(), z.copy()
+    inf[alive[0], :2], held[alive[0], :2] = (np.inf, -np.inf), (100.0, -100.0)
+    li, lh = (moe.balance_loss(torch.from_numpy(v).to(DEV), gi, 0.3, **kw)[0] for v in (inf, held))
+    assert torch.isfinite(li) and torch.equal(li, lh)
