@@ -196,14 +196,16 @@ template <int J2>
 __global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(const SeqArgs a, const float* __restrict__ z,
                                                          const int32_t* __restrict__ idx, float* __restrict__ part_p,
                                                          int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
-                                                         int32_t* __restrict__ ticket) {
+                                                         uint64_t* __restrict__ part_l, int32_t* __restrict__ ticket) {
     constexpr int NW = partial_waves(J2), kTok = partial_toks(J2);
     __shared__ float sp[NW][J2 * 128];
     __shared__ int hist[kMaxE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = blockIdx.x, c0 = c * kChunk, c1 = min(a.T, c0 + kChunk);
-    if (c == 0 && tid == 0) *ticket = 0;  // for k_balance_final
+    // for k_balance_final: no share is there yet
+    if (c == 0 && tid == 0) *ticket = 0;
+    for (int64_t i = c * 64ll * NW + tid; i < (a.E + 63) / 64 * a.S; i += gridDim.x * 64ll * NW) part_l[i] = 0;
     for (int q = seq_of(a, c0); q < a.S && seq_lo(a, q) < c1; ++q) {
         const int lo = max(seq_lo(a, q), c0), hi = min(seq_hi(a, q), c1);
         if (lo >= hi) continue;
@@ -237,12 +239,18 @@ __global__ __launch_bounds__(64 * partial_waves(J2)) void k_balance_partial(cons
 // rows in turn, their sums meet in LDS in wave order; the counts go out, and
 // the block's share of the loss goes to part_l.  The last block to finish
 // adds the shares up in a fixed order: a launch of its own for that would cost
-// more than this kernel.  Latency-bound: 7.8 us at 16384 x 384 x 4
-// sequences, 12.7 at 65521 x 896 x 37 (8 MB of partial rows).
+// more than this kernel.  A share is one atomic word that says itself that it is there (kThere),
+// so the last block needs no order between other blocks' shares and tickets: it
+// reads a word until it is there, and its block has stored it by then or is
+// just about to.  (An acquire-release ticket instead writes back and invalidates
+// the L2 in every block: 173 -> 180 us for loss and gradient of 65521 x 896 in 37
+// sequences, 230 -> 310 of 16384 x 256 in 4000.)  Latency-bound: 7.8 us at
+// 16384 x 384 x 4 sequences, 12.7 at 65521 x 896 x 37 (8 MB of partial rows).
+constexpr uint64_t kThere = 1ull << 32;
 __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const float* __restrict__ part_p,
                                                         const int32_t* __restrict__ part_c,
                                                         const int32_t* __restrict__ part_n, float alpha,
-                                                        float* part_l, int32_t* ticket, float* __restrict__ loss,
+                                                        uint64_t* part_l, int32_t* ticket, float* __restrict__ loss,
                                                         int32_t* __restrict__ seq_counts) {
     __shared__ float sp[16][64];
     __shared__ int sc[16][64], sn[16];
@@ -279,14 +287,8 @@ __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const f
         if (lane == 0) {
             const float nf = static_cast<float>(n);
             const float f = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.K) * nf) / nf : 0.f;
-            __hip_atomic_store(part_l + static_cast<int64_t>(q) * gridDim.x + blockIdx.x, l * f, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-            // The share is written through to memory and read from there (agent-
-            // scope atomics); all that has to be in order is this one store before
-            // the ticket, and an acquire-release ticket would write back and
-            // invalidate the whole L2 in every block.
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __hip_atomic_store(part_l + static_cast<int64_t>(q) * gridDim.x + blockIdx.x,
+                               kThere | __float_as_uint(l * f), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             const int total = static_cast<int>(gridDim.x * gridDim.y);
             last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
         }
@@ -295,8 +297,11 @@ __global__ __launch_bounds__(1024) void k_balance_final(const SeqArgs a, const f
     if (!last) return;
     const int total = static_cast<int>(gridDim.x * gridDim.y);
     float l = 0.f;
-    for (int i = threadIdx.x; i < total; i += 1024)
-        l += __hip_atomic_load(part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = threadIdx.x; i < total; i += 1024) {
+        uint64_t v = 0;
+        while (!(v & kThere)) v = __hip_atomic_load(part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        l += __uint_as_float(static_cast<uint32_t>(v));
+    }
     l = wave_sum(l);
     __syncthreads();
     if (lane == 0) sp[0][wid] = l;
@@ -1019,7 +1024,7 @@ int64_t balance_slots(int T, int S) { return (static_cast<int64_t>(T) + kChunk -
     }
 
 hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* idx, float alpha, float* part_p,
-                               int32_t* part_c, int32_t* part_n, float* part_l, int32_t* ticket, float* loss,
+                               int32_t* part_c, int32_t* part_n, uint64_t* part_l, int32_t* ticket, float* loss,
                                int32_t* seq_counts, hipStream_t stream) {
     if (a.T < 1 || a.E < 1 || a.E > kMaxE || a.S < 1 || a.S > 65535) return hipErrorInvalidValue;
     const int j2 = (a.E + 127) / 128;
@@ -1037,7 +1042,7 @@ hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* 
     const dim3 grid((a.T + kChunk - 1) / kChunk);
 #define MOE_CALL(J2) \
     hipLaunchKernelGGL(k_balance_partial<J2>, grid, dim3(64 * partial_waves(J2)), 0, stream, a, z, idx, part_p, part_c, \
-                       part_n, ticket)
+                       part_n, part_l, ticket)
     MOE_FOR_E(a.E, MOE_CALL);
 #undef MOE_CALL
     const hipError_t err = hipGetLastError();

@@ -24,11 +24,11 @@ struct SeqArgs {
 };
 
 // Balance loss.  part_p / part_c / part_n hold balance_slots(T, S) partial
-// rows of E (p sums, counts, tokens); part_l one float per (sequence, 64
+// rows of E (p sums, counts, tokens); part_l one word per (sequence, 64
 // experts); ticket one int.
 int64_t balance_slots(int T, int S);
 hipError_t launch_balance_loss(const SeqArgs& a, const float* z, const int32_t* idx, float alpha, float* part_p,
-                               int32_t* part_c, int32_t* part_n, float* part_l, int32_t* ticket, float* loss,
+                               int32_t* part_c, int32_t* part_n, uint64_t* part_l, int32_t* ticket, float* loss,
                                int32_t* seq_counts, hipStream_t stream);
 
 // d_logits; dw NULL: no gate term; counts NULL: no balance term.

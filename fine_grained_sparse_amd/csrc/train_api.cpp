@@ -74,7 +74,7 @@ BalancePlan balance_plan(const moe_layer_desc* D, int S) {
     p.o_p = ar.take(slots * D->E * 4);
     p.o_c = ar.take(slots * D->E * 4);
     p.o_n = ar.take(slots * 4);
-    p.o_l = ar.take(cdiv(D->E, 64) * S * 4);
+    p.o_l = ar.take(cdiv(D->E, 64) * S * 8);
     p.o_ticket = ar.take(4);
     p.total = ar.off;
     return p;
@@ -194,7 +194,7 @@ moe_status moe_balance_loss(const moe_layer_desc* desc, const float* logits, con
     if (workspace_bytes < static_cast<size_t>(p.total)) return MOE_ERR_WORKSPACE;
     MOE_HIP(launch_balance_loss(seq_args(desc, balance), logits, topk_idx, balance->alpha, at<float>(workspace, p.o_p),
                                 at<int32_t>(workspace, p.o_c), at<int32_t>(workspace, p.o_n),
-                                at<float>(workspace, p.o_l), at<int32_t>(workspace, p.o_ticket), loss, seq_counts, s));
+                                at<uint64_t>(workspace, p.o_l), at<int32_t>(workspace, p.o_ticket), loss, seq_counts, s));
     return MOE_OK;
 }
 

@@ -819,3 +819,25 @@ def test_a_nan_logit_shows(T, E, S, bits):
     inf[alive[0], :2], held[alive[0], :2] = (np.inf, -np.inf), (100.0, -100.0)
     li, lh = (moe.balance_loss(torch.from_numpy(v).to(DEV), gi, 0.3, **kw)[0] for v in (inf, held))
     assert torch.isfinite(li) and torch.equal(li, lh)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,S", [(300, 129, 2), (5000, 1024, 400), (9000, 70, 65535)])
+def test_the_loss_trusts_nothing_in_its_workspace(T, E, S):
+    # a workspace that holds another call's shares of the loss, or any bits at all, changes no bit of it
+    z, idx, dw, off, mask = _make(101, T, E, 4, S, 0.2, True)
+    loss, counts, _, _ = _balance64(z, idx, off, mask, 0.4)
+    gz, gi, _, go, gm = _dev(z, idx, dw, off, mask)
+    ws, got = moe.Workspace(), []
+    for fill in (0, 0xff, 0x01, None):
+        l, c = moe.balance_loss(gz, gi, 0.4, seq_offsets=go, token_mask=gm, workspace=ws)
+        got.append((l, c))
+        if fill is not None:
+            for buf in ws._buf.values():
+                buf.fill_(fill)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][1].cpu(), counts)
+    # the bound of test_loss_counts_and_logit_gradient; the shares are added up in 1024 threads
+    assert abs(got[0][0].item() - loss) <= (160 + T / 256 + (E + 63) // 64 * S / 1024) * E32 * loss
+    for l, c in got[1:]:
+        assert torch.equal(l, got[0][0]) and torch.equal(c, got[0][1])
