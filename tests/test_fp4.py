@@ -451,3 +451,52 @@ def test_rows_past_32bit_offsets():
     torch.cuda.synchronize()
     some = torch.cat((torch.arange(0, T, 997, device=DEV), torch.arange(T - 40, T, device=DEV)))
     _check("row offsets", out[some], *_reference(x[some], idx[some], wt[some], w, 0))
+
+
+def _rounded(x, idx, wt, w, e0, keep=()):
+    """The layer in float64 with H rounded to bf16, as the layer states, and what `keep` names too: "Y" (the experts' and
+    the shared experts' outputs), "x_lat", "R".  The output is left as it is."""
+    def r(v, name=None):
+        return v.bfloat16().double() if name is None or name in keep else v
+
+    def f(v, Wg, Wu, Wd):
+        a = v @ Wg.T
+        return r(r(a * torch.sigmoid(a) * (v @ Wu.T)) @ Wd.T, "Y")
+    X = x.double()
+    lat = w.get("W_lat_down") is not None
+    V = r(X @ w["W_lat_down"].double().T, "x_lat") if lat else X
+    R = torch.zeros_like(V)
+    for e in range(w["W_gate"].shape[0]):
+        t, k = (idx == e + e0).nonzero(as_tuple=True)
+        if len(t):
+            m = (_dequant(w[n][e], w[n + "_scale"][e]) for n in ("W_gate", "W_up", "W_down"))
+            R.index_add_(0, t, wt[t, k].double()[:, None] * f(V[t], *m))
+    out = r(R, "R") @ w["W_lat_up"].double().T if lat else R
+    if w.get("Ws_gate") is not None:
+        out = out + f(X, *(w[n].double() for n in ("Ws_gate", "Ws_up", "Ws_down")))
+    return out
+
+
+# one kernel for down and combine, direct, 16-row tiles, 64-row tiles; slices; latent maps by either kernel
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,E,Et,K,F,ns,dl", [
+    (1, 4096, 8, 8, 8, 256, 0, 0), (1, 4096, 8, 8, 2, 256, 1, 0), (7, 1024, 16, 32, 6, 512, 0, 0), (16, 1024, 4, 4, 2, 256, 2, 0),
+    (40, 1024, 16, 16, 3, 256, 0, 0), (90, 640, 24, 24, 1, 256, 1, 0), (400, 512, 8, 16, 8, 256, 0, 0), (700, 384, 6, 6, 4, 384, 1, 0),
+    (1, 4096, 8, 8, 8, 256, 0, 640), (12, 1024, 8, 8, 3, 256, 0, 512), (100, 640, 8, 8, 3, 256, 0, 512), (300, 512, 8, 8, 4, 256, 0, 384),
+    (600, 512, 8, 8, 4, 256, 0, 384), (600, 512, 8, 8, 4, 256, 2, 384)])
+def test_only_h_and_the_output_are_rounded(T, d, E, Et, K, F, ns, dl):
+    # Against the float64 layer with the same H, all that is left is the output's own rounding, whose norm is known from
+    # these very values, and what fp32 sums and 16-bit parts change (3e-4 norm-wise at most, mostly by an H that falls on
+    # the other side of a rounding: less than a fifth of it, 2% of the norm).  One more bf16 rounding in the chain
+    # adds as much again as a square, 41%.
+    _log(f"[gpu] fp4 roundings T={T} d={d} E={E}/{Et} K={K} F={F} ns={ns} dl={dl}")
+    x, idx, wt, w = _layer(83, T, d, E, Et, K, F, ns, 128 if ns else 0, dl)
+    out = _run(x, idx, wt, w, 0, Et, ns).double()
+    torch.cuda.synchronize()
+    ref = _rounded(x, idx, wt, w, 0)
+    own = (ref.bfloat16().double() - ref).norm()
+    got = (out - ref).norm() / own
+    _log(f"[gpu]   {got.item():.4f} of the output's own rounding")
+    assert got <= 1.1
+    for name in ("x_lat", "R") if dl and not ns else () if dl else ("Y",):   # the check sees each of these
+        assert (_rounded(x, idx, wt, w, 0, (name,)).bfloat16().double() - ref).norm() > 1.2 * own, name
