@@ -460,7 +460,13 @@ moe_status run_experts(const Plan& p, const void* x, const int32_t* idx, const f
     GemmGroup& G = g.g[0];
     int ns = 0;
     if (p.ns) G.seg[ns++] = GemmSeg{Hs, W->Ws_down, nullptr, p.Fsh, p.Fsh, p.Fsh, 0};
-    if (p.f4 && p.T <= kDenseRows16T) {
+    // R's two parts: one segment where the kernel takes them so, and must, as the
+    // register-fed tile has two segments and Hs is one; else a segment each.
+    // 7168 to 3584 with a shared expert, on that tile / the LDS tile (three segments):
+    // 830 / 871 us at 2048 tokens, 1488 / 1567 at 4096, 547 / 540 at 600
+    const int64_t widest = std::max(p.dl, p.Fsh);
+    if (p.f4 && (p.T <= kDenseRows16T ||
+                 (ns == 1 && p.dcfg == TILE_WIDE && p.d * widest * 2 < (int64_t{1} << 31)))) {
         G.seg[ns++] = GemmSeg{R, W->W_lat_up, nullptr, 2 * p.dl, p.dl, p.dl, 1};
     } else if (p.f4) {
         G.seg[ns++] = GemmSeg{R, W->W_lat_up, nullptr, 2 * p.dl, p.dl, p.dl, 0};

@@ -763,7 +763,8 @@ __device__ __forceinline__ void wide_tile(const GemmArgs& a, const Job& jb, char
     const GemmGroup& G = jb.gi ? a.g[1] : a.g[0];
     const int N = G.N, row0 = jb.row0, rows = jb.rows, n0 = jb.n0;
     const int nk0 = G.seg[0].K / BKE;
-    const int nkt = nk0 + (NSEG == 2 ? G.seg[1].K / BKE : 0);  // >= 1
+    const int nk1 = NSEG == 2 ? G.seg[1].K / BKE : 0;
+    const int nkt = nk0 + (NSEG == 2 && G.seg[1].two ? 2 * nk1 : nk1);  // >= 1
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -829,7 +830,9 @@ __device__ __forceinline__ void wide_tile(const GemmArgs& a, const Job& jb, char
         const bool s1 = NSEG == 2 && kt >= nk0;
         const bool up = EPI == EPI_SWIGLU && j >= NB / 2;
         const char* m = s1 ? (up ? sU1 : sB1) : (up ? sU0 : sB0);
-        const uint32_t kblk = F8 ? static_cast<uint32_t>(kt) : static_cast<uint32_t>((kt - (s1 ? nk0 : 0)) * 2 + sl);
+        // (segment 1 in two parts: A's columns go on, the weights start again)
+        const int k1 = kt >= nk0 + nk1 ? nk0 + nk1 : nk0;
+        const uint32_t kblk = F8 ? static_cast<uint32_t>(kt) : static_cast<uint32_t>((kt - (s1 ? k1 : 0)) * 2 + sl);
         const uint32_t blk = static_cast<uint32_t>(rb[j]) * (s1 ? kb1 : kb0) + kblk;
         // decode tiles (16 rows) stream each expert's FP8 codes once, with
         // the non-temporal hint and compiler-counted waits (exact explicit
@@ -1107,7 +1110,8 @@ int tile_bn_out(TileCfg cfg, Epi epi) {  // bf16 kernels (sizing heuristics only
 namespace {
 
 // What the wide kernel handles: packed weights, one or two K segments per
-// group (multiples of 64), no split K, fragment-block byte offsets in 31 bits.
+// group (multiples of 64; the second may be in two parts), no split K,
+// fragment-block byte offsets in 31 bits.
 bool wide_fits(const GemmArgs& a) {
     if (a.nsplit != 1) return false;
     for (int g = 0; g < 2; ++g) {
@@ -1115,11 +1119,18 @@ bool wide_fits(const GemmArgs& a) {
         if (G.N == 0) continue;
         if (G.nseg < 1 || G.nseg > 2 || G.N % 16 != 0) return false;
         for (int s = 0; s < G.nseg; ++s)
-            if (G.seg[s].K < 64 || G.seg[s].K % 64 != 0 ||
+            if (G.seg[s].K < 64 || G.seg[s].K % 64 != 0 || (G.seg[s].two && s != 1) ||
                 static_cast<int64_t>(G.N) * G.seg[s].K * 2 >= (int64_t{1} << 31))
                 return false;
     }
     return true;
+}
+
+bool in_two_parts(const GemmArgs& a) {
+    for (const GemmGroup& G : a.g)
+        for (int s = 0; s < G.nseg; ++s)
+            if (G.seg[s].two) return true;
+    return false;
 }
 
 int max_nseg(const GemmArgs& a) {
@@ -1136,6 +1147,7 @@ hipError_t launch_t(const GemmArgs& args, TileCfg cfg, int max_tiles, int max_n,
     if (cfg == TILE_WIDE16) cfg = TILE_SMALL;  // bf16 decode: the LDS tile streams slightly faster
     if (cfg == TILE_SMALL && sizeof(TC) == 4) cfg = TILE_NARROW;  // the router logits (fp32 out)
     const bool wide = cfg == TILE_WIDE;
+    if (!wide && in_two_parts(args)) return hipErrorInvalidValue;
     // output columns per N tile of the kernel actually launched
     const int bn = sizeof(T) == 4 ? kF32BN
                    : cfg == TILE_SMALL ? kSmBN

@@ -32,7 +32,8 @@ struct GemmSeg {
     const void* Bu;
     int64_t lda, ldb;
     int32_t K;
-    int32_t two;  // launch_dense_rows16: a row of A holds two parts of K columns, whose sum B meets
+    int32_t two;  // (launch_dense_rows16, and a second segment on TILE_WIDE) a row of A holds two parts of K columns,
+                  // whose sum B meets
 };
 
 // A family of tiles sharing operands: the routed experts (B offset by
