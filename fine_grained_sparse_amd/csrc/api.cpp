@@ -36,10 +36,12 @@ constexpr int64_t kAlign = 256;
 constexpr int kRouterGemvT = 32;  // router logits by k_router_gemv up to this many tokens
 static_assert(kRouterGemvT <= kRouterGemvMaxT, "the kernel's token capacity");
 // Latent maps of FP4 layers by launch_dense_rows16 up to this many tokens.
-// A 7168-to-3584 layer with few weights otherwise, against the GEMM tiles: 95
-// against 338 us at 8 tokens, 270 / 437 at 64, 367 / 441 at 128, 609 / 488 at
-// 256 (every 16 tokens are another pass over the weights).
-constexpr int kDenseRows16T = 128;
+// A 7168-to-3584 layer of 64 small experts, against the GEMM tiles (without /
+// with a shared expert): 73 / 84 against 301 / 346 us at 8 tokens, 144 / 197
+// against 322 / 392 at 64, 245 / 322 against 329 / 400 at 144, 326 / 408 against
+// 350 / 410 at 192, 404 / 514 against 355 / 424 at 256 (every 16 tokens are another
+// pass over the weights, and the GEMM tiles leave x_lat in fp32 to be split).
+constexpr int kDenseRows16T = 192;
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -500,3 +500,10 @@ def test_only_h_and_the_output_are_rounded(T, d, E, Et, K, F, ns, dl):
     assert got <= 1.1
     for name in ("x_lat", "R") if dl and not ns else () if dl else ("Y",):   # the check sees each of these
         assert (_rounded(x, idx, wt, w, 0, (name,)).bfloat16().double() - ref).norm() > 1.2 * own, name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [129, 192, 193])
+@pytest.mark.parametrize("ns", [0, 1])
+def test_latent_maps_on_either_side_of_their_limit(T, ns):
+    test_only_h_and_the_output_are_rounded(T, 512, 8, 16, 4, 256, ns, 384)
