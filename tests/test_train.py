@@ -841,3 +841,35 @@ def test_the_loss_trusts_nothing_in_its_workspace(T, E, S):
     assert abs(got[0][0].item() - loss) <= (160 + T / 256 + (E + 63) // 64 * S / 1024) * E32 * loss
     for l, c in got[1:]:
         assert torch.equal(l, got[0][0]) and torch.equal(c, got[0][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3000, 40000])
+def test_masked_gradients_captured_and_replayed(T):
+    # the mask, the sequences and the logits change between replays; both ways of counting a sequence's tokens
+    E, K, S, d = 40, 4, 9, 64
+    runs = [_foreign(seed, T, E, K, S, 0.3, True, 0.3) for seed in (111, 112, 113)]
+    x = torch.randn(T, d, device=DEV).bfloat16()
+    W = torch.randn(E, d, device=DEV)
+
+    def step(z, idx, dw, off, mask, ws, stream=None):
+        l, c = moe.balance_loss(z, idx, 0.3, seq_offsets=off, token_mask=mask, workspace=ws, stream=stream)
+        kw = dict(alpha=0.3, seq_counts=c, seq_offsets=off, token_mask=mask, stream=stream)
+        return (l, c, moe.gate_backward(z, idx, dw, **kw), *moe.router_backward(x, W, z, idx, dw, workspace=ws, **kw))
+    want = [[t.clone() for t in step(*_dev(*r), moe.Workspace())] for r in runs]
+    bufs, ws, s = _dev(*runs[0]), moe.Workspace(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    step(*bufs, ws, s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step(*bufs, ws, s)
+    for i in (1, 2, 0, 1):
+        for b, v in zip(bufs, _dev(*runs[i])):
+            b.copy_(v)
+        step(*_dev(*runs[2]), moe.Workspace())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(out, want[i]):
+            assert torch.equal(got, ref), i
