@@ -56,7 +56,7 @@ WEIGHTS_NOTE = {"frag16": "bf16, fragment-block layout (moe_pack_weights once at
 FP8_NOTE = ("routed experts FP8 E4M3FN with one E8M0 scale per 128x128 block, shared experts "
             "bf16; fragment-block layout (moe_pack_weights once at load, untimed)")
 # the library's sources that define or launch the layer's kernels
-LAYER_SOURCES = ("api.cpp", "common.hpp", "launch.hpp", "gemm.hip", "router.hip", "dispatch.hip")
+LAYER_SOURCES = ("api.cpp", "common.hpp", "launch.hpp", "jobs.hpp", "gemm.hip", "router.hip", "dispatch.hip")
 
 
 def weights_note(wl, layout):

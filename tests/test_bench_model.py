@@ -9,6 +9,7 @@ term in bench.work_model fails: per token and selected expert a SwiGLU
 expert is three d_in x F products, 2 flops per multiply-add; a touched
 expert's weights are read once."""
 import os
+import re
 import shutil
 
 import pytest
@@ -181,3 +182,13 @@ def test_clock_snapshot_has_its_fields():
     assert isinstance(c["source"], str) and c["source"]
     for k in ("sclk_mhz", "mclk_mhz"):
         assert c[k] is None or (isinstance(c[k], int) and c[k] > 0)
+
+
+def test_source_hash_covers_the_headers_of_the_layer_kernels():
+    # code that moves from a kernel file to a header of it still belongs to the kernels that counters describe
+    csrc = os.path.join(bench.ROOT, "fine_grained_sparse_amd", "csrc")
+    for name in bench.LAYER_SOURCES:
+        if name.endswith(".hip"):
+            text = open(os.path.join(csrc, name)).read()
+            for header in re.findall(r'#include "([^"/]+)"', text):
+                assert header in bench.LAYER_SOURCES, (name, header)
