@@ -36,13 +36,6 @@ __device__ __forceinline__ Sigm sigm(float z) {
     return o;
 }
 
-// v before it is rounded to bf16, which adds to v's bits and would carry a NaN
-// of many set bits over into a number.
-__device__ __forceinline__ float plain_nan(float v) {
-    const uint32_t u = __float_as_uint(v);
-    return __uint_as_float((u & 0x7fffffffu) > 0x7f800000u ? 0x7fc00000u : u);
-}
-
 // Sums over the 16 lanes of a row, and over the wave, in every lane: lane
 // moves inside the adds (partners at distance 1, 2, then the mirrored half
 // and row, whose sums are complete by then) and two half-wave swaps, where
@@ -631,9 +624,8 @@ __global__ __launch_bounds__(256) void k_gate_backward(const SeqArgs a, const fl
         for (int u = 0; u < kTok; ++u)
 #pragma unroll
             for (int j = 0; j < 2 * J2; ++j) {
-                const float v = plain_nan(d[u][j]);
-                hi[u][j] = f32_to_bf16(v);
-                const float r = v - bf16_to_f32(hi[u][j]);
+                hi[u][j] = f32_to_bf16(d[u][j]);
+                const float r = d[u][j] - bf16_to_f32(hi[u][j]);
                 mid[u][j] = f32_to_bf16(r);
                 lo[u][j] = f32_to_bf16(r - bf16_to_f32(mid[u][j]));
             }
@@ -946,7 +938,7 @@ __global__ __launch_bounds__(64 * kSmallNW) void k_small_products(const float* _
 #pragma unroll
     for (int w = 0; w < kSmallNW; ++w) v += red[w][wid][lane];
     if (isx) {
-        if (r0 + wid < T) dx[(r0 + wid) * d + col] = Elem<TX>::from_f32(plain_nan(v));
+        if (r0 + wid < T) dx[(r0 + wid) * d + col] = Elem<TX>::from_f32(v);
     } else {
         if (r0 + wid < E) dW[(r0 + wid) * d + col] = v;
     }

@@ -507,3 +507,23 @@ def test_only_h_and_the_output_are_rounded(T, d, E, Et, K, F, ns, dl):
 @pytest.mark.parametrize("ns", [0, 1])
 def test_latent_maps_on_either_side_of_their_limit(T, ns):
     test_only_h_and_the_output_are_rounded(T, 512, 8, 16, 4, 256, ns, 384)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,dl", [(1, 0), (5, 0), (40, 0), (600, 0), (1, 256), (40, 256), (600, 256)])
+@pytest.mark.parametrize("kind", ["fp4", "bf16"])
+def test_a_nan_gate_weight_shows(kind, T, dl):
+    # whatever the NaN's bits: all of them set carried over into a number in the rounding to bf16
+    d, E, K, F = 256, 6, 2, 128
+    x, idx, wt, w = _layer(85, T, d, E, E, K, F, 1, 64, dl)
+    if kind == "bf16":
+        w = {n: (_dequant(v, w[n + "_scale"]).bfloat16() if n + "_scale" in w else v) for n, v in w.items() if "_scale" not in n}
+    p = moe.pack_weights(w, n_shared=1)
+    ref = moe.forward_slice(x, idx, wt, p, 0, E, n_shared=1)
+    keep = torch.arange(T, device=DEV) != T // 2
+    for bits in (-1, 0x7fc00000, 0x7fffffff, -0x400000 + 1):
+        bad = wt.clone()
+        bad.view(torch.int32)[T // 2, 0] = bits
+        out = moe.forward_slice(x, idx, bad, p, 0, E, n_shared=1)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[T // 2]).all() and torch.equal(out[keep], ref[keep]), bits
