@@ -19,8 +19,10 @@
 //
 // Bound by the weights' bytes (0.53 per weight) until an expert has some 60
 // rows, from there by the MFMAs and the conversions beside them.  The sums
-// stay in fp32 through the K split and the combine; only H is rounded, to the
-// bf16 the next MFMA takes.
+// stay in fp32 through the K split and the combine; H is rounded, to the bf16
+// the next MFMA takes (as in the bf16 and FP8 layers; norm-wise 1.6e-3, about
+// the output's own rounding), and in latent layers x_lat and the sum R to two
+// bf16 parts, 16 bits.
 #include "common.hpp"
 #include "jobs.hpp"
 #include "launch.hpp"
@@ -433,7 +435,7 @@ __global__ __launch_bounds__(64 * kFusedNW) void k_fp4_down_combine(const GemmAr
 // Measured, 2048 tokens over 48 of 384 experts of 7168 x 2048 and a shared one
 // (43 rows an expert): up 296 to 322 us, down 168 to 182 us, 361 GFLOP together
 // at 0.72 to 0.78 PFLOP/s (a large bf16 product of the library: 1.37) while
-// 1.2 GB stream past.
+// 2.1 GB stream past, half of them for the shared pairs.
 template <typename TC, int EPI, int MT, bool ONCE, bool TWO>
 struct Fp4Tile {
     static constexpr int BM = 16 * MT, RB = 4, NJ = EPI == EPI_SWIGLU ? RB / 2 : RB;

@@ -8,6 +8,10 @@ library declared in include/moe_train.h (formulas and limits there).
                                seq_offsets=..., token_mask=...)
     bias_update(seq_counts.sum(0, dtype=torch.int32), b)
 
+Results carry no autograd graph, whatever their inputs do: gate_backward and
+router_backward are the gradients, called by hand or from the backward() of a
+torch.autograd.Function of the caller's.
+
 Like the package's other entry points these only check and marshal arguments,
 allocate outputs and workspaces on the launch stream, and enqueue HIP
 kernels; there is no fallback.  A call that is captured into a graph should be
