@@ -435,7 +435,7 @@ __global__ __launch_bounds__(64 * kFusedNW) void k_fp4_down_combine(const GemmAr
 // Measured, 2048 tokens over 48 of 384 experts of 7168 x 2048 and a shared one
 // (43 rows an expert): up 296 to 322 us, down 168 to 182 us, 361 GFLOP together
 // at 0.72 to 0.78 PFLOP/s (a large bf16 product of the library: 1.37) while
-// 2.1 GB stream past, half of them for the shared pairs.
+// 2.1 GB stream past, 0.8 of them for the shared pairs.
 template <typename TC, int EPI, int MT, bool ONCE, bool TWO>
 struct Fp4Tile {
     static constexpr int BM = 16 * MT, RB = 4, NJ = EPI == EPI_SWIGLU ? RB / 2 : RB;
