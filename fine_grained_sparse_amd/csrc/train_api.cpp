@@ -46,6 +46,16 @@ P* at(void* ws, int64_t off) {
     return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
 }
 
+// The router's own checks, and a T whose launches stay below 2^32 threads, as a
+// launch must (16 threads a token; 32 above 512 experts, whose logits fill the
+// memory before).  Token numbers that a kernel forms past the last one then fit
+// in 31 bits too.
+constexpr int32_t kMaxT = (1 << 28) - 65536;
+moe_status check_desc(const moe_layer_desc* D) {
+    const moe_status st = router_check(D);
+    return st == MOE_OK && D->T > kMaxT ? MOE_ERR_SHAPE : st;
+}
+
 moe_status check_balance(const moe_balance* b) {
     if (b->n_seq < 1 || b->n_seq > 65535) return MOE_ERR_SHAPE;
     if (!b->seq_offsets && b->n_seq != 1) return MOE_ERR_NULL;
@@ -142,7 +152,7 @@ GemmArgs dense(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t K
 // zeros of an empty batch.
 moe_status check_backward(const moe_layer_desc* D, const float* logits, const int32_t* idx, const float* dw,
                           const moe_balance* b, const int32_t* counts, const float* d_loss, bool* idle) {
-    const moe_status st = router_check(D);
+    const moe_status st = check_desc(D);
     if (st != MOE_OK) return st;
     *idle = D->T == 0;
     if (counts && !b) return MOE_ERR_NULL;
@@ -169,14 +179,14 @@ moe_status moe_router_train(const moe_layer_desc* desc, const void* x, const flo
 }
 
 size_t moe_balance_workspace_size(const moe_layer_desc* desc, int32_t n_seq) {
-    if (router_check(desc) != MOE_OK || n_seq < 1 || n_seq > 65535) return 0;
+    if (check_desc(desc) != MOE_OK || n_seq < 1 || n_seq > 65535) return 0;
     return static_cast<size_t>(balance_plan(desc, n_seq).total);
 }
 
 moe_status moe_balance_loss(const moe_layer_desc* desc, const float* logits, const int32_t* topk_idx,
                             const moe_balance* balance, float* loss, int32_t* seq_counts, void* workspace,
                             size_t workspace_bytes, void* stream) {
-    moe_status st = router_check(desc);
+    moe_status st = check_desc(desc);
     if (st != MOE_OK) return st;
     if (!balance || !loss || !seq_counts) return MOE_ERR_NULL;
     st = check_balance(balance);
@@ -212,7 +222,7 @@ moe_status moe_gate_backward(const moe_layer_desc* desc, const float* logits, co
 }
 
 size_t moe_router_backward_workspace_size(const moe_layer_desc* desc) {
-    if (router_check(desc) != MOE_OK) return 0;
+    if (check_desc(desc) != MOE_OK) return 0;
     return static_cast<size_t>(back_plan(desc).total);
 }
 

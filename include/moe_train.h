@@ -27,7 +27,8 @@
  * must belong to the current device, so they can be captured; nothing is
  * allocated; concurrent calls, and captured graphs that may run at the same
  * time, need distinct workspaces.  Results do not depend on timing: the same
- * call gives the same bits.  T == 0 is a no-op but for loss (0), seq_counts
+ * call gives the same bits.  T is at most 2^28 - 65536 (moe_router_train: as
+ * moe_router).  T == 0 is a no-op but for loss (0), seq_counts
  * (zeros) and dW_r (zeros).  A NaN logit of a token that counts (see
  * moe_balance) makes the loss NaN, and that token's gradient as far as it
  * depends on the logit; in tokens that do not count it is harmless.  Logits past

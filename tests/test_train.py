@@ -873,3 +873,18 @@ def test_masked_gradients_captured_and_replayed(T):
         torch.cuda.synchronize()
         for got, ref in zip(out, want[i]):
             assert torch.equal(got, ref), i
+
+
+def test_batches_past_the_largest_launch_are_refused():
+    # 16 threads a token: 2^32 threads are more than a launch can have, though T K still fits in 31 bits
+    L, vp = train.train_lib(), ctypes.c_void_p
+    for T, want in ((2 ** 28 - 65536, True), (2 ** 28 - 65535, False), (2 ** 31 - 1, False)):
+        D = ctypes.byref(moe.desc(T=T, d=64, E=1, K=1))
+        assert (L.moe_balance_workspace_size(D, 1) > 0) == want
+        assert (L.moe_router_backward_workspace_size(D) > 0) == want
+        # (a null output ends the calls that are not refused for T)
+        B = _ref(_bal(S=1, off=None))
+        assert L.moe_balance_loss(D, vp(FAKE), vp(FAKE), B, None, vp(FAKE), vp(FAKE), 1 << 50, None) == (NULL if want else SHAPE)
+        assert L.moe_gate_backward(D, vp(FAKE), vp(FAKE), vp(FAKE), B, vp(FAKE), None, None, None) == (NULL if want else SHAPE)
+        assert L.moe_router_backward(D, vp(FAKE), vp(FAKE), vp(FAKE), vp(FAKE), vp(FAKE), B, vp(FAKE), None, None, None,
+                                     vp(FAKE), 1 << 50, None) == (NULL if want else SHAPE)
