@@ -518,4 +518,10 @@ __all__ = ["router", "forward", "forward_noalloc", "pack_weights", "bias_update"
 
 from .train import balance_loss, gate_backward, router_backward, router_train  # noqa: E402  (needs the names above)
 
-__all__ += ["router_train", "balance_loss", "gate_backward", "router_backward"]
+from .experts import (Order, Saved, combine, combine_backward, dispatch, experts_backward, experts_forward,  # noqa: E402
+                      sort_tokens, sort_tokens_backward)
+from .optim import AdamW  # noqa: E402
+
+__all__ += ["router_train", "balance_loss", "gate_backward", "router_backward", "Order", "Saved", "dispatch",
+            "sort_tokens", "sort_tokens_backward", "combine", "combine_backward", "experts_forward", "experts_backward",
+            "AdamW"]

@@ -15,8 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "moe")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cpp", "gemm.hip", "fp4.hip", "router.hip", "dispatch.hip", "pack.hip", "noalloc.hip"]
-# the router's training side (include/moe_train.h), which calls into libmoe.so
-TRAIN_SOURCES = ["train_api.cpp", "train.hip"]
+# the training side (include/moe_train.h), which calls into libmoe.so
+TRAIN_SOURCES = ["train_api.cpp", "train.hip", "experts_api.cpp", "rows.hip", "experts.hip", "adamw.hip"]
 TRAIN_LIB = os.path.join(HERE, "libmoe_train.so")
 # measurement aid of bench.py (HBM streaming read, bf16 MFMA loop), a library
 # of its own so that libmoe.so exports only the layer's C ABI

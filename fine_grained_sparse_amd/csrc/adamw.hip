@@ -1,0 +1,391 @@
+// One AdamW step over many tensors: decoupled weight decay, moments in fp32 or
+// in 8 bits.
+//   m <- b1 m + (1 - b1) g,   v <- b2 v + (1 - b2) g^2   (g scaled by grad_scale)
+//   p <- (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// 8-bit moments.  128 consecutive values share a power of two (E8M0).  m is E4M3 (sign, 4
+// exponent bits, bias 7, 3 fraction bits), scaled so that the block's largest value lies in
+// [128, 256); v, never negative, has 5 exponent bits (bias 15) and 3 fraction
+// bits, the largest in [2^15, 2^16).  v keeps no root: the average is linear in
+// v, and rounded at random it keeps its mean, while rounded to nearest a
+// change of 1 - b2 = 1e-3 would never leave a value of 3 fraction bits.  The random
+// bits are a hash of (seed, step, tensor, element): the same step gives the same
+// bits, whatever the launch.  A product or sum of the moments is rounded by itself (no
+// fused multiply-add), so that the codes are those of the formula in fp32.
+// bf16 parameters are rounded at random too: lr of a step is mostly below half
+// a step of bf16.
+#include <cmath>
+
+#include "common.hpp"
+#include "experts.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kTensors = 48;     // of a launch: their table is a kernel argument
+constexpr int kPerThread = 8, kSpan = 256 * kPerThread, kRounds = 4;
+constexpr int64_t kChunk = static_cast<int64_t>(kSpan) * kRounds;  // elements of a block
+
+struct Table {
+    moe_adamw_tensor t[kTensors];
+    uint32_t first[kTensors];  // each tensor's first block
+    int32_t n, base;           // tensors, and the number of the first in the whole call
+};
+
+struct Step {
+    float b1, b2, n1, n2;      // b, 1 - b
+    double beta1, beta2, c1, c2;  // c: 1 - beta^step, of a step that the host knows
+    float lr, eps, wd;
+    int32_t step;
+    uint32_t seed;
+    const float* lr_dev;
+    const int32_t* step_dev;
+    const float* grad_scale;
+};
+
+// The finaliser of MurmurHash3 (Austin Appleby, public domain).
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x85ebca6bu;
+    h = (h ^ (h >> 13)) * 0xc2b2ae35u;
+    return h ^ (h >> 16);
+}
+
+// Block -> tensor: the last whose first block is not behind it.
+__device__ __forceinline__ int find_tensor(const Table& T, uint32_t block) {
+    int lo = 0, hi = T.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (T.first[mid] <= block) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The largest over the 16 lanes that share a block of 128 values.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o)));
+    return v;
+}
+
+// E8M0 code of a block whose largest magnitude has these bits: that value then
+// has exponent TOP; 255 for one with infinities or NaN.
+template <int TOP>
+__device__ __forceinline__ int scale_code(uint32_t bits) {
+    const int e = static_cast<int>(bits >> 23);
+    return e == 255 ? 255 : max(e - TOP, 0);
+}
+
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, int64_t i, int live, float (&o)[8]) {
+    if (live == 8) {
+        unpack8(p + i, o);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = k < live ? Elem<T>::to_f32(p[i + k]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put8(T* p, int64_t i, int live, const float (&v)[8]) {
+    if (live == 8) {
+        pack8(p + i, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < live) p[i + k] = Elem<T>::from_f32(v[k]);
+    }
+}
+__device__ __forceinline__ uint2 codes8(const uint8_t* p, int64_t i, int live) {
+    if (live == 8) return *reinterpret_cast<const uint2*>(p + i);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < live) w[k >> 2] |= static_cast<uint32_t>(p[i + k]) << (8 * (k & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void codes8(uint8_t* p, int64_t i, int live, uint2 v) {
+    if (live == 8) {
+        *reinterpret_cast<uint2*>(p + i) = v;
+    } else {
+        const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < live) p[i + k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
+    }
+}
+
+// A code's bits from bit 20 on are those of a float that is 2^-120 (m) or 2^-112
+// (v) of its scaled value, subnormals included.
+__device__ __forceinline__ float value_m(uint32_t c, int s) {
+    const float x = __uint_as_float(((c & 0x80u) << 24) | ((c & 0x7fu) << 20));
+    return s == 255 ? __builtin_nanf("") : ldexpf(x, s - 127 + 120);
+}
+__device__ __forceinline__ float value_v(uint32_t c, int s) {
+    return s == 255 ? __builtin_nanf("") : ldexpf(__uint_as_float(c << 20), s - 127 + 112);
+}
+// ... and back, 16 random bits deciding between a value's two neighbours.
+__device__ __forceinline__ uint32_t code(float x, int e, uint32_t rnd16) {
+    return (__float_as_uint(ldexpf(fabsf(x), e)) + rnd16 * 16u + 8u) >> 20;
+}
+
+__device__ __forceinline__ uint32_t bf16_at_random(float x, uint32_t rnd16) {
+    const uint32_t b = __float_as_uint(x);
+    if ((b & 0x7f800000u) == 0x7f800000u) return f32_to_bf16(x);  // infinities and NaN stay what they are
+    return (b + rnd16) >> 16;
+}
+
+// x b + y and x y with every operation rounded (__fmul_rn and its like are contracted).
+__device__ __forceinline__ float average(float x, float b, float y) {
+#pragma clang fp contract(off)
+    const float q = x * b;
+    return q + y;
+}
+__device__ __forceinline__ float product(float x, float y) {
+#pragma clang fp contract(off)
+    return x * y;
+}
+
+template <typename TP, typename TG, bool EIGHT>
+__global__ __launch_bounds__(256) void k_adamw(const Table T, const Step S) {
+    const int tid = threadIdx.x;
+    const int ti = find_tensor(T, blockIdx.x);
+    const moe_adamw_tensor& t = T.t[ti];
+    const int64_t n = t.n, c0 = static_cast<int64_t>(blockIdx.x - T.first[ti]) * kChunk;
+    const float lr = S.lr_dev ? *S.lr_dev : S.lr;
+    const int step = S.step_dev ? *S.step_dev : S.step;
+    const float gs = S.grad_scale ? *S.grad_scale : 1.f;
+    const float keep = static_cast<float>(1.0 - static_cast<double>(lr) * S.wd);
+    double d1 = S.c1, d2 = S.c2;
+    if (S.step_dev) {
+        double q1 = 1.0, q2 = 1.0, s1 = S.beta1, s2 = S.beta2;
+        for (uint32_t k = static_cast<uint32_t>(max(step, 1)); k; k >>= 1, s1 *= s1, s2 *= s2)
+            if (k & 1) q1 *= s1, q2 *= s2;
+        d1 = 1.0 - q1;
+        d2 = 1.0 - q2;
+    }
+    const float rate = static_cast<float>(static_cast<double>(lr) / d1);
+    const float root = static_cast<float>(1.0 / sqrt(d2));
+    const uint32_t key0 = mix(mix(mix(S.seed) + static_cast<uint32_t>(step)) + static_cast<uint32_t>(T.base + ti));
+    TP* const p = static_cast<TP*>(t.param);
+    const TG* const g = static_cast<const TG*>(t.grad);
+#pragma unroll 1
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t i = c0 + r * kSpan + tid * kPerThread;
+        const int live = static_cast<int>(min(max(n - i, int64_t(0)), int64_t(8)));
+        if (c0 + r * kSpan >= n) break;  // (uniform)
+        float pv[8], gv[8], m[8], v[8];
+        get8(p, i, live, pv);
+        get8(g, i, live, gv);
+        int sm = 0, sv = 0;
+        if (EIGHT) {
+            uint2 cm = make_uint2(0, 0), cv = cm;
+            if (live) {
+                cm = codes8(static_cast<const uint8_t*>(t.exp_avg), i, live);
+                cv = codes8(static_cast<const uint8_t*>(t.exp_avg_sq), i, live);
+                sm = t.exp_avg_scale[i >> 7];
+                sv = t.exp_avg_sq_scale[i >> 7];
+            }
+            const uint32_t wm[2] = {cm.x, cm.y}, wv[2] = {cv.x, cv.y};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                m[k] = value_m((wm[k >> 2] >> (8 * (k & 3))) & 0xffu, sm);
+                v[k] = value_v((wv[k >> 2] >> (8 * (k & 3))) & 0xffu, sv);
+            }
+        } else {
+            get8(static_cast<const float*>(t.exp_avg), i, live, m);
+            get8(static_cast<const float*>(t.exp_avg_sq), i, live, v);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float gk = gv[k] * gs;
+            m[k] = average(m[k], S.b1, gk * S.n1);
+            v[k] = average(v[k], S.b2, product(gk * S.n2, gk));
+            pv[k] = pv[k] * keep - rate * m[k] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[k]) * root + S.eps);
+        }
+        constexpr bool kHash = EIGHT || sizeof(TP) == 2;
+        uint32_t word[8];
+        if (kHash) {
+            const uint32_t key = key0 + static_cast<uint32_t>(i >> 32) * 0x9e3779b9u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) word[k] = mix(static_cast<uint32_t>(i) + k + key);
+        }
+        if (EIGHT) {
+            uint32_t am = 0, av = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k >= live) m[k] = v[k] = 0.f;
+                am = max(am, __float_as_uint(m[k]) & 0x7fffffffu);
+                av = max(av, __float_as_uint(v[k]) & 0x7fffffffu);
+            }
+            sm = scale_code<7>(max16(am));
+            sv = scale_code<15>(max16(av));
+            uint32_t wm[2] = {0, 0}, wv[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t cm = code(m[k], 127 - sm - 120, word[k] & 0xffffu) | ((__float_as_uint(m[k]) >> 24) & 0x80u);
+                const uint32_t cv = code(v[k], 127 - sv - 112, word[k] >> 16);
+                wm[k >> 2] |= (cm & 0xffu) << (8 * (k & 3));
+                wv[k >> 2] |= (cv & 0xffu) << (8 * (k & 3));
+            }
+            if (live) {
+                codes8(static_cast<uint8_t*>(t.exp_avg), i, live, make_uint2(wm[0], wm[1]));
+                codes8(static_cast<uint8_t*>(t.exp_avg_sq), i, live, make_uint2(wv[0], wv[1]));
+                if ((tid & 15) == 0) {
+                    t.exp_avg_scale[i >> 7] = static_cast<uint8_t>(sm);
+                    t.exp_avg_sq_scale[i >> 7] = static_cast<uint8_t>(sv);
+                }
+            }
+        } else {
+            put8(static_cast<float*>(t.exp_avg), i, live, m);
+            put8(static_cast<float*>(t.exp_avg_sq), i, live, v);
+        }
+        if (sizeof(TP) == 2) {
+            uint32_t b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = bf16_at_random(pv[k], mix(word[k] ^ 0x9e3779b9u) & 0xffffu);
+            if (live == 8) {
+                stg16(reinterpret_cast<char*>(p) + i * 2, make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16)));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < live) reinterpret_cast<uint16_t*>(p)[i + k] = static_cast<uint16_t>(b[k]);
+            }
+        } else {
+            put8(reinterpret_cast<float*>(p), i, live, pv);
+            if (t.copy) put8(static_cast<bf16_t*>(t.copy), i, live, pv);
+        }
+    }
+}
+
+struct MomentsTable {
+    const uint8_t *m[kTensors], *v[kTensors], *ms[kTensors], *vs[kTensors];
+    float *om[kTensors], *ov[kTensors];
+    int64_t len[kTensors];
+    uint32_t first[kTensors];
+    int32_t n;
+};
+
+// Codes to the values they stand for.
+__global__ __launch_bounds__(256) void k_moments(const MomentsTable T) {
+    int lo = 0, hi = T.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (T.first[mid] <= blockIdx.x) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t n = T.len[lo], c0 = static_cast<int64_t>(blockIdx.x - T.first[lo]) * kChunk;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t i = c0 + r * kSpan + threadIdx.x * kPerThread;
+        const int live = static_cast<int>(min(max(n - i, int64_t(0)), int64_t(8)));
+        if (!live) continue;
+        float o[8];
+        if (T.om[lo]) {
+            const uint2 c = codes8(T.m[lo], i, live);
+            const uint32_t w[2] = {c.x, c.y};
+            const int s = T.ms[lo][i >> 7];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = value_m((w[k >> 2] >> (8 * (k & 3))) & 0xffu, s);
+            put8(T.om[lo], i, live, o);
+        }
+        if (T.ov[lo]) {
+            const uint2 c = codes8(T.v[lo], i, live);
+            const uint32_t w[2] = {c.x, c.y};
+            const int s = T.vs[lo][i >> 7];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = value_v((w[k >> 2] >> (8 * (k & 3))) & 0xffu, s);
+            put8(T.ov[lo], i, live, o);
+        }
+    }
+}
+
+template <typename TP, typename TG>
+void enqueue(bool eight, const Table& T, const Step& S, unsigned blocks, hipStream_t stream) {
+    if (eight)
+        hipLaunchKernelGGL((k_adamw<TP, TG, true>), dim3(blocks), dim3(256), 0, stream, T, S);
+    else
+        hipLaunchKernelGGL((k_adamw<TP, TG, false>), dim3(blocks), dim3(256), 0, stream, T, S);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const moe_adamw_desc& D, const moe_adamw_tensor* t, int n, hipStream_t stream) {
+    Step S{};
+    S.beta1 = D.beta_avg;
+    S.beta2 = D.beta_sq;
+    S.b1 = static_cast<float>(D.beta_avg);
+    S.b2 = static_cast<float>(D.beta_sq);
+    S.n1 = static_cast<float>(1.0 - D.beta_avg);
+    S.n2 = static_cast<float>(1.0 - D.beta_sq);
+    S.c1 = 1.0 - std::pow(D.beta_avg, D.step);
+    S.c2 = 1.0 - std::pow(D.beta_sq, D.step);
+    S.lr = D.lr;
+    S.eps = D.eps;
+    S.wd = D.weight_decay;
+    S.step = D.step;
+    S.seed = D.seed;
+    S.lr_dev = D.lr_device;
+    S.step_dev = D.step_device;
+    S.grad_scale = D.grad_scale;
+    const bool p16 = D.param_dtype == MOE_BF16, g16 = D.grad_dtype == MOE_BF16, eight = D.moment_bits == 8;
+    Table T{};
+    int64_t blocks = 0;
+    auto flush = [&]() {
+        if (T.n == 0) return hipSuccess;
+        const unsigned b = static_cast<unsigned>(blocks);
+        if (p16) g16 ? enqueue<bf16_t, bf16_t>(eight, T, S, b, stream) : enqueue<bf16_t, float>(eight, T, S, b, stream);
+        else g16 ? enqueue<float, bf16_t>(eight, T, S, b, stream) : enqueue<float, float>(eight, T, S, b, stream);
+        T.n = 0;
+        blocks = 0;
+        return hipGetLastError();
+    };
+    for (int i = 0; i < n; ++i) {
+        if (t[i].n == 0) continue;
+        const int64_t nb = (t[i].n + kChunk - 1) / kChunk;
+        // (base + slot is a tensor's number: an empty tensor in between begins a new launch)
+        if (T.n == kTensors || blocks + nb >= (1 << 24) || (T.n && T.base + T.n != i)) {
+            const hipError_t err = flush();
+            if (err != hipSuccess) return err;
+        }
+        if (T.n == 0) T.base = i;
+        T.t[T.n] = t[i];
+        T.first[T.n++] = static_cast<uint32_t>(blocks);
+        blocks += nb;
+    }
+    return flush();
+}
+
+hipError_t launch_adamw_moments(const moe_adamw_tensor* t, float* const* avg, float* const* sq, int n,
+                                hipStream_t stream) {
+    MomentsTable T{};
+    int64_t blocks = 0;
+    auto flush = [&]() {
+        if (T.n == 0) return hipSuccess;
+        hipLaunchKernelGGL(k_moments, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, T);
+        T.n = 0;
+        blocks = 0;
+        return hipGetLastError();
+    };
+    for (int i = 0; i < n; ++i) {
+        float *om = avg ? avg[i] : nullptr, *ov = sq ? sq[i] : nullptr;
+        if (t[i].n == 0 || (!om && !ov)) continue;
+        const int64_t nb = (t[i].n + kChunk - 1) / kChunk;
+        if (T.n == kTensors || blocks + nb >= (1 << 24)) {
+            const hipError_t err = flush();
+            if (err != hipSuccess) return err;
+        }
+        const int k = T.n++;
+        T.m[k] = static_cast<const uint8_t*>(t[i].exp_avg);
+        T.v[k] = static_cast<const uint8_t*>(t[i].exp_avg_sq);
+        T.ms[k] = t[i].exp_avg_scale;
+        T.vs[k] = t[i].exp_avg_sq_scale;
+        T.om[k] = om;
+        T.ov[k] = ov;
+        T.len[k] = t[i].n;
+        T.first[k] = static_cast<uint32_t>(blocks);
+        blocks += nb;
+    }
+    return flush();
+}
+
+}  // namespace moe

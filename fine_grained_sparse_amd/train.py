@@ -25,12 +25,15 @@ import os
 
 import torch
 
-from . import HERE, LayerDesc, MoeError, _current_raw_stream, _DT, _Nothing, _default_ws, _need, _ptr, desc
+from . import HERE, ExpertWeights, LayerDesc, MoeError, _current_raw_stream, _DT, _Nothing, _default_ws, _need, _ptr, desc
 from . import lib as _moe_lib
 
 TRAIN_LIB_PATH = os.path.join(HERE, "libmoe_train.so")
 TRAIN_EXPORTS = ("moe_router_train", "moe_balance_workspace_size", "moe_balance_loss", "moe_gate_backward",
-                 "moe_router_backward_workspace_size", "moe_router_backward")
+                 "moe_router_backward_workspace_size", "moe_router_backward",
+                 "moe_dispatch_workspace_size", "moe_dispatch", "moe_sort_tokens", "moe_sort_tokens_backward",
+                 "moe_combine", "moe_combine_backward", "moe_experts_max_rows", "moe_experts_forward",
+                 "moe_experts_backward_workspace_size", "moe_experts_backward", "moe_adamw", "moe_adamw_moments")
 
 
 _NOTHING = _Nothing()
@@ -63,8 +66,26 @@ def train_lib():
         L.moe_router_backward_workspace_size.argtypes = [D]
         L.moe_router_backward_workspace_size.restype = size
         L.moe_router_backward.argtypes = [D, vp, vp, vp, vp, vp, B, vp, vp, vp, vp, vp, size, vp]
-        for n in ("moe_router_train", "moe_balance_loss", "moe_gate_backward", "moe_router_backward"):
-            getattr(L, n).restype = ctypes.c_int
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        L.moe_dispatch_workspace_size.argtypes = [D]
+        L.moe_dispatch_workspace_size.restype = size
+        L.moe_dispatch.argtypes = [D, vp, i32] + [vp] * 6 + [size, vp]
+        L.moe_sort_tokens.argtypes = [D, vp, vp, i64, vp, vp]
+        L.moe_sort_tokens_backward.argtypes = [D, vp, vp, vp, i64, vp, vp]
+        L.moe_combine.argtypes = [D, vp, vp, vp, vp, i64, vp, vp]
+        L.moe_combine_backward.argtypes = [D, vp, vp, vp, vp, i64, vp, vp, vp]
+        W = ctypes.POINTER(ExpertWeights)
+        L.moe_experts_max_rows.argtypes = [D]
+        L.moe_experts_max_rows.restype = i64
+        L.moe_experts_forward.argtypes = [D, i64, vp, vp, W, vp, vp, vp, vp]
+        L.moe_experts_backward_workspace_size.argtypes = [D, i64]
+        L.moe_experts_backward_workspace_size.restype = size
+        L.moe_experts_backward.argtypes = [D, i64, vp, vp, vp, W] + [vp] * 7 + [size, vp]
+        L.moe_adamw.argtypes = [vp, vp, i32, vp]
+        L.moe_adamw_moments.argtypes = [vp, i32, vp, vp, vp]
+        for n in TRAIN_EXPORTS:
+            if not n.endswith(("_size", "_max_rows")):
+                getattr(L, n).restype = ctypes.c_int
         _lib = L
     return _lib
 

@@ -1,9 +1,12 @@
 /*
- * moe_train.h -- C ABI of the router's training side (libmoe_train.so, which
+ * moe_train.h -- C ABI of the layer's training side (libmoe_train.so, which
  * needs libmoe.so): the router with its logits kept, the balance loss with
- * its per-expert counts, and the gradients of both back to x and W_r.
+ * its per-expert counts, and the gradients of both back to x and W_r; the
+ * tokens sorted by expert, the experts on the sorted rows and the weighted sum
+ * back, each with its gradient; and the optimizer's step (their formulas stand
+ * at their declarations).
  *
- * Formulas, with s = sigmoid(z), z = x W_r^T [T, E] and the router of moe.h:
+ * Formulas of the router, with s = sigmoid(z), z = x W_r^T [T, E] and the router of moe.h:
  *   gate weights   w_k = scale s_k / D,  D = sum_{j chosen} s_j + 1e-20;
  *                  dL/ds_k = scale / D (dw_k - sum_j dw_j s_j / D) over the
  *                  chosen experts, 0 elsewhere (the bias only chooses, and
@@ -113,6 +116,156 @@ moe_status moe_router_backward(const moe_layer_desc *desc, const void *x,
                                const int32_t *seq_counts, const float *d_loss,
                                void *dx, float *dW_r, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' side.  An assignment a = t K + k is token t's k-th choice; the
+ * R = T K assignments are sorted by expert into rows, stably (ascending a
+ * within an expert), and the experts work on the rows of x, y, ... in that
+ * order:
+ *   xs[pos[t,k]] = x[t]                  moe_sort_tokens
+ *   y = experts(xs)                      moe_experts_forward
+ *   out[t] = sum_k w[t,k] y[pos[t,k]]    moe_combine
+ * and back: moe_combine_backward (dout to dy and dw, which is the d_topk_w of
+ * moe_router_backward), moe_experts_backward, moe_sort_tokens_backward.
+ *
+ * Descriptor fields used: T, d, E, K, F and act_dtype, with 1 <= K <= 16,
+ * 1 <= E <= 1024, T K < 2^31 and d (F) a positive multiple of 64.  E is the
+ * number of this GPU's experts: K may exceed it.  A row whose place is behind
+ * expert_offsets[E], or outside 0 .. rows - 1, belongs to no assignment: it is
+ * neither read nor written.                                                 */
+
+/* The order.
+ *   topk_idx [T, K] int32; e0: the id of this GPU's first expert; token_mask
+ *   [T] uint8, or NULL: tokens whose byte is 0 have no rows
+ *   -> expert_counts [E] (nullable), expert_offsets [E + 1]: expert e holds
+ *      rows expert_offsets[e] .. expert_offsets[e + 1] - 1; sorted_token [T K]
+ *      (nullable): each row's token (behind the last row it is left as it
+ *      was); pos [T, K]: each assignment's row, -1 for ids outside e0 .. e0 +
+ *      E - 1 and for masked tokens.  An expert chosen twice by a token has two
+ *      rows of it.  All int32.
+ * Workspace of at least moe_dispatch_workspace_size(desc) bytes.             */
+size_t moe_dispatch_workspace_size(const moe_layer_desc *desc);
+moe_status moe_dispatch(const moe_layer_desc *desc, const int32_t *topk_idx,
+                        int32_t e0, const uint8_t *token_mask,
+                        int32_t *expert_counts, int32_t *expert_offsets,
+                        int32_t *sorted_token, int32_t *pos, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* x [T, d] -> xs [rows, d] (act_dtype): xs[pos[t,k]] = x[t]; and its gradient,
+ * dx[t] = residual[t] + sum_k dxs[pos[t,k]], summed in slot order in fp32 and
+ * rounded once.  residual [T, d] may be NULL (0) or dx itself.               */
+moe_status moe_sort_tokens(const moe_layer_desc *desc, const void *x,
+                           const int32_t *pos, int64_t rows, void *xs,
+                           void *stream);
+moe_status moe_sort_tokens_backward(const moe_layer_desc *desc, const void *dxs,
+                                    const int32_t *pos, const void *residual,
+                                    int64_t rows, void *dx, void *stream);
+
+/* out[t] = residual[t] + sum_k topk_w[t,k] y[pos[t,k]], summed in slot order in
+ * fp32 and rounded once: y [rows, d], residual and out [T, d] (act_dtype; residual
+ * NULL for 0, or out itself), topk_w [T, K] fp32.  Its gradients from dout [T, d]:
+ * dy[pos[t,k]] = topk_w[t,k] dout[t], dy [rows, d]; d_topk_w[t,k] = <dout[t],
+ * y[pos[t,k]]>, fp32 [T, K], 0 without a row.  dy or d_topk_w may be NULL (both:
+ * MOE_ERR_NULL); y is needed for d_topk_w, topk_w for dy.  (residual's gradient
+ * is dout.)                                                                  */
+moe_status moe_combine(const moe_layer_desc *desc, const void *y,
+                       const float *topk_w, const int32_t *pos,
+                       const void *residual, int64_t rows, void *out,
+                       void *stream);
+moe_status moe_combine_backward(const moe_layer_desc *desc, const void *dout,
+                                const void *y, const float *topk_w,
+                                const int32_t *pos, int64_t rows, void *dy,
+                                float *d_topk_w, void *stream);
+
+/* The SwiGLU experts on sorted rows, bf16 (act_dtype MOE_BF16, weights of
+ * MOE_LAYOUT_ROWS: W->W_gate, W_up [E, F, d], W->W_down [E, d, F]):
+ *   a = xs W_gate^T, b = xs W_up^T, h = a sigmoid(a) b, y = h W_down^T.
+ *   xs, y [rows, d]; expert_offsets [E + 1] int32, ascending, within 0 .. rows
+ *   gate_up [rows, 2 F] (a, then b, of a row) and h [rows, F] are kept for the
+ *   backward call; gate_up may be NULL.
+ * Sums are kept in fp32; a, b and h are rounded to bf16, h from the unrounded a
+ * and b.  rows at most moe_experts_max_rows(desc) (0 or less: the sizes are out
+ * of range; d F < 2^31).                                                      */
+int64_t moe_experts_max_rows(const moe_layer_desc *desc);
+moe_status moe_experts_forward(const moe_layer_desc *desc, int64_t rows,
+                               const void *xs, const int32_t *expert_offsets,
+                               const moe_expert_weights *W, void *gate_up,
+                               void *h, void *y, void *stream);
+
+/* Its gradients from dy [rows, d], with what the forward call was given and
+ * kept:  dh = dy W_down,  db = dh a s,  da = dh b s (1 + a (1 - s)),  s =
+ * sigmoid(a) (da, db rounded to bf16);
+ *   dxs [rows, d] = da W_gate + db W_up, or NULL;
+ *   dW_gate = da^T xs, dW_up = db^T xs [E, F, d], dW_down = dy^T h [E, d, F],
+ *   all bf16, zero for an expert without rows, or all NULL.
+ * Workspace of at least moe_experts_backward_workspace_size(desc, rows) bytes
+ * (0: out of range).                                                          */
+size_t moe_experts_backward_workspace_size(const moe_layer_desc *desc, int64_t rows);
+moe_status moe_experts_backward(const moe_layer_desc *desc, int64_t rows,
+                                const void *dy, const void *xs,
+                                const int32_t *expert_offsets,
+                                const moe_expert_weights *W,
+                                const void *gate_up, const void *h, void *dxs,
+                                void *dW_gate, void *dW_up, void *dW_down,
+                                void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* ------------------------------------------------------------------------
+ * One AdamW step over many tensors (decoupled weight decay), t = step >= 1:
+ *   g = grad_scale grad,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g g,
+ *   param = (1 - lr weight_decay) param
+ *           - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps).
+ * Moments in 32 bits are fp32.  In 8 bits, 128 consecutive values of a tensor share
+ * a scale 2^(s - 127) (one byte s; s = 255: the block holds NaN, as after an
+ * infinite or NaN moment in it); m is an E4M3 code (sign, 4 exponent bits with
+ * bias 7, 3 fraction bits), v an unsigned code of 5 exponent bits with bias
+ * 15 and 3 fraction bits; the value is code x scale.  A new moment x, computed in
+ * fp32, is rounded to one of its two neighbours at random, up with the
+ * probability that keeps the mean; so is a bf16 parameter.  The random bits are
+ * of (seed, step, the tensor's number in `tensors`, the element): with mix the
+ * finaliser of MurmurHash3 and all sums modulo 2^32,
+ *   word = mix(i % 2^32 + mix(mix(mix(seed) + step) + tensor)
+ *              + (i / 2^32) 0x9e3779b9);
+ * m takes its low 16 bits, v its high ones, a parameter the low ones of
+ * mix(word ^ 0x9e3779b9).                                                     */
+typedef struct {
+    int32_t param_dtype;   /* moe_dtype: MOE_F32 or MOE_BF16                  */
+    int32_t grad_dtype;    /* MOE_F32 or MOE_BF16                             */
+    int32_t moment_bits;   /* 32 or 8                                         */
+    int32_t step;          /* t, from 1 on                                    */
+    uint32_t seed;
+    float lr, eps, weight_decay;
+    double beta_avg, beta_sq;     /* b1, b2 in [0, 1)                         */
+    const float *lr_device;       /* [1] on the device, in place of lr; or NULL */
+    const int32_t *step_device;   /* likewise, in place of step: for a call that
+                                     is captured and replayed                  */
+    const float *grad_scale;      /* [1] on the device, or NULL for 1          */
+} moe_adamw_desc;
+
+/* One tensor of n elements; 16-byte aligned pointers (scales: any).
+ *   copy (may be NULL, and is for bf16 parameters): bf16 [n], receives fp32
+ *   parameters rounded to nearest.
+ *   exp_avg, exp_avg_sq: fp32 [n], or uint8 [n] codes with their scales
+ *   uint8 [(n + 127) / 128] (NULL with 32 bits).                              */
+typedef struct {
+    void *param;
+    const void *grad;
+    void *exp_avg, *exp_avg_sq;
+    uint8_t *exp_avg_scale, *exp_avg_sq_scale;
+    void *copy;
+    int64_t n;
+} moe_adamw_tensor;
+
+/* `tensors` is host memory and is read before the call returns.  A tensor may
+ * be empty (n = 0); no two may overlap.                                      */
+moe_status moe_adamw(const moe_adamw_desc *desc, const moe_adamw_tensor *tensors,
+                     int32_t n_tensors, void *stream);
+
+/* 8-bit moments to the values they stand for: avg[i] and sq[i] (host arrays of
+ * device pointers; an entry, or a whole array, may be NULL) receive fp32 [n] of
+ * tensor i.                                                                  */
+moe_status moe_adamw_moments(const moe_adamw_tensor *tensors, int32_t n_tensors,
+                             float *const *avg, float *const *sq, void *stream);
 
 #ifdef __cplusplus
 }

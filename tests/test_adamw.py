@@ -1,0 +1,289 @@
+"""AdamW over many tensors (include/moe_train.h): refusals on the CPU, and on the
+GPU parameters and moments against float64, the 8-bit codes bit for bit.
+
+Tolerances.  E32 = 2^-24 is half a step of fp32 relative to the value.  m and v
+are two products and a sum: 3 E32 of the terms.  The parameter's change is
+lr / c1 m / (sqrt(v) / sqrt(c2) + eps) with a square root and a reciprocal good to
+a step (2 E32 each) among nine rounded operations: 16 E32 of it, with what m and v
+carry; keeping the parameter adds 3 E32 of it.
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import fine_grained_sparse_amd as moe
+from fine_grained_sparse_amd import optim, train
+from test_abi import ALIGN, FAKE, FAKE_ODD, NULL, OK, SHAPE, UNSUP
+
+E32 = 2.0 ** -24
+DEV = "cuda:0"
+F32, B16 = torch.float32, torch.bfloat16
+
+
+# ------------------------------------------------------------- refusals (CPU)
+def _d(**kw):
+    v = dict(param_dtype=0, grad_dtype=1, moment_bits=32, step=1, seed=0, lr=1e-3, eps=1e-8, weight_decay=0.0,
+             beta_avg=0.9, beta_sq=0.999, lr_device=None, step_device=None, grad_scale=None)
+    v.update(kw)
+    return optim._Desc(**v)
+
+
+def _t(n=10, **kw):
+    v = dict(param=FAKE, grad=FAKE, exp_avg=FAKE, exp_avg_sq=FAKE, exp_avg_scale=None, exp_avg_sq_scale=None, copy=None,
+             n=n)
+    v.update(kw)
+    return optim._Tensor(**v)
+
+
+def test_adamw_rejects_bad_arguments():
+    L = train.train_lib()
+
+    def f(D, *ts, n=None):
+        table = (optim._Tensor * max(len(ts), 1))(*ts)
+        return L.moe_adamw(ctypes.byref(D), table, len(ts) if n is None else n, None)
+    assert L.moe_adamw(None, None, 0, None) == NULL
+    assert L.moe_adamw(ctypes.byref(_d()), None, 1, None) == NULL
+    assert f(_d(), _t(), n=-1) == SHAPE
+    for bad in (dict(step=0), dict(beta_avg=1.0), dict(beta_sq=-0.1), dict(beta_avg=math.nan)):
+        assert f(_d(**bad), _t()) == SHAPE, bad
+    for bad in (dict(param_dtype=2), dict(grad_dtype=3), dict(moment_bits=16)):
+        assert f(_d(**bad), _t()) == UNSUP, bad
+    for name in ("lr_device", "step_device", "grad_scale"):
+        assert f(_d(**{name: FAKE + 2}), _t()) == ALIGN, name
+    for name in ("param", "grad", "exp_avg", "exp_avg_sq"):
+        assert f(_d(), _t(**{name: None})) == NULL, name
+        assert f(_d(), _t(n=0), _t(**{name: FAKE_ODD})) == ALIGN, name
+    assert f(_d(), _t(copy=FAKE_ODD)) == ALIGN
+    assert f(_d(param_dtype=1), _t(copy=FAKE)) == UNSUP
+    assert f(_d(), _t(n=-1)) == SHAPE and f(_d(), _t(n=1 << 36)) == SHAPE
+    assert f(_d(moment_bits=8), _t()) == NULL
+    assert f(_d(moment_bits=8), _t(exp_avg_scale=FAKE)) == NULL
+    assert f(_d(), _t(n=0, param=None, grad=None)) == OK and f(_d()) == OK
+    m = L.moe_adamw_moments
+    ptr = (ctypes.c_void_p * 1)(FAKE_ODD)
+    full = (optim._Tensor * 1)(_t(exp_avg_scale=FAKE, exp_avg_sq_scale=FAKE))
+    assert m(full, -1, ptr, ptr, None) == SHAPE and m(None, 1, ptr, ptr, None) == NULL
+    assert m(full, 1, None, None, None) == NULL and m(full, 1, ptr, None, None) == ALIGN
+    assert m((optim._Tensor * 1)(_t()), 1, ptr, ptr, None) == NULL and m(None, 0, None, None, None) == OK
+
+
+def test_adamw_object_refuses():
+    p = torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.AdamW([p])
+    with pytest.raises(ValueError, match="no parameters"):
+        moe.AdamW([])
+    with pytest.raises(ValueError, match="8 or 32"):
+        moe.AdamW([p], state_bits=16)
+
+
+# ------------------------------------------------------------------- plain form
+def _mix(h):
+    h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
+    h = ((h ^ (h >> 13)) * 0xC2B2AE35) & 0xFFFFFFFF
+    return h ^ (h >> 16)
+
+
+def _word(n, seed, step, tensor):
+    key = _mix((_mix((_mix(torch.tensor(seed & 0xFFFFFFFF)) + step) & 0xFFFFFFFF) + tensor) & 0xFFFFFFFF)
+    return _mix((torch.arange(n) + key) & 0xFFFFFFFF)
+
+
+def _grid(mant, least, top):
+    """The non-negative numbers of `mant` fraction bits with exponents least .. top, subnormals and 0 among them."""
+    step = 2.0 ** -mant
+    v = [i * step * 2.0 ** least for i in range(2 ** mant)]
+    for e in range(least, top + 1):
+        v += [(1 + i * step) * 2.0 ** e for i in range(2 ** mant)]
+    return torch.tensor(v, dtype=torch.float64)
+
+
+E4M3, E5M3 = _grid(3, -6, 8), _grid(3, -14, 16)
+
+
+def _encode(x, grid, top, r16):
+    """Codes and scales of blocks of 128 fp32 values, by search in the table of numbers."""
+    n = x.numel()
+    codes, scales = torch.zeros(n, dtype=torch.int64), []
+    for b in range(0, n, 128):
+        v = x[b:b + 128].double().abs()
+        big = float(v.max())
+        e = max(math.frexp(big)[1] - 1 - top, -127) if big else -127
+        y = v / 2.0 ** e
+        lo = torch.searchsorted(grid, y, right=True) - 1
+        width = grid[(lo + 1).clamp(max=len(grid) - 1)] - grid[lo]
+        part = torch.floor((y - grid[lo]) / width * 2 ** 20)
+        codes[b:b + 128] = lo + ((part + r16[b:b + 128] * 16 + 8) >= 2 ** 20).long()
+        scales.append(e + 127)
+    return codes, torch.tensor(scales)
+
+
+def _decode(c, s, grid):
+    return grid[c] * (2.0 ** (s.double() - 127)).repeat_interleave(128)[:c.numel()]
+
+
+SIZES = [1, 7, 128, 129, 0, 1000, 4096, 8191, 8192, 8193, 20001] + [5 + 3 * i for i in range(60)]
+
+
+def _tensors(dt, gdt, seed, sizes=SIZES):
+    g = torch.Generator().manual_seed(seed)
+    ps = [(torch.randn(n, generator=g) * 0.05).to(dt) for n in sizes]
+    gs = [(torch.randn(n, generator=g) * 10.0 ** float(torch.empty(1).uniform_(-6, 0, generator=g))).to(gdt) for n in sizes]
+    return ps, gs
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("copies", [False, True])
+@pytest.mark.parametrize("gdt", [F32, B16])
+def test_fp32_moments_against_float64(gdt, copies):
+    ps, gs = _tensors(F32, gdt, 1)
+    dev = [p.to(DEV) for p in ps]
+    cp = [torch.full(p.shape, 7.0, dtype=B16, device=DEV) if i % 3 else None for i, p in enumerate(ps)] if copies else None
+    opt = moe.AdamW(dev, lr=0.01, betas=(0.8, 0.99), eps=1e-6, weight_decay=0.1, copies=cp)
+    P, M, V = [p.double() for p in ps], [torch.zeros(p.shape, dtype=torch.float64) for p in ps], None
+    V = [m.clone() for m in M]
+    bound = [torch.zeros_like(m) for m in M]
+    for t in range(1, 5):
+        _, gs = _tensors(F32, gdt, 10 + t)
+        opt.step([g.to(DEV) for g in gs])
+        for i, g in enumerate(gs):
+            g = g.double()
+            M[i], V[i] = 0.8 * M[i] + 0.2 * g, 0.99 * V[i] + 0.01 * g * g
+            change = 0.01 / (1 - 0.8 ** t) * M[i].abs() / (torch.sqrt(V[i] / (1 - 0.99 ** t)) + 1e-6)
+            # m's own error is 3 E32 of |b1 m| + |(1 - b1) g| a step, not of what is left of them
+            mag = 0.01 / (1 - 0.8 ** t) * (M[i].abs() + 3 * 0.2 * g.abs()) / (torch.sqrt(V[i] / (1 - 0.99 ** t)) + 1e-6)
+            P[i] = P[i] * (1 - 0.001) - torch.sign(M[i]) * change
+            bound[i] += (3 * P[i].abs() + 16 * t * mag) * E32
+    for i in range(len(ps)):
+        assert ((dev[i].cpu().double() - P[i]).abs() <= 2 * bound[i]).all(), i
+        assert ((opt.exp_avg_sq[i].cpu().double() - V[i]).abs() <= 4 * 4 * E32 * V[i] + 1e-45).all(), i
+        if copies and i % 3:
+            assert torch.equal(cp[i], dev[i].to(B16))
+    assert opt.steps == 4 and opt.moments() == (opt.exp_avg, opt.exp_avg_sq)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt,gdt", [(F32, F32), (F32, B16), (B16, B16), (B16, F32)])
+def test_eight_bit_moments_bit_for_bit(dt, gdt):
+    ps, gs = _tensors(dt, gdt, 2)
+    dev = [p.to(DEV) for p in ps]
+    b1, b2, lr, eps, wd, seed = 0.9, 0.999, 1e-2, 1e-8, 0.01, 2 ** 40 + 77
+    opt = moe.AdamW(dev, state_bits=8, lr=lr, betas=(b1, b2), eps=eps, weight_decay=wd, seed=seed)
+    f = lambda v: torch.tensor(v, dtype=F32)  # noqa: E731
+    C = [[torch.zeros(n, dtype=torch.int64), torch.zeros((n + 127) // 128, dtype=torch.int64)] * 2 for n in SIZES]
+    sign = [torch.zeros(n, dtype=torch.int64) for n in SIZES]
+    for t in range(1, 4):
+        _, gs = _tensors(dt, gdt, 20 + t)
+        before = [p.cpu() for p in dev]
+        opt.step([g.to(DEV) for g in gs])
+        got_m, got_v = opt.moments()
+        for i, n in enumerate(SIZES):
+            if n == 0:
+                continue
+            g = gs[i].float()
+            m = _decode(C[i][0], C[i][1], E4M3).float() * (1 - 2 * sign[i]).float()
+            v = _decode(C[i][2], C[i][3], E5M3).float()
+            m = m * f(b1) + g * f(1 - b1)          # fp32, every operation rounded
+            v = v * f(b2) + g * f(1 - b2) * g
+            w = _word(n, seed, t, i)
+            cm, sm = _encode(m, E4M3, 7, w & 0xFFFF)
+            cv, sv = _encode(v, E5M3, 15, w >> 16)
+            C[i], sign[i] = [cm, sm, cv, sv], (torch.signbit(m)).long()
+            assert torch.equal(opt.exp_avg[i].cpu().long(), cm + 128 * sign[i]), (t, i)
+            assert torch.equal(opt.exp_avg_sq[i].cpu().long(), cv), (t, i)
+            assert torch.equal(opt.exp_avg_scale[i].cpu().long(), sm) and torch.equal(opt.exp_avg_sq_scale[i].cpu().long(), sv)
+            assert torch.equal(got_m[i].cpu().double(), _decode(cm, sm, E4M3) * (1 - 2 * sign[i]))
+            assert torch.equal(got_v[i].cpu().double(), _decode(cv, sv, E5M3))
+            m, v, p = m.double(), v.double(), before[i].double()
+            change = lr / (1 - b1 ** t) * m / (torch.sqrt(v / (1 - b2 ** t)) + eps)
+            want, tol = p * (1 - lr * wd) - change, (3 * p.abs() + 16 * change.abs()) * E32
+            q = dev[i].cpu().double()
+            if dt is F32:
+                assert ((q - want).abs() <= tol).all(), (t, i)
+            else:  # one of the two neighbours, as the random bits say
+                lo = torch.tensor([(x.item() >> 16) << 16 for x in want.float().view(torch.int32)]).int().view(F32).double()
+                assert ((q - want).abs() < 2.0 ** -7 * want.abs() + tol).all(), (t, i)
+                r = _mix(w ^ 0x9E3779B9) & 0xFFFF
+                up = ((want.float().view(torch.int32).long() & 0xFFFF) + r) >> 16
+                exact = (up == 1) == (q.abs() > lo.abs())
+                assert exact.float().mean() > 0.99 or (~exact).sum() <= 1
+
+
+@pytest.mark.gpu
+def test_random_rounding_keeps_the_mean():
+    """v of a constant gradient approaches its square, where rounding to nearest would leave it at its start."""
+    n = 1 << 16
+    p, g = torch.zeros(n, device=DEV), torch.full((n,), 1.0, device=DEV)
+    opt = moe.AdamW([p], state_bits=8, lr=0.0, betas=(0.9, 0.99))
+    opt.exp_avg_sq[0].fill_(0xF0)            # 2^15 in units of the scale
+    opt.exp_avg_sq_scale[0].fill_(127 - 15 + 2)  # v = 4 everywhere
+    vals = []
+    for _ in range(60):
+        opt.step([g])
+        vals.append(float(opt.moments()[1][0].double().mean()))
+    want = [1 + 3 * 0.99 ** (t + 1) for t in range(60)]
+    # a value's variance grows a step by at most change x grid step (0.03 x 0.5), over n values
+    for t, (a, b) in enumerate(zip(vals, want)):
+        assert abs(a - b) <= 6 * math.sqrt(0.03 * 0.5 * (t + 1) / n), (t, a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_infinities_and_nan(bits):
+    n = 512
+    g = torch.randn(n, generator=torch.Generator().manual_seed(1)) * 1e-3
+    clean, p = torch.ones(n, device=DEV), torch.ones(n, device=DEV)
+    a, b = moe.AdamW([clean], state_bits=bits), moe.AdamW([p], state_bits=bits)
+    a.step([g.to(DEV)])
+    bad = g.clone()
+    bad[5], bad[300] = math.nan, math.inf
+    b.step([bad.to(DEV)])
+    same = [i for i in range(n) if i not in (5, 300)]
+    assert torch.equal(p[same], clean[same]) and p[5].isnan() and not p[300].isfinite()
+    m, v = b.moments()
+    if bits == 8:  # the block's scale is lost with it
+        assert m[0][:128].isnan().all() and v[0][256:384].isnan().all()
+        assert torch.equal(m[0][128:256], a.moments()[0][0][128:256]) and m[0][384:].isfinite().all()
+    # tiny and zero gradients
+    z = torch.zeros(n, device=DEV)
+    q = torch.ones(n, device=DEV)
+    c = moe.AdamW([q], state_bits=bits, weight_decay=0.0)
+    c.step([z])
+    assert (q == 1).all() and (c.moments()[1][0] == 0).all()
+    c.step([torch.full((n,), 1e-20, device=DEV)])
+    assert q.isfinite().all() and c.moments()[0][0].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_captured_with_a_step_on_the_device(bits):
+    ps, _ = _tensors(F32, F32, 3)
+    eager, graph = [p.to(DEV) for p in ps], [p.to(DEV) for p in ps]
+    grads = [torch.zeros(p.shape, device=DEV) for p in ps]
+    a = moe.AdamW(eager, state_bits=bits, seed=3, grads=grads)
+    b = moe.AdamW(graph, state_bits=bits, seed=3, grads=grads)
+    step, lr = torch.zeros(1, dtype=torch.int32, device=DEV), torch.full((1,), 1e-3, device=DEV)
+    scale = torch.ones(1, device=DEV)
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        step.add_(1)
+        b.step(lr=lr, step=step, grad_scale=scale)
+    for t in range(1, 6):
+        _, gs = _tensors(F32, F32, 40 + t)
+        for d, v in zip(grads, gs):
+            d.copy_(v)
+        lr.fill_(1e-3 * t)
+        scale.fill_(0.5 * t)
+        g.replay()
+        a.step(lr=1e-3 * t, grad_scale=torch.full((1,), 0.5 * t, device=DEV))
+        torch.cuda.synchronize()
+        assert int(step) == t == a.steps and b.steps == 0
+        for i in range(len(ps)):
+            assert torch.equal(a.exp_avg[i], b.exp_avg[i]) and torch.equal(a.exp_avg_sq[i], b.exp_avg_sq[i]), (t, i)
+            # (1 - beta^t by repeated squaring on the device, and lr as fp32: a few steps of fp32 in the rate)
+            assert ((eager[i] - graph[i]).abs() <= 16 * t * E32 * (0.02 * t + eager[i].abs())).all(), (t, i)
+        torch.randn(256, 256, device=DEV).sum().item()
