@@ -8,9 +8,10 @@
 //   EXP_DX       dx = da W_gate + db W_up       rows x d,      K = 2 F
 //   EXP_DW_DOWN  dW_down = dy^T h               d x F,         K = rows
 //   EXP_DW_UP    [dW_gate; dW_up] = [da; db]^T x   2 F x d,    K = rows
-// h, a, b, da and db are rounded to bf16, as the activations of the layer are
-// (each then carries half a step, 2^-9 on average, into sums of hundreds of
-// terms whose own result is rounded to bf16).
+// h, da and db are rounded to bf16, as the activations of the layer are.  a and b are
+// kept in fp32 between the calls: in bf16 they would add as much to the gradients' error as
+// all else (dW_gate and dx of normal rows: 3.1e-3 of the 2-norm against 2.4e-3, of
+// which 1.7e-3 is the result's own rounding), and they are 2% of the bytes at 683 rows an expert.
 #include <type_traits>
 
 #include "common.hpp"
@@ -33,13 +34,12 @@ namespace {
 // A are replaced one by one under the slab's last products.
 //
 // Rows operand: a 1 KiB block holds 16 rows x 32 k; 16-byte chunk c of row r at r
-// 64 + (c ^ (r / 4 % 4)) 16, so that four neighbouring lanes load 64 bytes of a
-// row and sixteen lanes that read one chunk of sixteen rows meet every bank once.
-// Columns operand: a block holds 2 k x 256 columns; with f = r % 4 + 4 (r / 8 % 2), 32-byte
-// chunk c of row r of A sits at c ^ f, 64-byte chunk c of B (whose lanes read every
-// other 8 bytes of one) at c ^ f: rows that are read together differ in f.
-// The 16 n of fragments j and j + 1 (j even) are interleaved by fours, so that the
-// eight results of a lane in both are eight neighbouring columns: 16-byte stores.
+// 64 + (c ^ (r / 2 % 4)) 16, so that four neighbouring lanes load 64 bytes of a
+// row, and eight lanes that read one chunk of eight rows meet all banks once.
+// Columns operand: a block holds 2 k x 256 columns; 32-byte chunk c of row r at c
+// ^ (r % 4 + 4 (r / 8 % 2)) (see k_dw).
+// A lane has four neighbouring columns of each product; two of them are exchanged
+// between the lanes of neighbouring groups of 16 for eight: 16-byte stores.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ void dma(const char* base, uint32_t off, uint32_t lds) {
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const Expert
             const int r = 2 * q + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
             oa[k] = static_cast<uint32_t>(r * lda + min(job.m0 + c * 8, M - 8)) * 2;
         } else {
-            const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 4) & 3);
+            const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 3) & 3);
             oa[k] = static_cast<uint32_t>(min(q * 16 + r, M - 1 - job.m0) * lda + c * 8) * 2;
         }
     }
@@ -182,14 +182,13 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const Expert
     for (int k = 0; k < S::LB; ++k) {
         const int q = wid + 4 * k;
         if (S::kBCol) {
-            const int r = 2 * q + (lane >> 5), c = ((((lane & 31) >> 2) ^ fl(r)) << 2) | (lane & 3);
+            const int r = 2 * q + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
             ob[k] = static_cast<uint32_t>(r * ldb + min(n0 + c * 8, N - 8)) * 2;
         } else {
-            const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 4) & 3);
+            const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 3) & 3);
             // EXP_UP: half of a wave's fragments are of W_gate, the other half the same of W_up
             const int f = S::kPair ? q / NJ * (NJ / 2) + q % (NJ / 2) : q;
-            const int n = n0 + 32 * (f >> 1) + 8 * (r >> 2) + (r & 3) + 4 * (f & 1);
-            ob[k] = static_cast<uint32_t>(min(n, N - 1) * ldb + c * 8) * 2;
+            ob[k] = static_cast<uint32_t>(min(n0 + f * 16 + r, N - 1) * ldb + c * 8) * 2;
         }
     }
     // Slab b's k-th load of this wave.  Every call issues one instruction, so that
@@ -232,7 +231,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const Expert
             }
             return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
         }
-        return *reinterpret_cast<const uint4*>(lds + o + (wm * MI + i) * 1024 + r16 * 64 + ((grp ^ (r16 >> 2)) << 4));
+        return *reinterpret_cast<const uint4*>(lds + o + (wm * MI + i) * 1024 + r16 * 64 + ((grp ^ ((r16 >> 1) & 3)) << 4));
     };
     auto read_b = [&](int b, int j) -> uint4 {
         const uint32_t o = (b & 3) * S::kSlot + S::NA * 1024;
@@ -242,12 +241,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const Expert
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int r = 8 * grp + (r16 >> 2) + 4 * u;
-                // four columns 8 (r16 % 4) + 4 (f % 2) .. of the 32 of fragments f and f ^ 1
-                h[u] = tr(o + r * 512 + (((f >> 1) ^ fl(r)) << 6) + (r16 & 3) * 16 + (f & 1) * 8);
+                h[u] = tr(o + r * 512 + ((f ^ fl(r)) << 5) + (r16 & 3) * 8);
             }
             return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
         }
-        return *reinterpret_cast<const uint4*>(lds + o + f * 1024 + r16 * 64 + ((grp ^ (r16 >> 2)) << 4));
+        return *reinterpret_cast<const uint4*>(lds + o + f * 1024 + r16 * 64 + ((grp ^ ((r16 >> 1) & 3)) << 4));
     };
 
     f32x4 acc[MI][NJ];
@@ -304,43 +302,46 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const Expert
         }
     }
 
-    // acc[i][2 j'], acc[i][2 j' + 1] of a lane: row 16 i + r16, columns 32 j' + 8 grp .. + 7
+    // A lane's part of fragments j and j + 1 of row 16 i + r16: columns 16 j + nl .. + 7,
+    // nl = 16 (grp % 2) + 8 (grp / 2), once the odd groups' j and the even groups' j + 1 are exchanged.
+    const int nl = 16 * (grp & 1) + 8 * (grp >> 1);
     auto eight = [&](int i, int j, float (&v)[8]) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            v[u] = acc[i][j][u];
-            v[4 + u] = acc[i][j + 1][u];
+            const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][u]), __float_as_uint(acc[i][j + 1][u]),
+                                                            false, false);
+            v[u] = __uint_as_float(q[0]);
+            v[4 + u] = __uint_as_float(q[1]);
         }
     };
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const int m = job.m0 + (wm * MI + i) * 16 + r16;
-        if (m >= M) continue;
         if (KIND == EXP_UP) {
             const int64_t row = job.r0 + m;
 #pragma unroll
             for (int j = 0; j < NJ / 2; j += 2) {
-                const int n = n0 + (wn * NJ / 2 + j) * 16 + grp * 8;
-                if (n >= N) continue;
+                const int n = n0 + (wn * NJ / 2 + j) * 16 + nl;
                 float g[8], u[8], h[8];
                 eight(i, j, g);
                 eight(i, j + NJ / 2, u);
+                if (m >= M || n >= N) continue;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
-                if (a.C) {
-                    stg16(a.C + row * 2 * F + n, pack8v(g));
-                    stg16(a.C + row * 2 * F + F + n, pack8v(u));
+                if (a.gu) {
+                    pack8(a.gu + row * 2 * F + n, g);
+                    pack8(a.gu + row * 2 * F + F + n, u);
                 }
-                stg16(a.C2 + row * F + n, pack8v(h));
+                stg16(a.C + row * F + n, pack8v(h));
             }
         } else if (KIND == EXP_DH) {
             const int64_t row = job.r0 + m;
 #pragma unroll
             for (int j = 0; j < NJ; j += 2) {
-                const int n = n0 + (wn * NJ + j) * 16 + grp * 8;
-                if (n >= N) continue;
+                const int n = n0 + (wn * NJ + j) * 16 + nl;
                 float dh[8], g[8], u[8], dg[8], du[8];
                 eight(i, j, dh);
+                if (m >= M || n >= N) continue;
                 unpack8(a.gu + row * 2 * F + n, g);
                 unpack8(a.gu + row * 2 * F + F + n, u);
 #pragma unroll
@@ -362,10 +363,10 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const Expert
                 out = a.C + (job.r0 + m) * d;
 #pragma unroll
             for (int j = 0; j < NJ; j += 2) {
-                const int n = n0 + (wn * NJ + j) * 16 + grp * 8;
-                if (n >= N) continue;
+                const int n = n0 + (wn * NJ + j) * 16 + nl;
                 float v[8];
                 eight(i, j, v);
+                if (m >= M || n >= N) continue;
                 stg16(out + n, pack8v(v));
             }
         }

@@ -32,8 +32,8 @@ enum ExpertsKind { EXP_UP, EXP_DOWN, EXP_DH, EXP_DX, EXP_DW_DOWN, EXP_DW_UP };
 struct ExpertsArgs {
     const int32_t* off;
     const uint16_t *A, *B, *B2;  // B2: W_up beside W_gate
-    const uint16_t* gu;          // EXP_DH: the saved [R, 2 F]
-    uint16_t *C, *C2;            // EXP_UP: gu (may be null) and h; EXP_DW_UP: dW_gate and dW_up
+    float* gu;                   // [R, 2 F]: a and b, written by EXP_UP (may be null), read by EXP_DH
+    uint16_t *C, *C2;            // EXP_DW_UP: dW_gate and dW_up
     int64_t R;
     int32_t E, d, F;
 };

@@ -155,7 +155,7 @@ int64_t moe_experts_max_rows(const moe_layer_desc* desc) {
 }
 
 moe_status moe_experts_forward(const moe_layer_desc* desc, int64_t rows, const void* xs, const int32_t* expert_offsets,
-                               const moe_expert_weights* W, void* gate_up, void* h, void* y, void* stream) {
+                               const moe_expert_weights* W, float* gate_up, void* h, void* y, void* stream) {
     const moe_status st = check_experts(desc, rows);
     if (st != MOE_OK) return st;
     if (rows == 0) return MOE_OK;
@@ -166,8 +166,8 @@ moe_status moe_experts_forward(const moe_layer_desc* desc, int64_t rows, const v
     a.A = in(xs);
     a.B = in(W->W_gate);
     a.B2 = in(W->W_up);
-    a.C = out(gate_up);
-    a.C2 = out(h);
+    a.gu = gate_up;
+    a.C = out(h);
     MOE_HIP(launch_experts(EXP_UP, a, s));
     a.A = in(h);
     a.B = in(W->W_down);
@@ -182,7 +182,7 @@ size_t moe_experts_backward_workspace_size(const moe_layer_desc* desc, int64_t r
 }
 
 moe_status moe_experts_backward(const moe_layer_desc* desc, int64_t rows, const void* dy, const void* xs,
-                                const int32_t* expert_offsets, const moe_expert_weights* W, const void* gate_up,
+                                const int32_t* expert_offsets, const moe_expert_weights* W, const float* gate_up,
                                 const void* h, void* dxs, void* dW_gate, void* dW_up, void* dW_down, void* workspace,
                                 size_t workspace_bytes, void* stream) {
     const moe_status st = check_experts(desc, rows);
@@ -205,7 +205,7 @@ moe_status moe_experts_backward(const moe_layer_desc* desc, int64_t rows, const 
     ExpertsArgs a = experts_args(desc, rows, expert_offsets);
     a.A = in(dy);
     a.B = in(W->W_down);
-    a.gu = in(gate_up);
+    a.gu = const_cast<float*>(gate_up);
     a.C = out(workspace);
     MOE_HIP(launch_experts(EXP_DH, a, s));
     if (dw) {

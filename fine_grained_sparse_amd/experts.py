@@ -41,7 +41,7 @@ class Order(NamedTuple):
 
 
 class Saved(NamedTuple):
-    """What experts_backward needs of the forward call, bf16: gate_up [rows, 2 F], h [rows, F]."""
+    """What experts_backward needs of the forward call: gate_up fp32 [rows, 2 F], h bf16 [rows, F]."""
     gate_up: torch.Tensor
     h: torch.Tensor
 
@@ -217,7 +217,7 @@ def experts_forward(xs, offsets, weights, *, save=True, out=None, stream=None):
     with ctx:
         y = torch.empty_like(xs) if out is None else out
         _need(y, "out", torch.bfloat16, (R, d), dev)
-        gu = torch.empty((R, 2 * F), dtype=torch.bfloat16, device=dev) if save else None
+        gu = torch.empty((R, 2 * F), dtype=torch.float32, device=dev) if save else None
         h = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
         _call("moe_experts_forward", D, R, _ptr(xs), _ptr(offsets), ctypes.byref(W), _ptr(gu), _ptr(h), _ptr(y), s)
     return y, Saved(gu, h) if save else None
@@ -231,7 +231,7 @@ def experts_backward(dy, xs, offsets, weights, saved, *, need_dx=True, need_dW=T
     gradients."""
     R, E, d, F, dev, W = _expert_args(dy, "dy", offsets, weights)
     _need(xs, "xs", torch.bfloat16, (R, d), dev)
-    _need(saved.gate_up, "saved.gate_up", torch.bfloat16, (R, 2 * F), dev)
+    _need(saved.gate_up, "saved.gate_up", torch.float32, (R, 2 * F), dev)
     _need(saved.h, "saved.h", torch.bfloat16, (R, F), dev)
     if not (need_dx or need_dW):
         raise ValueError("neither dxs nor the weights' gradients are wanted")

@@ -74,8 +74,8 @@ class AdamW:
                 raise ValueError(f"{name}: {len(given)} tensors for {len(params)} parameters")
             for g, p in zip(given, params):
                 _need(g, name, dtype, device=dev)
-                if g.numel() != p.numel() and dtype is sdt or g.numel() < size(p):
-                    raise ValueError(f"{name} has {g.numel()} values for a parameter of {p.numel()}")
+                if g.numel() != size(p):
+                    raise ValueError(f"{name} has {g.numel()} values, a parameter of {p.numel()} needs {size(p)}")
             return given
         self.exp_avg = state(exp_avg, "exp_avg", torch.Tensor.numel, sdt)
         self.exp_avg_sq = state(exp_avg_sq, "exp_avg_sq", torch.Tensor.numel, sdt)

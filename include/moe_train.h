@@ -181,15 +181,14 @@ moe_status moe_combine_backward(const moe_layer_desc *desc, const void *dout,
  * MOE_LAYOUT_ROWS: W->W_gate, W_up [E, F, d], W->W_down [E, d, F]):
  *   a = xs W_gate^T, b = xs W_up^T, h = a sigmoid(a) b, y = h W_down^T.
  *   xs, y [rows, d]; expert_offsets [E + 1] int32, ascending, within 0 .. rows
- *   gate_up [rows, 2 F] (a, then b, of a row) and h [rows, F] are kept for the
- *   backward call; gate_up may be NULL.
- * Sums are kept in fp32; a, b and h are rounded to bf16, h from the unrounded a
- * and b.  rows at most moe_experts_max_rows(desc) (0 or less: the sizes are out
+ *   gate_up [rows, 2 F] fp32 (a, then b, of a row) and h [rows, F] are kept for
+ *   the backward call; gate_up may be NULL.
+ * Sums are kept in fp32; h is rounded to bf16.  rows at most moe_experts_max_rows(desc) (0 or less: the sizes are out
  * of range; d F < 2^31).                                                      */
 int64_t moe_experts_max_rows(const moe_layer_desc *desc);
 moe_status moe_experts_forward(const moe_layer_desc *desc, int64_t rows,
                                const void *xs, const int32_t *expert_offsets,
-                               const moe_expert_weights *W, void *gate_up,
+                               const moe_expert_weights *W, float *gate_up,
                                void *h, void *y, void *stream);
 
 /* Its gradients from dy [rows, d], with what the forward call was given and
@@ -205,7 +204,7 @@ moe_status moe_experts_backward(const moe_layer_desc *desc, int64_t rows,
                                 const void *dy, const void *xs,
                                 const int32_t *expert_offsets,
                                 const moe_expert_weights *W,
-                                const void *gate_up, const void *h, void *dxs,
+                                const float *gate_up, const void *h, void *dxs,
                                 void *dW_gate, void *dW_up, void *dW_down,
                                 void *workspace, size_t workspace_bytes,
                                 void *stream);

@@ -5,7 +5,7 @@ and every gradient against float64.
 Tolerances.  E32 = 2^-24 and U = 2^-8 are half a step of fp32 and bf16 relative
 to the value.  A sum of n products in fp32 carries at most n E32 of the sum of
 their absolute values, whatever its order; an output rounded to bf16 U of its
-value on top.  The experts' a, b, h, da and db are rounded to bf16, so their
+value on top.  The experts' h, da and db are rounded to bf16, so their
 products are compared with float64 under the same roundings: what is then left
 is the output's own rounding, and roundings that fall on the other side because
 of the fp32 sums (relative errors of some 1e-6 against a step of 2^-7: about one
@@ -332,7 +332,7 @@ def _b(t):
 
 
 def _experts_ref(xs, dy, W, sizes, first=0):
-    """float64 on the GPU, expert by expert, with a, b, h, da, db rounded to bf16 as stated."""
+    """float64 on the GPU, expert by expert, with h, da, db rounded to bf16 as stated."""
     d, F = xs.shape[1], W["W_gate"].shape[1]
     r = {"y": torch.zeros_like(xs, dtype=torch.float64), "dxs": torch.zeros_like(xs, dtype=torch.float64)}
     r |= {n: torch.zeros(w.shape, dtype=torch.float64, device=w.device) for n, w in W.items()}
@@ -345,7 +345,7 @@ def _experts_ref(xs, dy, W, sizes, first=0):
         a, b = x @ wg.T, x @ wu.T
         h = _b(a * torch.sigmoid(a) * b)
         r["y"][at:at + n] = h @ wd.T
-        a, b, dh = _b(a), _b(b), g @ wd
+        dh = g @ wd
         s = torch.sigmoid(a)
         db, da = _b(dh * a * s), _b(dh * b * s * (1 + a * (1 - s)))
         r["dxs"][at:at + n] = da @ wg + db @ wu
@@ -510,7 +510,8 @@ def test_training_step_of_the_layer_against_autograd(T, d, E, K, F):
             rows.append(P["W_down"][e] @ (a * torch.sigmoid(a) * c))
         out = out + w[:, k:k + 1] * torch.stack(rows)
     (out * dout.double().cpu()).sum().backward()
-    # norm-wise, at most seven roundings to bf16 on the way to a gradient (y, dy, a, b, h, da or db, the output): U each
+    # norm-wise, at most five roundings to bf16 on the way to a gradient (y, dy, h, da or db, the output): U each, but for
+    # the gradient through w, whose <dout, y> cancels: seven in all
     for n, ref in dict(out=out.detach(), dx=P["x"].grad, dW_r=P["W_r"].grad, **{n: P[n].grad for n in W}).items():
         err = float((got[n].double().cpu() - ref).norm() / ref.norm())
         _log(f"  {n}: {err:.2e}")
