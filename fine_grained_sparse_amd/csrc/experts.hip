@@ -13,6 +13,7 @@
 // all else (dW_gate and dx of normal rows: 3.1e-3 of the 2-norm against 2.4e-3, of
 // which 1.7e-3 is the result's own rounding), and they are 2% of the bytes at 683 rows an expert.
 #include <type_traits>
+#include <utility>
 
 #include "common.hpp"
 #include "experts.hpp"
@@ -24,102 +25,173 @@ namespace {
 // with its k side by side (rows: a row of the matrix is one m or n) or with its m
 // or n side by side (columns: a row is one k; read transposed from LDS).
 //
-// A block of four waves holds a tile of BM x 256 in registers, over slabs of 32
-// k.  A slab of both operands is (BM + 256) x 64 bytes and goes from global
-// memory straight into one of four LDS slots (global_load_lds_dwordx4, 1 KiB per
-// wave and instruction).  In the middle of slab b every wave waits for its loads of
-// b + 1, issued two slabs before, and meets the others: after that b + 1 may be
-// read, and the slot of b - 1, which nobody reads any more, takes b + 3.
-// A wave holds the A fragments of a slab, and B's one ahead of their products; those of
-// A are replaced one by one under the slab's last products.
+// A block of eight waves holds a tile of 256 x 256 in registers (four waves 64 x 256).  Stages of 64 k of both
+// operands go from global memory straight into LDS (global_load_lds_dwordx4, 1 KiB
+// per wave and instruction): A into two slots, B, the weights, which come
+// from further away, into three (two of the small tile, of which a CU holds
+// two).  While the products of a stage run, a wave asks for the next stage of A and the
+// one after the next of B, one load every eight products; near its end it waits
+// for its loads of the next stage and meets the other waves: after that the
+// next stage may be read, and this one, which all have in registers by then, be overwritten.
+// Half a stage (32 k) is one step of products; its fragments are read from LDS
+// under the products before: those of B two ahead, those of A each after its last use.
 //
-// Rows operand: a 1 KiB block holds 16 rows x 32 k; 16-byte chunk c of row r at r
-// 64 + (c ^ (r / 2 % 4)) 16, so that four neighbouring lanes load 64 bytes of a
-// row, and eight lanes that read one chunk of eight rows meet all banks once.
+// Rows operand: a 1 KiB block holds 8 rows x 64 k; 16-byte chunk c of row r at r 128 +
+// (c ^ r) 16: a load takes whole lines of 128 bytes (segments of 64 bytes reach half
+// the L2's rate: 16 against 33 TB/s, measured by itself), and eight lanes that read a
+// chunk of eight rows meet all banks once.
 // Columns operand: a block holds 2 k x 256 columns; 32-byte chunk c of row r at c
 // ^ (r % 4 + 4 (r / 8 % 2)) (see k_dw).
 // A lane has four neighbouring columns of each product; two of them are exchanged
 // between the lanes of neighbouring groups of 16 for eight: 16-byte stores.
+//
+// Blocks stay for all their tiles: the first loads of the next one are on their
+// way while a tile is stored.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ void dma(const char* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+// 16 bytes per lane from base + off (src) to LDS at slot + AT + 16 lane.
+template <int AT>
+__device__ __forceinline__ void dma(const char* base, uint32_t off, uint32_t slot) {
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(slot), "v"(off), "s"(base), "n"(AT) : "memory", "m0", "scc");
 }
-__device__ __forceinline__ void dma(const char* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+template <int AT>
+__device__ __forceinline__ void dma(const char* src, uint32_t slot) {
+    asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(slot)), "v"(src), "n"(AT) : "memory", "m0", "scc");
 }
-// This wave's loads but the newest N, and its reads of LDS, have landed; then all waves'.
+// This wave's vector memory operations but the newest N, and its reads of LDS, are done; then all waves'.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+// The same without regard to loads and stores.
+__device__ __forceinline__ void meet() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // What rows behind an expert's last one are read as in the columns operands.
 __device__ const uint4 kZero16 = {0, 0, 0, 0};
 
-struct Job {  // a tile: its expert, that expert's rows, and the tile's place in C
-    int e, r0, rows, m0, nt;
-};
+constexpr int kCUs = 256;
 
 template <int KIND, int BM>
 struct Tile {
     static constexpr bool kDw = KIND == EXP_DW_DOWN || KIND == EXP_DW_UP;
     static constexpr bool kACol = kDw, kBCol = kDw || KIND == EXP_DH || KIND == EXP_DX;
     static constexpr bool kPair = KIND == EXP_UP;          // 128 columns of W_gate and the same of W_up
-    static constexpr int kWM = BM == 256 ? 2 : 1, kWN = 4 / kWM;
+    static constexpr int kWaves = BM == 256 ? 8 : 4, kWM = BM == 256 ? 2 : 1, kWN = 4;
     static constexpr int MI = BM / 16 / kWM, NJ = 16 / kWN;  // fragments of a wave
-    static constexpr int NA = BM / 16, NB = 16;              // 1 KiB blocks of a slab
-    static constexpr int kSlot = (NA + NB) * 1024;
-    static constexpr int LA = NA / 4, LB = NB / 4, NL = LA + LB;  // loads of a wave
-    static constexpr int kN = kPair ? 128 : 256;                // columns of C per tile
+    static constexpr int kA = BM * 128, kB = 256 * 128;      // bytes of a stage
+    static constexpr int kSB = BM == 256 ? 3 : 2;            // slots of B
+    static constexpr int kLds = 2 * kA + kSB * kB;
+    static constexpr int LA = BM / 8 / kWaves, LB = 32 / kWaves;  // loads of a wave and stage
+    static constexpr int kN = kPair ? 128 : 256;             // columns of C per tile
+    static constexpr int kGrid = kCUs * (BM == 256 ? 1 : 2);
 };
 
-// The tile of job `lin`, expert by expert, M tiles side by side; rows == 0: none.
+// A block's tiles: it takes every gridDim.x / 8-th of its XCD's stretch of the list
+// (blocks go to the eight XCDs round robin), which has the experts in order, an expert's
+// M tiles side by side, so that the tiles which share weights run together.
+struct Jobs {
+    int lin, end, step;               // this tile, past the stretch, to the next one
+    int e, r0, rows, first, n;        // its expert, that one's rows, the M tiles before and of it
+    int m0, nt;                       // the tile's first row (of the expert's, or of C) and N tile
+};
+__device__ __forceinline__ int row_at(const ExpertsArgs& a, int e) {  // (e is the same for all lanes)
+    const int v = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(a.off))[e];
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(min(max(static_cast<int64_t>(v), int64_t(0)), a.R)));
+}
+
 template <int KIND, int BM>
-__device__ __forceinline__ Job find_job(const ExpertsArgs& a, int ntm, int ntn) {
-    const int lane = threadIdx.x & 63;
-    auto clamped = [&](int e) { return static_cast<int>(min(max(static_cast<int64_t>(a.off[e]), int64_t(0)), a.R)); };
-    // blocks go to the eight XCDs round robin: each takes one stretch of the list
+__device__ __forceinline__ void place(const ExpertsArgs& a, int ntm, int ntn, Jobs& j) {
     if (Tile<KIND, BM>::kDw) {
-        const int total = a.E * ntm * ntn, lin = xcd_slot_pair(static_cast<int>(blockIdx.x), total, total);
-        if (lin < 0) return Job{0, 0, 0, 0, -1};
-        const int e = lin / (ntm * ntn), in = lin % (ntm * ntn);
-        const int r0 = clamped(e), r1 = clamped(e + 1);
-        return Job{e, r0, max(r1 - r0, 0), in % ntm * BM, in / ntm};
+        const int e = j.lin / (ntm * ntn), in = j.lin - e * (ntm * ntn);
+        j.e = e;
+        j.r0 = row_at(a, e);
+        j.rows = max(row_at(a, e + 1) - j.r0, 0);
+        j.nt = in / ntm;
+        j.m0 = (in - j.nt * ntm) * BM;
+    } else {
+        const int in = j.lin - j.first * ntn;
+        j.nt = in / j.n;
+        j.m0 = (in - j.nt * j.n) * BM;
     }
-    // tiles of all experts, then those before this one's
+}
+
+// The block's first tile; false: it has none.
+template <int KIND, int BM>
+__device__ __forceinline__ bool first_job(const ExpertsArgs& a, int ntm, int ntn, Jobs& j) {
+    const int lane = threadIdx.x & 63, xcd = blockIdx.x & 7;
+    auto clamped = [&](int e) { return static_cast<int>(min(max(static_cast<int64_t>(a.off[e]), int64_t(0)), a.R)); };
     int total = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        const int e = e0 + lane;
-        int n = e < a.E ? max(clamped(e + 1) - clamped(e), 0) : 0;
-        n = (n + BM - 1) / BM;
+    if (Tile<KIND, BM>::kDw) {
+        total = a.E * ntm;
+    } else {
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            const int e = e0 + lane;
+            int n = e < a.E ? max(clamped(e + 1) - clamped(e), 0) : 0;
+            n = (n + BM - 1) / BM;
 #pragma unroll
-        for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
-        total += n;
+            for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
+            total += n;
+        }
+        total = __builtin_amdgcn_readfirstlane(total);
     }
-    const int lin = xcd_slot_pair(static_cast<int>(blockIdx.x), total * ntn, total * ntn);
-    if (lin < 0) return Job{0, 0, 0, 0, -1};
-    int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        const int e = e0 + lane;
-        const int r0 = e < a.E ? clamped(e) : 0, rows = e < a.E ? max(clamped(e + 1) - r0, 0) : 0;
-        const int n = (rows + BM - 1) / BM;
-        int incl = n;
+    total *= ntn;
+    const int per = (total + 7) >> 3;
+    j.step = gridDim.x >> 3;
+    j.lin = xcd * per + (blockIdx.x >> 3);
+    j.end = min(total, (xcd + 1) * per);
+    if (j.lin >= j.end) return false;
+    if (!Tile<KIND, BM>::kDw) {
+        int before = 0;
+        bool found = false;
+        for (int e0 = 0; e0 < a.E && !found; e0 += 64) {
+            const int e = e0 + lane;
+            const int r0 = e < a.E ? clamped(e) : 0, rows = e < a.E ? max(clamped(e + 1) - r0, 0) : 0;
+            const int n = (rows + BM - 1) / BM;
+            int incl = n;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(incl, o);
-            if (lane >= o) incl += v;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int first = before + incl - n;
+            const uint64_t mine = __ballot(n > 0 && first * ntn <= j.lin && j.lin < (first + n) * ntn);
+            if (mine) {
+                const int l = __ffsll(static_cast<unsigned long long>(mine)) - 1;
+                j.e = e0 + l;
+                j.r0 = __builtin_amdgcn_readlane(r0, l);
+                j.rows = __builtin_amdgcn_readlane(rows, l);
+                j.n = __builtin_amdgcn_readlane(n, l);
+                j.first = __builtin_amdgcn_readlane(first, l);
+                found = true;
+            }
+            before += __builtin_amdgcn_readlane(incl, 63);
         }
-        const int first = before + incl - n;
-        const uint64_t mine = __ballot(n > 0 && first * ntn <= lin && lin < (first + n) * ntn);
-        if (mine) {
-            const int l = __ffsll(static_cast<unsigned long long>(mine)) - 1;
-            const int in = lin - __shfl(first, l) * ntn, m = __shfl(n, l);
-            return Job{e0 + l, __shfl(r0, l), __shfl(rows, l), in % m * BM, in / m};
-        }
-        before += __shfl(incl, 63);
+        if (!found) return false;
     }
-    return Job{0, 0, 0, 0, -1};
+    place<KIND, BM>(a, ntm, ntn, j);
+    return true;
+}
+template <int KIND, int BM>
+__device__ __forceinline__ bool next_job(const ExpertsArgs& a, int ntm, int ntn, Jobs& j) {
+    j.lin += j.step;
+    if (j.lin >= j.end) return false;
+    if (!Tile<KIND, BM>::kDw)
+        while (j.lin >= (j.first + j.n) * ntn) {
+            if (++j.e >= a.E) return false;
+            j.first += j.n;
+            j.r0 = row_at(a, j.e);
+            j.rows = max(row_at(a, j.e + 1) - j.r0, 0);
+            j.n = (j.rows + BM - 1) / BM;
+        }
+    place<KIND, BM>(a, ntm, ntn, j);
+    return true;
 }
 
 __device__ __forceinline__ float sigmoid(float a) { return 1.f / (1.f + __expf(-a)); }
@@ -131,249 +203,298 @@ __device__ __forceinline__ uint4 pack8v(const float (&v)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// f(0), f(1), .. f(N - 1), each a constant.
+template <typename F, int... I>
+__device__ __forceinline__ void for_each(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void for_each(F&& f) {
+    for_each(f, std::make_integer_sequence<int, N>());
+}
+
 template <int KIND, int BM>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_experts(const ExpertsArgs a, int ntm, int ntn) {
+__global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(const ExpertsArgs a, int ntm, int ntn) {
     using S = Tile<KIND, BM>;
-    constexpr int MI = S::MI, NJ = S::NJ;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * S::kSlot];
+    constexpr int MI = S::MI, NJ = S::NJ, LA = S::LA, LB = S::LB;
+    __shared__ __attribute__((aligned(1024))) char lds[S::kLds];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wid / S::kWN, wn = wid % S::kWN;
-    Job job = find_job<KIND, BM>(a, ntm, ntn);
-    if (job.nt < 0) return;
-    job.e = __builtin_amdgcn_readfirstlane(job.e);
-    job.r0 = __builtin_amdgcn_readfirstlane(job.r0);
-    job.rows = __builtin_amdgcn_readfirstlane(job.rows);
-    job.m0 = __builtin_amdgcn_readfirstlane(job.m0);
-    job.nt = __builtin_amdgcn_readfirstlane(job.nt);
+    Jobs job;
+    if (!first_job<KIND, BM>(a, ntm, ntn, job)) return;
     const int64_t d = a.d, F = a.F;
-    const int n0 = job.nt * S::kN;
-
-    // Leading dimensions, extents and the operands' first bytes.
     const int64_t lda = KIND == EXP_UP || KIND == EXP_DH || KIND == EXP_DW_DOWN ? d : KIND == EXP_DOWN ? F : 2 * F;
     const int64_t ldb = KIND == EXP_DOWN || KIND == EXP_DH || KIND == EXP_DW_DOWN ? F : d;
     const int N = KIND == EXP_UP || KIND == EXP_DH || KIND == EXP_DW_DOWN ? a.F : a.d;
-    const int M = KIND == EXP_DW_DOWN ? a.d : KIND == EXP_DW_UP ? 2 * a.F : job.rows;
-    const int K = S::kDw ? job.rows : KIND == EXP_UP || KIND == EXP_DH ? a.d : KIND == EXP_DOWN ? a.F : 2 * a.F;
-    const int slabs = (K + 31) / 32;
-    const char* A = reinterpret_cast<const char*>(a.A + job.r0 * lda);
-    const char* B = reinterpret_cast<const char*>(a.B + (S::kDw ? job.r0 * ldb : job.e * F * d));
-    const char* B2 = reinterpret_cast<const char*>(KIND == EXP_UP || KIND == EXP_DX ? a.B2 + job.e * F * d : a.B);
-    if (!S::kACol) A += job.m0 * lda * 2;
 
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(lds)));
     auto fl = [](int r) { return (r & 3) | ((r >> 1) & 4); };
-    // Where a lane reads its 16 bytes of a load: from the operand's base, slab 0.
+
+    // The operands of a tile: first bytes, the lane's offset of each load, extents.
     // Past the last m, n or column the last one is read again (its results are
     // not stored).
-    uint32_t oa[S::LA], ob[S::LB];
-#pragma unroll
-    for (int k = 0; k < S::LA; ++k) {
-        const int q = wid + 4 * k;
-        if (S::kACol) {
-            const int r = 2 * q + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
-            oa[k] = static_cast<uint32_t>(r * lda + min(job.m0 + c * 8, M - 8)) * 2;
-        } else {
-            const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 3) & 3);
-            oa[k] = static_cast<uint32_t>(min(q * 16 + r, M - 1 - job.m0) * lda + c * 8) * 2;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < S::LB; ++k) {
-        const int q = wid + 4 * k;
-        if (S::kBCol) {
-            const int r = 2 * q + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
-            ob[k] = static_cast<uint32_t>(r * ldb + min(n0 + c * 8, N - 8)) * 2;
-        } else {
-            const int r = lane >> 2, c = (lane & 3) ^ ((lane >> 3) & 3);
-            // EXP_UP: half of a wave's fragments are of W_gate, the other half the same of W_up
-            const int f = S::kPair ? q / NJ * (NJ / 2) + q % (NJ / 2) : q;
-            ob[k] = static_cast<uint32_t>(min(n0 + f * 16 + r, N - 1) * ldb + c * 8) * 2;
-        }
-    }
-    // Slab b's k-th load of this wave.  Every call issues one instruction, so that
-    // counting the newest ones is enough to wait for the others.
-    auto load = [&](int b, int k) {
-        const bool isA = k < S::LA;
-        const int q = wid + 4 * (isA ? k : k - S::LA);
-        const uint32_t dst = lds0 + (b & 3) * S::kSlot + (isA ? q : S::NA + q) * 1024;
-        const uint32_t off = isA ? oa[isA ? k : 0] : ob[isA ? 0 : k - S::LA];
-        const char* base;
-        if (isA) {
-            base = A + static_cast<int64_t>(b) * (S::kACol ? 32 * lda * 2 : 64);
-        } else if (KIND == EXP_DX) {  // [W_gate; W_up], F rows each (a multiple of 32)
-            const int64_t row = static_cast<int64_t>(b) * 32;
-            base = row < F ? B + row * ldb * 2 : B2 + (row - F) * ldb * 2;
-        } else if (S::kPair) {
-            base = ((q & (NJ / 2)) ? B2 : B) + static_cast<int64_t>(b) * 64;
-        } else {
-            base = B + static_cast<int64_t>(b) * (S::kBCol ? 32 * ldb * 2 : 64);
-        }
-        if (S::kDw && (b + 1) * 32 > K) {  // the last rows: zeros behind them
-            const bool in = b * 32 + 2 * q + (lane >> 5) < K;
-            dma(in ? base + off : reinterpret_cast<const char*>(&kZero16), dst);
-        } else {
-            dma(base, off, dst);
-        }
-    };
-    auto tr = [&](uint32_t at) {
-        return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                             (__attribute__((address_space(3))) s16x4*)(lds + at)));
-    };
-    auto read_a = [&](int b, int i) -> uint4 {
-        const uint32_t o = (b & 3) * S::kSlot;
-        if (S::kACol) {
-            uint2 h[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int r = 8 * grp + (r16 >> 2) + 4 * u;
-                h[u] = tr(o + r * 512 + (((wm * MI + i) ^ fl(r)) << 5) + (r16 & 3) * 8);
-            }
-            return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
-        }
-        return *reinterpret_cast<const uint4*>(lds + o + (wm * MI + i) * 1024 + r16 * 64 + ((grp ^ ((r16 >> 1) & 3)) << 4));
-    };
-    auto read_b = [&](int b, int j) -> uint4 {
-        const uint32_t o = (b & 3) * S::kSlot + S::NA * 1024;
-        const int f = wn * NJ + j;
-        if (S::kBCol) {
-            uint2 h[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int r = 8 * grp + (r16 >> 2) + 4 * u;
-                h[u] = tr(o + r * 512 + ((f ^ fl(r)) << 5) + (r16 & 3) * 8);
-            }
-            return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
-        }
-        return *reinterpret_cast<const uint4*>(lds + o + f * 1024 + r16 * 64 + ((grp ^ ((r16 >> 1) & 3)) << 4));
-    };
-
-    f32x4 acc[MI][NJ];
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    if (slabs > 0) {
-        uint4 fa[MI], fb[2];
-#pragma unroll
-        for (int b = 0; b < 3; ++b)
-            if (b < slabs)
-#pragma unroll
-                for (int k = 0; k < S::NL; ++k) load(b, k);
-        // slab b has landed: `newer` later ones may be on their way
-        auto arrive = [&](int newer) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (newer >= 2) wait_and_meet<2 * S::NL>();
-            else if (newer == 1) wait_and_meet<S::NL>();
-            else wait_and_meet<0>();
-            __builtin_amdgcn_sched_barrier(0);
+    const char *A, *B, *B2;
+    uint32_t oa[LA], ob[LB];
+    int M, K, stages;
+    auto setup = [&](const Jobs& j) {
+        M = KIND == EXP_DW_DOWN ? a.d : KIND == EXP_DW_UP ? 2 * a.F : j.rows;
+        K = S::kDw ? j.rows : KIND == EXP_UP || KIND == EXP_DH ? a.d : KIND == EXP_DOWN ? a.F : 2 * a.F;
+        stages = (K + 63) >> 6;
+        A = reinterpret_cast<const char*>(a.A + (j.r0 + (S::kACol ? 0 : j.m0)) * lda);
+        B = reinterpret_cast<const char*>(a.B + (S::kDw ? j.r0 * ldb : j.e * F * d));
+        // EXP_DX: [W_gate; W_up], F rows each (a multiple of 64)
+        B2 = reinterpret_cast<const char*>(KIND == EXP_UP || KIND == EXP_DX ? a.B2 + j.e * F * d : a.B);
+        if (KIND == EXP_DX) B2 -= F * ldb * 2;
+        const int n0 = j.nt * S::kN;
+        auto columns = [&](int k, int64_t ld, int c0, int end) {  // of k row 2 (wid + 4 k) + lane / 32
+            const int r = 2 * (wid + S::kWaves * k) + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
+            return static_cast<uint32_t>(r * ld + min(c0 + c * 8, end - 8)) * 2;
         };
-        arrive(slabs - 1);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i] = read_a(0, i);
-        fb[0] = read_b(0, 0);
-        for (int b = 0; b < slabs; ++b) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                if (j == NJ / 2 && b + 1 < slabs) arrive(min(1, slabs - 2 - b));
-                __builtin_amdgcn_sched_barrier(0);
-                fb[(j + 1) & 1] = j + 1 < NJ ? read_b(b, j + 1) : read_b(b + 1, 0);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    acc[i][j] = Mfma<bf16_t>::run(fb[j & 1], fa[i], acc[i][j]);
-                    if (j == NJ - 1) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        fa[i] = read_a(b + 1, i);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                    if (j >= NJ / 2) {
-#pragma unroll
-                        for (int k = 0; k < S::NL; ++k)
-                            if (k * (MI * NJ / 2) / S::NL == (j - NJ / 2) * MI + i) {
-                                __builtin_amdgcn_sched_barrier(0);
-                                if (b + 3 < slabs) load(b + 3, k);
-                                __builtin_amdgcn_sched_barrier(0);
-                            }
-                    }
-                }
-            }
+        for (int k = 0; k < LA; ++k) {
+            const int r = lane >> 3, c = (lane & 7) ^ r;
+            oa[k] = S::kACol ? columns(k, lda, j.m0, M)
+                             : static_cast<uint32_t>(min((wid + S::kWaves * k) * 8 + r, M - 1 - j.m0) * lda + c * 8) * 2;
         }
-    }
-
-    // A lane's part of fragments j and j + 1 of row 16 i + r16: columns 16 j + nl .. + 7,
-    // nl = 16 (grp % 2) + 8 (grp / 2), once the odd groups' j and the even groups' j + 1 are exchanged.
-    const int nl = 16 * (grp & 1) + 8 * (grp >> 1);
-    auto eight = [&](int i, int j, float (&v)[8]) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][u]), __float_as_uint(acc[i][j + 1][u]),
-                                                            false, false);
-            v[u] = __uint_as_float(q[0]);
-            v[4 + u] = __uint_as_float(q[1]);
+        for (int k = 0; k < LB; ++k) {
+            const int q = wid + S::kWaves * k, r = lane >> 3, c = (lane & 7) ^ r;
+            // EXP_UP: half of a wave's fragments (two blocks each) are of W_gate, the other half the same of W_up
+            const int f = S::kPair ? q / (2 * NJ) * NJ + q % NJ : q;
+            ob[k] = S::kBCol ? columns(k, ldb, n0, N)
+                             : static_cast<uint32_t>(min(n0 + f * 8 + r, N - 1) * ldb + c * 8) * 2;
         }
     };
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int m = job.m0 + (wm * MI + i) * 16 + r16;
-        if (KIND == EXP_UP) {
-            const int64_t row = job.r0 + m;
-#pragma unroll
-            for (int j = 0; j < NJ / 2; j += 2) {
-                const int n = n0 + (wn * NJ / 2 + j) * 16 + nl;
-                float g[8], u[8], h[8];
-                eight(i, j, g);
-                eight(i, j + NJ / 2, u);
-                if (m >= M || n >= N) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
-                if (a.gu) {
-                    pack8(a.gu + row * 2 * F + n, g);
-                    pack8(a.gu + row * 2 * F + F + n, u);
-                }
-                stg16(a.C + row * F + n, pack8v(h));
-            }
-        } else if (KIND == EXP_DH) {
-            const int64_t row = job.r0 + m;
-#pragma unroll
-            for (int j = 0; j < NJ; j += 2) {
-                const int n = n0 + (wn * NJ + j) * 16 + nl;
-                float dh[8], g[8], u[8], dg[8], du[8];
-                eight(i, j, dh);
-                if (m >= M || n >= N) continue;
-                unpack8(a.gu + row * 2 * F + n, g);
-                unpack8(a.gu + row * 2 * F + F + n, u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float s = sigmoid(g[e]);
-                    du[e] = dh[e] * g[e] * s;
-                    dg[e] = dh[e] * u[e] * s * (1.f + g[e] * (1.f - s));
-                }
-                stg16(a.C + row * 2 * F + n, pack8v(dg));
-                stg16(a.C + row * 2 * F + F + n, pack8v(du));
-            }
+    // Stage s's K-th load of this wave, of A or B, to a slot.  Every call issues one
+    // instruction, so that counting the newest ones is enough to wait for the others.
+    // LAST: it may be the last stage, whose rows (of columns operands) behind the end are zeros.
+    auto one = [&](auto k_, auto last_, const char* base, uint32_t off, int s, uint32_t slot) {
+        constexpr int k = decltype(k_)::value;
+        if (S::kDw && decltype(last_)::value) {
+            const bool in = s * 64 + 2 * (wid + S::kWaves * k) + (lane >> 5) < K;
+            dma<k * S::kWaves * 1024>(in ? base + off : reinterpret_cast<const char*>(&kZero16), slot);
         } else {
-            bf16_t* out;
-            if (KIND == EXP_DW_DOWN)
-                out = a.C + (job.e * d + m) * F;
-            else if (KIND == EXP_DW_UP)
-                out = m < a.F ? a.C + (job.e * F + m) * d : a.C2 + (job.e * F + m - F) * d;
-            else
-                out = a.C + (job.r0 + m) * d;
+            dma<k * S::kWaves * 1024>(base, off, slot);
+        }
+    };
+    const uint32_t lds_w = lds0 + wid * 1024;
+    auto load_a = [&](int s, int slot, auto k, auto last) {
+        one(k, last, A + s * (S::kACol ? 128 * lda : 128), oa[decltype(k)::value], s, lds_w + slot * S::kA);
+    };
+    auto load_b = [&](int s, int slot, auto k_, auto last) {
+        constexpr int k = decltype(k_)::value;
+        const bool up = KIND == EXP_DX ? s * 64 >= a.F : S::kPair && ((wid + S::kWaves * k) & NJ);
+        one(k_, last, (up ? B2 : B) + s * (S::kBCol ? 128 * ldb : 128), ob[k], s, lds_w + 2 * S::kA + slot * S::kB);
+    };
+    // Fragment f of half h of the stage at `o`.  (Columns: a lane's rows are 8 grp + r16 / 4 and that + 4, alike in f.)
+    const uint32_t lt = (8 * grp + (r16 >> 2)) * 512 + (((r16 >> 2) | ((grp & 1) << 2)) << 5) + (r16 & 3) * 8;
+    const uint32_t lr = r16 * 128, lc = (grp ^ (r16 & 3)) | (r16 & 4);
+    auto read = [&](bool col, uint32_t o, int f, int h) -> uint4 {
+        if (col) {
+            typedef __attribute__((address_space(3))) s16x4* P;
+            const P q = (P)(lds + o + (lt ^ (f << 5)));
+            const uint2 v0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(q + h * 2048));
+            const uint2 v1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(q + h * 2048 + 256));
+            return make_uint4(v0.x, v0.y, v1.x, v1.y);
+        }
+        return *reinterpret_cast<const uint4*>(lds + o + f * 2048 + lr + ((lc ^ (4 * h)) << 4));
+    };
+    auto read_a = [&](int slot, int i, int h) { return read(S::kACol, slot * S::kA, wm * MI + i, h); };
+    auto read_b = [&](int slot, int j, int h) { return read(S::kBCol, 2 * S::kA + slot * S::kB, wn * NJ + j, h); };
+
+    // The loads that go out while stage s runs, in 2 NJ portions: A of s + 1, then B
+    // of s + kSB - 1 (to bslot).  Portions 0 and 1 belong to the last quarter of stage s - 1.
+    // SURE: those stages exist and are not the last one.
+    constexpr int LATE = NJ - 2, NW = LA + LB;
+    constexpr int kEach = S::kSB == 3 ? 1 : 2;  // loads of a portion
+    static_assert(NW <= 2 * NJ * kEach, "portions");
+    auto portion = [&](int s, auto p_, int bslot, auto sure_) {
+        constexpr int p = decltype(p_)::value;
+        constexpr bool SURE = decltype(sure_)::value;
+        auto go = [&](auto k_) {
+            constexpr int k = decltype(k_)::value;
+            if constexpr (k < LA) {
+                if (SURE || s + 1 < stages) load_a(s + 1, (s + 1) & 1, k_, std::bool_constant<!SURE>());
+            } else if constexpr (k < NW) {
+                if (SURE || s + S::kSB - 1 < stages)
+                    load_b(s + S::kSB - 1, bslot, std::integral_constant<int, k - LA>(), std::bool_constant<!SURE>());
+            }
+        };
+        go(std::integral_constant<int, p * kEach>());
+        if constexpr (kEach == 2) go(std::integral_constant<int, p * kEach + 1>());
+    };
+    // A tile's first loads: stage 0, B of stage 1 (three slots), portions 0 and 1 of stage 0.
+    constexpr int kFirst = (S::kSB == 3 ? LB : 0) + 2 * kEach;  // those behind stage 0's, of two stages or more
+    static_assert(2 * kEach <= (S::kSB == 3 ? LA : NW), "portions 0 and 1 need stage 1 only");
+    auto begin = [&]() {
+        if (stages == 0) return;
+        for_each<LA>([&](auto k) { load_a(0, 0, k, std::true_type()); });
+        for_each<LB>([&](auto k) { load_b(0, 0, k, std::true_type()); });
+        if (S::kSB == 3 && stages > 1) for_each<LB>([&](auto k) { load_b(1, 1, k, std::true_type()); });
+        portion(0, std::integral_constant<int, 0>(), S::kSB - 1, std::false_type());
+        portion(0, std::integral_constant<int, 1>(), S::kSB - 1, std::false_type());
+    };
+
+    setup(job);
+    begin();
+    int stored = 0;  // stores of the tile before, all behind these loads (0: none, or some other number)
+    constexpr int kStores = KIND == EXP_UP ? 0 : MI * NJ / 2 * (KIND == EXP_DH ? 2 : 1);
+    for (;;) {
+        f32x4 acc[MI][NJ];
 #pragma unroll
-            for (int j = 0; j < NJ; j += 2) {
-                const int n = n0 + (wn * NJ + j) * 16 + nl;
-                float v[8];
-                eight(i, j, v);
-                if (m >= M || n >= N) continue;
-                stg16(out + n, pack8v(v));
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (stages > 0) {
+            uint4 fa[MI], fb[4];  // (fb: a ring, two fragments ahead)
+            if (stages > 1) {
+                if (kStores && kFirst + kStores < 64 && stored) wait_and_meet<(kFirst + kStores) & 63>();
+                else wait_and_meet<kFirst>();
+            } else {
+                wait_and_meet<0>();
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i) fa[i] = read_a(0, i, 0);
+            fb[0] = read_b(0, 0, 0);
+            fb[1] = read_b(0, 1, 0);
+            int bs = 0;  // B slot of stage s
+            // half H of stage s
+            auto half = [&](int s, auto h_, auto sure) {
+                constexpr int H = decltype(h_)::value;
+                const int bnext = bs == S::kSB - 1 ? 0 : bs + 1, bprev = bs == 0 ? S::kSB - 1 : bs - 1;
+                for_each<NJ>([&](auto j_) {
+                    constexpr int j = decltype(j_)::value;
+                    if (H == 1 && j == LATE && (decltype(sure)::value || s + 1 < stages)) {
+                        // stage s + 1 has landed, and nobody reads stage s any more
+                        if (S::kSB == 3 && (decltype(sure)::value || s + 2 < stages)) wait_and_meet<LB>();
+                        else wait_and_meet<0>();
+                    }
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) {
+                        acc[i][j] = Mfma<bf16_t>::run(fb[j & 3], fa[i], acc[i][j]);
+                        if (i == 0) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            fb[(j + 2) & 3] = j < LATE ? read_b(bs, j + 2, H) : read_b(H ? bnext : bs, j - LATE, H ^ 1);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if constexpr (j == NJ - 1) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            fa[i] = read_a((s + H) & 1, i, H ^ 1);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if (i == MI / 2) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            // B of s + kSB - 1 takes the slot of stage s - 1, that of s + kSB the slot of s
+                            if constexpr (H == 0) portion(s, std::integral_constant<int, j + 2>(), bprev, sure);
+                            else if constexpr (j < LATE) portion(s, std::integral_constant<int, NJ + 2 + j>(), bprev, sure);
+                            else portion(s + 1, std::integral_constant<int, j - LATE>(), bs, sure);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                });
+                if (H) bs = bnext;
+            };
+            using H0 = std::integral_constant<int, 0>;
+            using H1 = std::integral_constant<int, 1>;
+            // (stages that the loads of stage s reach: s + 2, of kDw not the last one)
+            int s = 0;
+            for (; s < stages - (S::kDw ? 3 : 2); ++s) {
+                half(s, H0(), std::true_type());
+                half(s, H1(), std::true_type());
+            }
+            for (; s < stages; ++s) {
+                half(s, H0(), std::false_type());
+                if (!S::kDw || K - s * 64 > 32) half(s, H1(), std::false_type());
             }
         }
+
+        const Jobs at = job;
+        const int m_end = M;
+        const bool again = next_job<KIND, BM>(a, ntm, ntn, job);
+        if (again) {
+            meet();  // nobody reads this tile's stages any more
+            setup(job);
+            begin();
+        }
+        const int n0 = at.nt * S::kN;
+        stored = at.m0 + BM <= m_end && n0 + S::kN <= N;
+
+        // A lane's part of fragments j and j + 1 of row 16 i + r16: columns 16 j + nl .. + 7,
+        // nl = 16 (grp % 2) + 8 (grp / 2), once the odd groups' j and the even groups' j + 1 are exchanged.
+        const int nl = 16 * (grp & 1) + 8 * (grp >> 1);
+        auto eight = [&](int i, int j, float (&v)[8]) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][u]),
+                                                                __float_as_uint(acc[i][j + 1][u]), false, false);
+                v[u] = __uint_as_float(q[0]);
+                v[4 + u] = __uint_as_float(q[1]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // (or all of acc is moved at once, and spilled)
+            const int m = at.m0 + (wm * MI + i) * 16 + r16;
+            if (KIND == EXP_UP) {
+                const int64_t row = at.r0 + m;
+#pragma unroll
+                for (int j = 0; j < NJ / 2; j += 2) {
+                    const int n = n0 + (wn * NJ / 2 + j) * 16 + nl;
+                    float g[8], u[8], h[8];
+                    eight(i, j, g);
+                    eight(i, j + NJ / 2, u);
+                    if (m >= m_end || n >= N) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
+                    if (a.gu) {
+                        pack8(a.gu + row * 2 * F + n, g);
+                        pack8(a.gu + row * 2 * F + F + n, u);
+                    }
+                    stg16(a.C + row * F + n, pack8v(h));
+                }
+            } else if (KIND == EXP_DH) {
+                const int64_t row = at.r0 + m;
+#pragma unroll
+                for (int j = 0; j < NJ; j += 2) {
+                    const int n = n0 + (wn * NJ + j) * 16 + nl;
+                    float dh[8], g[8], u[8], dg[8], du[8];
+                    eight(i, j, dh);
+                    if (m >= m_end || n >= N) continue;
+                    unpack8(a.gu + row * 2 * F + n, g);
+                    unpack8(a.gu + row * 2 * F + F + n, u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float s = sigmoid(g[e]);
+                        du[e] = dh[e] * g[e] * s;
+                        dg[e] = dh[e] * u[e] * s * (1.f + g[e] * (1.f - s));
+                    }
+                    stg16(a.C + row * 2 * F + n, pack8v(dg));
+                    stg16(a.C + row * 2 * F + F + n, pack8v(du));
+                }
+            } else {
+                bf16_t* out;
+                if (KIND == EXP_DW_DOWN)
+                    out = a.C + (at.e * d + m) * F;
+                else if (KIND == EXP_DW_UP)
+                    out = m < a.F ? a.C + (at.e * F + m) * d : a.C2 + (at.e * F + m - F) * d;
+                else
+                    out = a.C + (at.r0 + m) * d;
+#pragma unroll
+                for (int j = 0; j < NJ; j += 2) {
+                    const int n = n0 + (wn * NJ + j) * 16 + nl;
+                    float v[8];
+                    eight(i, j, v);
+                    if (m >= m_end || n >= N) continue;
+                    stg16(out + n, pack8v(v));
+                }
+            }
+        }
+        if (!again) return;
     }
 }
 
-// Blocks of a launch: at least one per tile, whatever the experts' row counts.
+// The most tiles that a launch can have, whatever the experts' row counts.
 template <int KIND, int BM>
 int64_t tiles(int64_t R, int64_t E, int64_t d, int64_t F, int* ntm, int* ntn) {
     using S = Tile<KIND, BM>;
@@ -384,7 +505,7 @@ int64_t tiles(int64_t R, int64_t E, int64_t d, int64_t F, int* ntm, int* ntn) {
     return mt * *ntn;
 }
 
-constexpr int64_t kMaxTiles = 1 << 23;  // a launch has less than 2^32 threads
+constexpr int64_t kMaxTiles = 1 << 26;  // (tile numbers are 32 bits)
 
 template <int KIND, int BM>
 hipError_t launch(const ExpertsArgs& a, hipStream_t stream) {
@@ -392,7 +513,10 @@ hipError_t launch(const ExpertsArgs& a, hipStream_t stream) {
     const int64_t n = tiles<KIND, BM>(a.R, a.E, a.d, a.F, &ntm, &ntn);
     if (n > kMaxTiles) return hipErrorInvalidValue;
     if (n == 0) return hipSuccess;
-    hipLaunchKernelGGL((k_experts<KIND, BM>), dim3(job_blocks(static_cast<int>(n), 1)), dim3(256), 0, stream, a, ntm, ntn);
+    // whole eights of blocks; up to seven XCDs' stretches end early
+    const int64_t blocks = (n + 7) / 8 * 8;
+    const unsigned grid = static_cast<unsigned>(blocks < Tile<KIND, BM>::kGrid ? blocks : Tile<KIND, BM>::kGrid);
+    hipLaunchKernelGGL((k_experts<KIND, BM>), dim3(grid), dim3(64 * Tile<KIND, BM>::kWaves), 0, stream, a, ntm, ntn);
     return hipGetLastError();
 }
 
