@@ -320,7 +320,10 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
         }
         return *reinterpret_cast<const uint4*>(lds + o + f * 2048 + lr + ((lc ^ (4 * h)) << 4));
     };
-    auto read_a = [&](int slot, int i, int h) { return read(S::kACol, slot * S::kA, wm * MI + i, h); };
+    // Fragments of A's rows per wave: an expert's last tile has fewer, in steps of kStep, and the waves share them.
+    constexpr int kStep = MI / 4;
+    int mi = MI;
+    auto read_a = [&](int slot, int i, int h) { return read(S::kACol, slot * S::kA, wm * mi + i, h); };
     auto read_b = [&](int slot, int j, int h) { return read(S::kBCol, 2 * S::kA + slot * S::kB, wn * NJ + j, h); };
 
     // The loads that go out while stage s runs, in 2 NJ portions: A of s + 1, then B
@@ -362,6 +365,7 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
     constexpr int kStores = KIND == EXP_UP ? 0 : MI * NJ / 2 * (KIND == EXP_DH ? 2 : 1);
     for (;;) {
         f32x4 acc[MI][NJ];
+        if (!S::kDw) mi = kStep * min((M - job.m0 + BM / 4 - 1) / (BM / 4), 4);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -372,7 +376,8 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
                 if (kStores && kFirst + kStores < 64 && stored) wait_and_meet<(kFirst + kStores) & 63>();
                 else wait_and_meet<kFirst>();
             } else {
-                wait_and_meet<0>();
+                if (kStores && kStores < 64 && stored) wait_and_meet<kStores & 63>();
+                else wait_and_meet<0>();
             }
 #pragma unroll
             for (int i = 0; i < MI; ++i) fa[i] = read_a(0, i, 0);
@@ -391,24 +396,21 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
                         else wait_and_meet<0>();
                     }
 #pragma unroll
-                    for (int i = 0; i < MI; ++i) {
-                        acc[i][j] = Mfma<bf16_t>::run(fb[j & 3], fa[i], acc[i][j]);
-                        if (i == 0) {
+                    for (int g = 0; g < 4; ++g) {
+                        if (!S::kDw && g > 0 && mi <= g * kStep) break;  // (uniform)
+#pragma unroll
+                        for (int i = g * kStep; i < (g + 1) * kStep; ++i) {
+                            acc[i][j] = Mfma<bf16_t>::run(fb[j & 3], fa[i], acc[i][j]);
                             __builtin_amdgcn_sched_barrier(0);
-                            fb[(j + 2) & 3] = j < LATE ? read_b(bs, j + 2, H) : read_b(H ? bnext : bs, j - LATE, H ^ 1);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                        if constexpr (j == NJ - 1) {
-                            __builtin_amdgcn_sched_barrier(0);
-                            fa[i] = read_a((s + H) & 1, i, H ^ 1);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                        if (i == MI / 2) {
+                            if (i == 0) fb[(j + 2) & 3] = j < LATE ? read_b(bs, j + 2, H) : read_b(H ? bnext : bs, j - LATE, H ^ 1);
+                            if (j == NJ - 1) fa[i] = read_a((s + H) & 1, i, H ^ 1);
                             __builtin_amdgcn_sched_barrier(0);
                             // B of s + kSB - 1 takes the slot of stage s - 1, that of s + kSB the slot of s
-                            if constexpr (H == 0) portion(s, std::integral_constant<int, j + 2>(), bprev, sure);
-                            else if constexpr (j < LATE) portion(s, std::integral_constant<int, NJ + 2 + j>(), bprev, sure);
-                            else portion(s + 1, std::integral_constant<int, j - LATE>(), bs, sure);
+                            if (i == kStep - 1) {
+                                if constexpr (H == 0) portion(s, std::integral_constant<int, j + 2>(), bprev, sure);
+                                else if constexpr (j < LATE) portion(s, std::integral_constant<int, NJ + 2 + j>(), bprev, sure);
+                                else portion(s + 1, std::integral_constant<int, j - LATE>(), bs, sure);
+                            }
                             __builtin_amdgcn_sched_barrier(0);
                         }
                     }
@@ -455,7 +457,8 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             __builtin_amdgcn_sched_barrier(0);  // (or all of acc is moved at once, and spilled)
-            const int m = at.m0 + (wm * MI + i) * 16 + r16;
+            if (!S::kDw && i >= mi) break;  // (uniform)
+            const int m = at.m0 + (wm * mi + i) * 16 + r16;
             if (KIND == EXP_UP) {
                 const int64_t row = at.r0 + m;
 #pragma unroll
