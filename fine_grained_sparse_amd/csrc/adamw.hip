@@ -22,15 +22,24 @@
 namespace moe {
 namespace {
 
-constexpr int kTensors = 48;     // of a launch: their table is a kernel argument
 constexpr int kPerThread = 8, kSpan = 256 * kPerThread, kRounds = 4;
 constexpr int64_t kChunk = static_cast<int64_t>(kSpan) * kRounds;  // elements of a block
 
-struct Table {
-    moe_adamw_tensor t[kTensors];
-    uint32_t first[kTensors];  // each tensor's first block
-    int32_t n, base;           // tensors, and the number of the first in the whole call
+// The tensors' table in device memory: an entry each, then each one's first block.
+constexpr int kPiece = 56;  // entries that a launch writes, from its arguments
+struct Piece {
+    moe_adamw_tensor t[kPiece];
+    uint32_t first[kPiece];
+    int32_t at, n;
 };
+__global__ __launch_bounds__(64) void k_adamw_table(const Piece p, moe_adamw_tensor* __restrict__ table,
+                                                    uint32_t* __restrict__ first) {
+    const int i = threadIdx.x;
+    if (i < p.n) {
+        table[p.at + i] = p.t[i];
+        first[p.at + i] = p.first[i];
+    }
+}
 
 struct Step {
     float b1, b2, n1, n2;      // b, 1 - b
@@ -50,15 +59,19 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
     return h ^ (h >> 16);
 }
 
-// Block -> tensor: the last whose first block is not behind it.
-__device__ __forceinline__ int find_tensor(const Table& T, uint32_t block) {
-    int lo = 0, hi = T.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (T.first[mid] <= block) lo = mid;
-        else hi = mid - 1;
+// Block -> tensor: the last whose first block is not behind it (an empty one has the
+// first block of the one after it).  Two loads deep up to 4096 tensors.
+__device__ __forceinline__ int find_tensor(const uint32_t* __restrict__ first, int n, uint32_t block) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 63) / 64, i = lane * step;
+        const bool before = i < n && first[lo + i] <= block;  // (lane 0's always is)
+        const int last = 63 - __clzll(__ballot(before));
+        lo += last * step;
+        n = min(step, n - last * step);
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // The largest over the 16 lanes that share a block of 128 values.
@@ -146,11 +159,12 @@ __device__ __forceinline__ float product(float x, float y) {
 }
 
 template <typename TP, typename TG, bool EIGHT>
-__global__ __launch_bounds__(256) void k_adamw(const Table T, const Step S) {
+__global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restrict__ table,
+                                               const uint32_t* __restrict__ first, int tensors, const Step S) {
     const int tid = threadIdx.x;
-    const int ti = find_tensor(T, blockIdx.x);
-    const moe_adamw_tensor& t = T.t[ti];
-    const int64_t n = t.n, c0 = static_cast<int64_t>(blockIdx.x - T.first[ti]) * kChunk;
+    const int ti = find_tensor(first, tensors, blockIdx.x);
+    const moe_adamw_tensor t = table[ti];
+    const int64_t n = t.n, c0 = static_cast<int64_t>(blockIdx.x - first[ti]) * kChunk;
     const float lr = S.lr_dev ? *S.lr_dev : S.lr;
     const int step = S.step_dev ? *S.step_dev : S.step;
     const float gs = S.grad_scale ? *S.grad_scale : 1.f;
@@ -165,7 +179,7 @@ __global__ __launch_bounds__(256) void k_adamw(const Table T, const Step S) {
     }
     const float rate = static_cast<float>(static_cast<double>(lr) / d1);
     const float root = static_cast<float>(1.0 / sqrt(d2));
-    const uint32_t key0 = mix(mix(mix(S.seed) + static_cast<uint32_t>(step)) + static_cast<uint32_t>(T.base + ti));
+    const uint32_t key0 = mix(mix(mix(S.seed) + static_cast<uint32_t>(step)) + static_cast<uint32_t>(ti));
     TP* const p = static_cast<TP*>(t.param);
     const TG* const g = static_cast<const TG*>(t.grad);
 #pragma unroll 1
@@ -257,6 +271,7 @@ __global__ __launch_bounds__(256) void k_adamw(const Table T, const Step S) {
     }
 }
 
+constexpr int kTensors = 48;  // of a launch: their table is a kernel argument
 struct MomentsTable {
     const uint8_t *m[kTensors], *v[kTensors], *ms[kTensors], *vs[kTensors];
     float *om[kTensors], *ov[kTensors];
@@ -300,16 +315,44 @@ __global__ __launch_bounds__(256) void k_moments(const MomentsTable T) {
 }
 
 template <typename TP, typename TG>
-void enqueue(bool eight, const Table& T, const Step& S, unsigned blocks, hipStream_t stream) {
+void enqueue(bool eight, const moe_adamw_tensor* t, const uint32_t* f, int n, const Step& S, unsigned blocks,
+             hipStream_t stream) {
     if (eight)
-        hipLaunchKernelGGL((k_adamw<TP, TG, true>), dim3(blocks), dim3(256), 0, stream, T, S);
+        hipLaunchKernelGGL((k_adamw<TP, TG, true>), dim3(blocks), dim3(256), 0, stream, t, f, n, S);
     else
-        hipLaunchKernelGGL((k_adamw<TP, TG, false>), dim3(blocks), dim3(256), 0, stream, T, S);
+        hipLaunchKernelGGL((k_adamw<TP, TG, false>), dim3(blocks), dim3(256), 0, stream, t, f, n, S);
 }
 
 }  // namespace
 
-hipError_t launch_adamw(const moe_adamw_desc& D, const moe_adamw_tensor* t, int n, hipStream_t stream) {
+int64_t adamw_table_bytes(int n) { return static_cast<int64_t>(n) * (sizeof(moe_adamw_tensor) + 4); }
+int64_t adamw_blocks(const moe_adamw_tensor* t, int n) {
+    int64_t blocks = 0;
+    for (int i = 0; i < n; ++i) blocks += (t[i].n + kChunk - 1) / kChunk;
+    return blocks;
+}
+
+hipError_t launch_adamw(const moe_adamw_desc& D, const moe_adamw_tensor* t, int n, void* table, hipStream_t stream) {
+    moe_adamw_tensor* const entries = static_cast<moe_adamw_tensor*>(table);
+    uint32_t* const first = reinterpret_cast<uint32_t*>(entries + n);
+    const int64_t blocks = adamw_blocks(t, n);
+    if (blocks == 0) return hipSuccess;
+    if (!D.keep_table) {
+        int64_t at = 0;
+        for (int i = 0; i < n; i += kPiece) {
+            Piece p;
+            p.at = i;
+            p.n = n - i < kPiece ? n - i : kPiece;
+            for (int k = 0; k < p.n; ++k) {
+                p.t[k] = t[i + k];
+                p.first[k] = static_cast<uint32_t>(at);
+                at += (t[i + k].n + kChunk - 1) / kChunk;
+            }
+            hipLaunchKernelGGL(k_adamw_table, dim3(1), dim3(64), 0, stream, p, entries, first);
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+        }
+    }
     Step S{};
     S.beta1 = D.beta_avg;
     S.beta2 = D.beta_sq;
@@ -328,31 +371,10 @@ hipError_t launch_adamw(const moe_adamw_desc& D, const moe_adamw_tensor* t, int 
     S.step_dev = D.step_device;
     S.grad_scale = D.grad_scale;
     const bool p16 = D.param_dtype == MOE_BF16, g16 = D.grad_dtype == MOE_BF16, eight = D.moment_bits == 8;
-    Table T{};
-    int64_t blocks = 0;
-    auto flush = [&]() {
-        if (T.n == 0) return hipSuccess;
-        const unsigned b = static_cast<unsigned>(blocks);
-        if (p16) g16 ? enqueue<bf16_t, bf16_t>(eight, T, S, b, stream) : enqueue<bf16_t, float>(eight, T, S, b, stream);
-        else g16 ? enqueue<float, bf16_t>(eight, T, S, b, stream) : enqueue<float, float>(eight, T, S, b, stream);
-        T.n = 0;
-        blocks = 0;
-        return hipGetLastError();
-    };
-    for (int i = 0; i < n; ++i) {
-        if (t[i].n == 0) continue;
-        const int64_t nb = (t[i].n + kChunk - 1) / kChunk;
-        // (base + slot is a tensor's number: an empty tensor in between begins a new launch)
-        if (T.n == kTensors || blocks + nb >= (1 << 24) || (T.n && T.base + T.n != i)) {
-            const hipError_t err = flush();
-            if (err != hipSuccess) return err;
-        }
-        if (T.n == 0) T.base = i;
-        T.t[T.n] = t[i];
-        T.first[T.n++] = static_cast<uint32_t>(blocks);
-        blocks += nb;
-    }
-    return flush();
+    const unsigned b = static_cast<unsigned>(blocks);
+    if (p16) g16 ? enqueue<bf16_t, bf16_t>(eight, entries, first, n, S, b, stream) : enqueue<bf16_t, float>(eight, entries, first, n, S, b, stream);
+    else g16 ? enqueue<float, bf16_t>(eight, entries, first, n, S, b, stream) : enqueue<float, float>(eight, entries, first, n, S, b, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_adamw_moments(const moe_adamw_tensor* t, float* const* avg, float* const* sq, int n,

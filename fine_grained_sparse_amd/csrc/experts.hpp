@@ -41,7 +41,9 @@ int64_t experts_max_rows(int E, int d, int F);
 hipError_t launch_experts(ExpertsKind kind, const ExpertsArgs& a, hipStream_t stream);
 
 // ---- adamw.hip
-hipError_t launch_adamw(const moe_adamw_desc& D, const moe_adamw_tensor* t, int n, hipStream_t stream);
+int64_t adamw_table_bytes(int n);
+int64_t adamw_blocks(const moe_adamw_tensor* t, int n);
+hipError_t launch_adamw(const moe_adamw_desc& D, const moe_adamw_tensor* t, int n, void* table, hipStream_t stream);
 hipError_t launch_adamw_moments(const moe_adamw_tensor* t, float* const* avg, float* const* sq, int n,
                                 hipStream_t stream);
 

@@ -25,6 +25,8 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
         if ((x) != hipSuccess) return MOE_ERR_HIP; \
     } while (0)
 
+constexpr int32_t kMaxTensors = 65536;
+constexpr int64_t kMaxBlocks = 1 << 24;  // (a launch has less than 2^32 threads)
 constexpr int32_t kMaxD = 1 << 24;  // columns of a row: byte offsets within a tile of rows stay below 2^32
 
 // The fields of a call on rows: T, d, K and the type.
@@ -228,9 +230,14 @@ moe_status moe_experts_backward(const moe_layer_desc* desc, int64_t rows, const 
     return MOE_OK;
 }
 
-moe_status moe_adamw(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors, int32_t n_tensors, void* stream) {
+size_t moe_adamw_table_size(int32_t n_tensors) {
+    return n_tensors < 0 || n_tensors > kMaxTensors ? 0 : static_cast<size_t>(up(adamw_table_bytes(n_tensors) + 1, 256));
+}
+
+moe_status moe_adamw(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors, int32_t n_tensors, void* table,
+                     size_t table_bytes, void* stream) {
     if (!desc || (n_tensors > 0 && !tensors)) return MOE_ERR_NULL;
-    if (n_tensors < 0 || (desc->step < 1 && !desc->step_device)) return MOE_ERR_SHAPE;
+    if (n_tensors < 0 || n_tensors > kMaxTensors || (desc->step < 1 && !desc->step_device)) return MOE_ERR_SHAPE;
     auto beta = [](double b) { return b >= 0.0 && b < 1.0; };
     if (!beta(desc->beta_avg) || !beta(desc->beta_sq)) return MOE_ERR_SHAPE;
     auto type = [](int32_t t) { return t == MOE_F32 || t == MOE_BF16; };
@@ -246,7 +253,13 @@ moe_status moe_adamw(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors
         if (t.copy && desc->param_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
         if (!aligned16(t.param, t.grad, t.copy)) return MOE_ERR_ALIGN;
     }
-    MOE_HIP(launch_adamw(*desc, tensors, n_tensors, static_cast<hipStream_t>(stream)));
+    const int64_t blocks = adamw_blocks(tensors, n_tensors);
+    if (blocks == 0) return MOE_OK;
+    if (blocks >= kMaxBlocks) return MOE_ERR_SHAPE;
+    if (!table) return MOE_ERR_NULL;
+    if (!aligned16(table)) return MOE_ERR_ALIGN;
+    if (table_bytes < static_cast<size_t>(adamw_table_bytes(n_tensors))) return MOE_ERR_WORKSPACE;
+    MOE_HIP(launch_adamw(*desc, tensors, n_tensors, table, static_cast<hipStream_t>(stream)));
     return MOE_OK;
 }
 

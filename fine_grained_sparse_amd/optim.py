@@ -20,7 +20,8 @@ class _Desc(ctypes.Structure):
     _fields_ = [("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("moment_bits", ctypes.c_int32),
                 ("step", ctypes.c_int32), ("seed", ctypes.c_uint32), ("lr", ctypes.c_float), ("eps", ctypes.c_float),
                 ("weight_decay", ctypes.c_float), ("beta_avg", ctypes.c_double), ("beta_sq", ctypes.c_double),
-                ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+                ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+                ("keep_table", ctypes.c_int32)]
 
 
 class _Tensor(ctypes.Structure):
@@ -47,12 +48,15 @@ class AdamW:
     exp_avg, exp_avg_sq (and, with 8 bits, exp_avg_scale, exp_avg_sq_scale)
                  moments to go on from, used in place (default: zeros);
     step         the number of steps they have seen.
-    lr and the others may be changed between steps (opt.lr = ...)."""
+    lr and the others may be changed between steps (opt.lr = ...).
+    The object works on the memory that all these tensors have when it is given
+    them, and keeps it alive: a parameter that is moved (p.data = ...) needs a new
+    object, a gradient buffer that is moved is handed over again."""
 
     def __init__(self, params, *, grads=None, state_bits=32, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, seed=0, exp_avg=None, exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None,
                  step=0):
-        params = list(params)
+        params = [p.detach() if isinstance(p, torch.Tensor) else p for p in params]  # (the memory, whatever becomes of p)
         if not params:
             raise ValueError("no parameters")
         if state_bits not in (8, 32):
@@ -101,12 +105,16 @@ class AdamW:
                                      self.exp_avg_scale[i].data_ptr() if eight else None,
                                      self.exp_avg_sq_scale[i].data_ptr() if eight else None,
                                      None if c is None else c.data_ptr(), p.numel())
+        self._nbytes = int(train_lib().moe_adamw_table_size(len(params)))
+        if self._nbytes == 0:
+            raise ValueError(f"{len(params)} parameters: too many")
+        self._tables = {}  # device tables of the addresses by stream, written by the first step there
         self.grads, self._grad_dtype = None, None
         if grads is not None:
             self.grads = self._take(grads)
 
     def _take(self, grads):
-        grads = list(grads)
+        grads = [g.detach() if isinstance(g, torch.Tensor) else g for g in grads]
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         dt = _typed(grads, "grads", self.device)
@@ -115,6 +123,7 @@ class AdamW:
                 raise ValueError(f"grads[{i}] has shape {tuple(g.shape)}, expected {tuple(p.shape)}")
             self._table[i].grad = g.data_ptr()
         self._grad_dtype = _DT[dt]
+        self._tables.clear()
         return grads
 
     def step(self, grads=None, *, lr=None, step=None, grad_scale=None, stream=None):
@@ -144,7 +153,15 @@ class AdamW:
             D.lr = float(lr)
         s, ctx = _launch(self.device, stream)
         with ctx:
-            _call("moe_adamw", ctypes.byref(D), self._table, len(self.params), s)
+            table = self._tables.get(s)
+            if table is None or torch.cuda.is_current_stream_capturing():
+                # (a captured step writes a table of its own, which the graph's memory keeps)
+                table = torch.empty(self._nbytes, dtype=torch.uint8, device=self.device)
+                if not torch.cuda.is_current_stream_capturing():
+                    self._tables[s] = table
+            else:
+                D.keep_table = 1
+            _call("moe_adamw", ctypes.byref(D), self._table, len(self.params), table.data_ptr(), self._nbytes, s)
         if step is None:
             self.steps += 1
 

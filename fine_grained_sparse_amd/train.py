@@ -33,7 +33,8 @@ TRAIN_EXPORTS = ("moe_router_train", "moe_balance_workspace_size", "moe_balance_
                  "moe_router_backward_workspace_size", "moe_router_backward",
                  "moe_dispatch_workspace_size", "moe_dispatch", "moe_sort_tokens", "moe_sort_tokens_backward",
                  "moe_combine", "moe_combine_backward", "moe_experts_max_rows", "moe_experts_forward",
-                 "moe_experts_backward_workspace_size", "moe_experts_backward", "moe_adamw", "moe_adamw_moments")
+                 "moe_experts_backward_workspace_size", "moe_experts_backward", "moe_adamw_table_size", "moe_adamw",
+                 "moe_adamw_moments")
 
 
 _NOTHING = _Nothing()
@@ -81,7 +82,9 @@ def train_lib():
         L.moe_experts_backward_workspace_size.argtypes = [D, i64]
         L.moe_experts_backward_workspace_size.restype = size
         L.moe_experts_backward.argtypes = [D, i64, vp, vp, vp, W] + [vp] * 7 + [size, vp]
-        L.moe_adamw.argtypes = [vp, vp, i32, vp]
+        L.moe_adamw_table_size.argtypes = [i32]
+        L.moe_adamw_table_size.restype = size
+        L.moe_adamw.argtypes = [vp, vp, i32, vp, size, vp]
         L.moe_adamw_moments.argtypes = [vp, i32, vp, vp, vp]
         for n in TRAIN_EXPORTS:
             if not n.endswith(("_size", "_max_rows")):

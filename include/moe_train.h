@@ -239,6 +239,9 @@ typedef struct {
     const int32_t *step_device;   /* likewise, in place of step: for a call that
                                      is captured and replayed                  */
     const float *grad_scale;      /* [1] on the device, or NULL for 1          */
+    int32_t keep_table;    /* 0: the call writes the tensors' table first (one */
+                           /* launch per 56 of them); else the table holds it, */
+                           /* from a call with the same `tensors`              */
 } moe_adamw_desc;
 
 /* One tensor of n elements; 16-byte aligned pointers (scales: any).
@@ -256,9 +259,14 @@ typedef struct {
 } moe_adamw_tensor;
 
 /* `tensors` is host memory and is read before the call returns.  A tensor may
- * be empty (n = 0); no two may overlap.                                      */
+ * be empty (n = 0); no two may overlap; at most 65536 of them, with less than
+ * 2^36 elements each and 2^37 in all.  `table`: device memory of at least
+ * moe_adamw_table_size(n_tensors) bytes (0: out of range), 16-byte aligned,
+ * which the call writes unless keep_table says that it is written, and reads.  */
+size_t moe_adamw_table_size(int32_t n_tensors);
 moe_status moe_adamw(const moe_adamw_desc *desc, const moe_adamw_tensor *tensors,
-                     int32_t n_tensors, void *stream);
+                     int32_t n_tensors, void *table, size_t table_bytes,
+                     void *stream);
 
 /* 8-bit moments to the values they stand for: avg[i] and sq[i] (host arrays of
  * device pointers; an entry, or a whole array, may be NULL) receive fp32 [n] of

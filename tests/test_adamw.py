@@ -15,7 +15,7 @@ import torch
 
 import fine_grained_sparse_amd as moe
 from fine_grained_sparse_amd import optim, train
-from test_abi import ALIGN, FAKE, FAKE_ODD, NULL, OK, SHAPE, UNSUP
+from test_abi import ALIGN, FAKE, FAKE_ODD, NULL, OK, SHAPE, UNSUP, WS
 
 E32 = 2.0 ** -24
 DEV = "cuda:0"
@@ -25,7 +25,7 @@ F32, B16 = torch.float32, torch.bfloat16
 # ------------------------------------------------------------- refusals (CPU)
 def _d(**kw):
     v = dict(param_dtype=0, grad_dtype=1, moment_bits=32, step=1, seed=0, lr=1e-3, eps=1e-8, weight_decay=0.0,
-             beta_avg=0.9, beta_sq=0.999, lr_device=None, step_device=None, grad_scale=None)
+             beta_avg=0.9, beta_sq=0.999, lr_device=None, step_device=None, grad_scale=None, keep_table=0)
     v.update(kw)
     return optim._Desc(**v)
 
@@ -40,11 +40,17 @@ def _t(n=10, **kw):
 def test_adamw_rejects_bad_arguments():
     L = train.train_lib()
 
-    def f(D, *ts, n=None):
-        table = (optim._Tensor * max(len(ts), 1))(*ts)
-        return L.moe_adamw(ctypes.byref(D), table, len(ts) if n is None else n, None)
-    assert L.moe_adamw(None, None, 0, None) == NULL
-    assert L.moe_adamw(ctypes.byref(_d()), None, 1, None) == NULL
+    def f(D, *ts, n=None, table=FAKE, nbytes=1 << 30):
+        host = (optim._Tensor * max(len(ts), 1))(*ts)
+        return L.moe_adamw(ctypes.byref(D), host, len(ts) if n is None else n, table, nbytes, None)
+    assert L.moe_adamw(None, None, 0, None, 0, None) == NULL
+    assert L.moe_adamw(ctypes.byref(_d()), None, 1, None, 0, None) == NULL
+    assert L.moe_adamw_table_size(-1) == 0 and L.moe_adamw_table_size(65537) == 0 and L.moe_adamw_table_size(0) > 0
+    n = 3 * (ctypes.sizeof(optim._Tensor) + 4)
+    assert L.moe_adamw_table_size(3) >= n
+    assert f(_d(), _t(), _t(), _t(), nbytes=n - 1) == WS
+    assert f(_d(), _t(), table=None) == NULL and f(_d(), _t(), table=FAKE_ODD) == ALIGN
+    assert f(_d(), *[_t(n=(1 << 36) - 1)] * 3) == SHAPE and f(_d(), _t(), n=65537) == SHAPE
     assert f(_d(), _t(), n=-1) == SHAPE
     for bad in (dict(step=0), dict(beta_avg=1.0), dict(beta_sq=-0.1), dict(beta_avg=math.nan)):
         assert f(_d(**bad), _t()) == SHAPE, bad
