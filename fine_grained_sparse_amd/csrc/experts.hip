@@ -25,16 +25,16 @@ namespace {
 // with its k side by side (rows: a row of the matrix is one m or n) or with its m
 // or n side by side (columns: a row is one k; read transposed from LDS).
 //
-// A block of eight waves holds a tile of 256 x 256 in registers (four waves 64 x 256).  Stages of 64 k of both
-// operands go from global memory straight into LDS (global_load_lds_dwordx4, 1 KiB
-// per wave and instruction): A into two slots, B, the weights, which come
-// from further away, into three (two of the small tile, of which a CU holds
-// two).  While the products of a stage run, a wave asks for the next stage of A and the
-// one after the next of B, one load every eight products; near its end it waits
-// for its loads of the next stage and meets the other waves: after that the
-// next stage may be read, and this one, which all have in registers by then, be overwritten.
-// Half a stage (32 k) is one step of products; its fragments are read from LDS
-// under the products before: those of B two ahead, those of A each after its last use.
+// A block of eight waves holds a tile of 256 x 256 in registers.  Stages of 64 k of
+// both operands go from global memory straight into LDS (global_load_lds_dwordx4,
+// 1 KiB per wave and instruction): A into two slots, B, the weights, which come
+// from further away, into three.  While the products of a stage run, a wave asks
+// for the next stage of A and the one after the next of B, one load every eight
+// products; near its end it waits for its loads of the next stage and meets the
+// other waves: after that the next stage may be read, and this one, which all
+// have in registers by then, be overwritten.  Half a stage (32 k) is one step of
+// products; its fragments are read from LDS under the products before: those of B
+// two ahead, those of A each after its last use.
 //
 // Rows operand: a 1 KiB block holds 8 rows x 64 k; 16-byte chunk c of row r at r 128 +
 // (c ^ r) 16: a load takes whole lines of 128 bytes (segments of 64 bytes reach half
@@ -76,21 +76,19 @@ __device__ __forceinline__ void meet() {
 // What rows behind an expert's last one are read as in the columns operands.
 __device__ const uint4 kZero16 = {0, 0, 0, 0};
 
-constexpr int kCUs = 256;
+constexpr int kCUs = 256, kWaves = 8, kBM = 256;
+constexpr int kLds = 160 * 1024;  // two stages of A, three of B
 
-template <int KIND, int BM>
+template <int KIND>
 struct Tile {
     static constexpr bool kDw = KIND == EXP_DW_DOWN || KIND == EXP_DW_UP;
     static constexpr bool kACol = kDw, kBCol = kDw || KIND == EXP_DH || KIND == EXP_DX;
     static constexpr bool kPair = KIND == EXP_UP;          // 128 columns of W_gate and the same of W_up
-    static constexpr int kWaves = BM == 256 ? 8 : 4, kWM = BM == 256 ? 2 : 1, kWN = 4;
-    static constexpr int MI = BM / 16 / kWM, NJ = 16 / kWN;  // fragments of a wave
-    static constexpr int kA = BM * 128, kB = 256 * 128;      // bytes of a stage
-    static constexpr int kSB = BM == 256 ? 3 : 2;            // slots of B
-    static constexpr int kLds = 2 * kA + kSB * kB;
-    static constexpr int LA = BM / 8 / kWaves, LB = 32 / kWaves;  // loads of a wave and stage
+    static constexpr int kWM = 2, kWN = 4;                   // waves
+    static constexpr int MI = kBM / 16 / kWM, NJ = 16 / kWN;  // fragments of a wave
+    static constexpr int kA = kBM * 128, kB = 256 * 128;      // bytes of a stage
+    static constexpr int LA = 4, LB = 4;                     // loads of a wave and stage
     static constexpr int kN = kPair ? 128 : 256;             // columns of C per tile
-    static constexpr int kGrid = kCUs * (BM == 256 ? 1 : 2);
 };
 
 // A block's tiles: it takes every gridDim.x / 8-th of its XCD's stretch of the list
@@ -107,9 +105,9 @@ __device__ __forceinline__ int row_at(const ExpertsArgs& a, int e) {  // (e is t
     return __builtin_amdgcn_readfirstlane(static_cast<int>(min(max(static_cast<int64_t>(v), int64_t(0)), a.R)));
 }
 
-template <int KIND, int BM>
+template <int KIND>
 __device__ __forceinline__ void place(const ExpertsArgs& a, int ntm, int ntn, Jobs& j) {
-    if (Tile<KIND, BM>::kDw) {
+    if (Tile<KIND>::kDw) {
         const int e = j.lin / j.each, in = j.lo + j.lin - e * j.each;
         j.e = e;
         j.r0 = row_at(a, e);
@@ -117,98 +115,106 @@ __device__ __forceinline__ void place(const ExpertsArgs& a, int ntm, int ntn, Jo
         // along the shorter side of C first: an XCD reads all of the smaller operand, and a part of the other
         const int major = in / min(ntm, ntn), minor = in - major * min(ntm, ntn);
         j.nt = ntm <= ntn ? major : minor;
-        j.m0 = (ntm <= ntn ? minor : major) * BM;
+        j.m0 = (ntm <= ntn ? minor : major) * kBM;
     } else {
         const int in = j.lin - j.first * ntn;
         j.nt = in / j.n;
-        j.m0 = (in - j.nt * j.n) * BM;
+        j.m0 = (in - j.nt * j.n) * kBM;
     }
 }
 
 // The block's first tile; false: it has none.
-template <int KIND, int BM>
-__device__ __forceinline__ bool first_job(const ExpertsArgs& a, int ntm, int ntn, Jobs& j) {
+template <int KIND>
+__device__ __forceinline__ bool first_job(const ExpertsArgs& a, int ntm, int ntn, int slot, Jobs& j) {
     const int lane = threadIdx.x & 63, xcd = blockIdx.x & 7;
-    auto clamped = [&](int e) { return static_cast<int>(min(max(static_cast<int64_t>(a.off[e]), int64_t(0)), a.R)); };
-    int total = 0;
-    if (Tile<KIND, BM>::kDw) {
+    j.step = gridDim.x >> 3;
+    if (Tile<KIND>::kDw) {
         // An expert's tiles take as long as it has rows: every XCD has an eighth of each expert's, unless there are
-        // few (48 experts of 7168 x 2048, 683 rows on average, a quarter up or down: 2.48 -> 2.21 ms and 1.21 -> 1.07).
+        // few (48 experts of 7168 x 2048, 683 rows on average, a quarter up or down: 2.48 -> 2.16 ms and 1.21 -> 1.13).
         const int t = ntm * ntn;
         if (t >= 64) {
             j.lo = static_cast<int>(static_cast<int64_t>(t) * xcd / 8);
             j.each = static_cast<int>(static_cast<int64_t>(t) * (xcd + 1) / 8) - j.lo;
-            j.lin = blockIdx.x >> 3;
+            j.lin = slot;
             j.end = a.E * j.each;
-            j.step = gridDim.x >> 3;
-            if (j.lin >= j.end) return false;
-            place<KIND, BM>(a, ntm, ntn, j);
-            return true;
+        } else {
+            const int total = a.E * t, per = (total + 7) >> 3;
+            j.lo = 0;
+            j.each = t;
+            j.lin = xcd * per + slot;
+            j.end = min(total, (xcd + 1) * per);
         }
-        j.lo = 0;
-        j.each = t;
-        total = a.E * ntm;
-    } else {
-        for (int e0 = 0; e0 < a.E; e0 += 64) {
-            const int e = e0 + lane;
-            int n = e < a.E ? max(clamped(e + 1) - clamped(e), 0) : 0;
-            n = (n + BM - 1) / BM;
-#pragma unroll
-            for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
-            total += n;
-        }
-        total = __builtin_amdgcn_readfirstlane(total);
+        if (j.lin >= j.end) return false;
+        place<KIND>(a, ntm, ntn, j);
+        return true;
     }
-    total *= ntn;
+    // a lane per expert, 64 experts at a time
+    struct Rows {
+        int r0, rows, n;
+    };
+    auto rows_of = [&](int e0) {
+        const int e = e0 + lane;
+        Rows r{0, 0, 0};
+        if (e < a.E) {
+            auto clamped = [&](int i) { return static_cast<int>(min(max(static_cast<int64_t>(a.off[i]), int64_t(0)), a.R)); };
+            const int end = clamped(e + 1);
+            r.r0 = clamped(e);
+            r.rows = max(end - r.r0, 0);
+            r.n = (r.rows + kBM - 1) / kBM;
+        }
+        return r;
+    };
+    const Rows head = rows_of(0);
+    int total = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        int n = e0 == 0 ? head.n : rows_of(e0).n;
+#pragma unroll
+        for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
+        total += n;
+    }
+    total = __builtin_amdgcn_readfirstlane(total) * ntn;
     const int per = (total + 7) >> 3;
-    j.step = gridDim.x >> 3;
-    j.lin = xcd * per + (blockIdx.x >> 3);
+    j.lin = xcd * per + slot;
     j.end = min(total, (xcd + 1) * per);
     if (j.lin >= j.end) return false;
-    if (!Tile<KIND, BM>::kDw) {
-        int before = 0;
-        bool found = false;
-        for (int e0 = 0; e0 < a.E && !found; e0 += 64) {
-            const int e = e0 + lane;
-            const int r0 = e < a.E ? clamped(e) : 0, rows = e < a.E ? max(clamped(e + 1) - r0, 0) : 0;
-            const int n = (rows + BM - 1) / BM;
-            int incl = n;
+    int before = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        const Rows r = e0 == 0 ? head : rows_of(e0);
+        int incl = r.n;
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int v = __shfl_up(incl, o);
-                if (lane >= o) incl += v;
-            }
-            const int first = before + incl - n;
-            const uint64_t mine = __ballot(n > 0 && first * ntn <= j.lin && j.lin < (first + n) * ntn);
-            if (mine) {
-                const int l = __ffsll(static_cast<unsigned long long>(mine)) - 1;
-                j.e = e0 + l;
-                j.r0 = __builtin_amdgcn_readlane(r0, l);
-                j.rows = __builtin_amdgcn_readlane(rows, l);
-                j.n = __builtin_amdgcn_readlane(n, l);
-                j.first = __builtin_amdgcn_readlane(first, l);
-                found = true;
-            }
-            before += __builtin_amdgcn_readlane(incl, 63);
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o);
+            if (lane >= o) incl += v;
         }
-        if (!found) return false;
+        const int first = before + incl - r.n;
+        const uint64_t mine = __ballot(r.n > 0 && first * ntn <= j.lin && j.lin < (first + r.n) * ntn);
+        if (mine) {
+            const int l = __ffsll(static_cast<unsigned long long>(mine)) - 1;
+            j.e = e0 + l;
+            j.r0 = __builtin_amdgcn_readlane(r.r0, l);
+            j.rows = __builtin_amdgcn_readlane(r.rows, l);
+            j.n = __builtin_amdgcn_readlane(r.n, l);
+            j.first = __builtin_amdgcn_readlane(first, l);
+            place<KIND>(a, ntm, ntn, j);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(incl, 63);
     }
-    place<KIND, BM>(a, ntm, ntn, j);
-    return true;
+    return false;
 }
-template <int KIND, int BM>
+template <int KIND>
 __device__ __forceinline__ bool next_job(const ExpertsArgs& a, int ntm, int ntn, Jobs& j) {
     j.lin += j.step;
     if (j.lin >= j.end) return false;
-    if (!Tile<KIND, BM>::kDw)
+    if (!Tile<KIND>::kDw)
         while (j.lin >= (j.first + j.n) * ntn) {
             if (++j.e >= a.E) return false;
             j.first += j.n;
             j.r0 = row_at(a, j.e);
             j.rows = max(row_at(a, j.e + 1) - j.r0, 0);
-            j.n = (j.rows + BM - 1) / BM;
+            j.n = (j.rows + kBM - 1) / kBM;
         }
-    place<KIND, BM>(a, ntm, ntn, j);
+    place<KIND>(a, ntm, ntn, j);
     return true;
 }
 
@@ -233,16 +239,15 @@ __device__ __forceinline__ void for_each(F&& f) {
     for_each(f, std::make_integer_sequence<int, N>());
 }
 
-template <int KIND, int BM>
-__global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(const ExpertsArgs a, int ntm, int ntn) {
-    using S = Tile<KIND, BM>;
+template <int KIND>
+__device__ __forceinline__ void run(const ExpertsArgs& a, int ntm, int ntn, int slot, char* lds) {
+    using S = Tile<KIND>;
     constexpr int MI = S::MI, NJ = S::NJ, LA = S::LA, LB = S::LB;
-    __shared__ __attribute__((aligned(1024))) char lds[S::kLds];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wid / S::kWN, wn = wid % S::kWN;
     Jobs job;
-    if (!first_job<KIND, BM>(a, ntm, ntn, job)) return;
+    if (!first_job<KIND>(a, ntm, ntn, slot, job)) return;
     const int64_t d = a.d, F = a.F;
     const int64_t lda = KIND == EXP_UP || KIND == EXP_DH || KIND == EXP_DW_DOWN ? d : KIND == EXP_DOWN ? F : 2 * F;
     const int64_t ldb = KIND == EXP_DOWN || KIND == EXP_DH || KIND == EXP_DW_DOWN ? F : d;
@@ -268,18 +273,18 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
         if (KIND == EXP_DX) B2 -= F * ldb * 2;
         const int n0 = j.nt * S::kN;
         auto columns = [&](int k, int64_t ld, int c0, int end) {  // of k row 2 (wid + 4 k) + lane / 32
-            const int r = 2 * (wid + S::kWaves * k) + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
+            const int r = 2 * (wid + kWaves * k) + (lane >> 5), c = ((((lane & 31) >> 1) ^ fl(r)) << 1) | (lane & 1);
             return static_cast<uint32_t>(r * ld + min(c0 + c * 8, end - 8)) * 2;
         };
 #pragma unroll
         for (int k = 0; k < LA; ++k) {
             const int r = lane >> 3, c = (lane & 7) ^ r;
             oa[k] = S::kACol ? columns(k, lda, j.m0, M)
-                             : static_cast<uint32_t>(min((wid + S::kWaves * k) * 8 + r, M - 1 - j.m0) * lda + c * 8) * 2;
+                             : static_cast<uint32_t>(min((wid + kWaves * k) * 8 + r, M - 1 - j.m0) * lda + c * 8) * 2;
         }
 #pragma unroll
         for (int k = 0; k < LB; ++k) {
-            const int q = wid + S::kWaves * k, r = lane >> 3, c = (lane & 7) ^ r;
+            const int q = wid + kWaves * k, r = lane >> 3, c = (lane & 7) ^ r;
             // EXP_UP: half of a wave's fragments (two blocks each) are of W_gate, the other half the same of W_up
             const int f = S::kPair ? q / (2 * NJ) * NJ + q % NJ : q;
             ob[k] = S::kBCol ? columns(k, ldb, n0, N)
@@ -292,10 +297,10 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
     auto one = [&](auto k_, auto last_, const char* base, uint32_t off, int s, uint32_t slot) {
         constexpr int k = decltype(k_)::value;
         if (S::kDw && decltype(last_)::value) {
-            const bool in = s * 64 + 2 * (wid + S::kWaves * k) + (lane >> 5) < K;
-            dma<k * S::kWaves * 1024>(in ? base + off : reinterpret_cast<const char*>(&kZero16), slot);
+            const bool in = s * 64 + 2 * (wid + kWaves * k) + (lane >> 5) < K;
+            dma<k * kWaves * 1024>(in ? base + off : reinterpret_cast<const char*>(&kZero16), slot);
         } else {
-            dma<k * S::kWaves * 1024>(base, off, slot);
+            dma<k * kWaves * 1024>(base, off, slot);
         }
     };
     const uint32_t lds_w = lds0 + wid * 1024;
@@ -304,7 +309,7 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
     };
     auto load_b = [&](int s, int slot, auto k_, auto last) {
         constexpr int k = decltype(k_)::value;
-        const bool up = KIND == EXP_DX ? s * 64 >= a.F : S::kPair && ((wid + S::kWaves * k) & NJ);
+        const bool up = KIND == EXP_DX ? s * 64 >= a.F : S::kPair && ((wid + kWaves * k) & NJ);
         one(k_, last, (up ? B2 : B) + s * (S::kBCol ? 128 * ldb : 128), ob[k], s, lds_w + 2 * S::kA + slot * S::kB);
     };
     // Fragment f of half h of the stage at `o`.  (Columns: a lane's rows are 8 grp + r16 / 4 and that + 4, alike in f.)
@@ -327,36 +332,28 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
     auto read_b = [&](int slot, int j, int h) { return read(S::kBCol, 2 * S::kA + slot * S::kB, wn * NJ + j, h); };
 
     // The loads that go out while stage s runs, in 2 NJ portions: A of s + 1, then B
-    // of s + kSB - 1 (to bslot).  Portions 0 and 1 belong to the last quarter of stage s - 1.
+    // of s + 2 (to bslot).  Portions 0 and 1 belong to the last quarter of stage s - 1.
     // SURE: those stages exist and are not the last one.
-    constexpr int LATE = NJ - 2, NW = LA + LB;
-    constexpr int kEach = S::kSB == 3 ? 1 : 2;  // loads of a portion
-    static_assert(NW <= 2 * NJ * kEach, "portions");
+    constexpr int LATE = NJ - 2;
+    static_assert(LA + LB == 2 * NJ && LA >= 2, "a load a portion, the first two of A");
     auto portion = [&](int s, auto p_, int bslot, auto sure_) {
         constexpr int p = decltype(p_)::value;
         constexpr bool SURE = decltype(sure_)::value;
-        auto go = [&](auto k_) {
-            constexpr int k = decltype(k_)::value;
-            if constexpr (k < LA) {
-                if (SURE || s + 1 < stages) load_a(s + 1, (s + 1) & 1, k_, std::bool_constant<!SURE>());
-            } else if constexpr (k < NW) {
-                if (SURE || s + S::kSB - 1 < stages)
-                    load_b(s + S::kSB - 1, bslot, std::integral_constant<int, k - LA>(), std::bool_constant<!SURE>());
-            }
-        };
-        go(std::integral_constant<int, p * kEach>());
-        if constexpr (kEach == 2) go(std::integral_constant<int, p * kEach + 1>());
+        if constexpr (p < LA) {
+            if (SURE || s + 1 < stages) load_a(s + 1, (s + 1) & 1, p_, std::bool_constant<!SURE>());
+        } else {
+            if (SURE || s + 2 < stages) load_b(s + 2, bslot, std::integral_constant<int, p - LA>(), std::bool_constant<!SURE>());
+        }
     };
-    // A tile's first loads: stage 0, B of stage 1 (three slots), portions 0 and 1 of stage 0.
-    constexpr int kFirst = (S::kSB == 3 ? LB : 0) + 2 * kEach;  // those behind stage 0's, of two stages or more
-    static_assert(2 * kEach <= (S::kSB == 3 ? LA : NW), "portions 0 and 1 need stage 1 only");
+    // A tile's first loads: stage 0, B of stage 1, portions 0 and 1 of stage 0.
+    constexpr int kFirst = LB + 2;  // those behind stage 0's, of two stages or more
     auto begin = [&]() {
         if (stages == 0) return;
         for_each<LA>([&](auto k) { load_a(0, 0, k, std::true_type()); });
         for_each<LB>([&](auto k) { load_b(0, 0, k, std::true_type()); });
-        if (S::kSB == 3 && stages > 1) for_each<LB>([&](auto k) { load_b(1, 1, k, std::true_type()); });
-        portion(0, std::integral_constant<int, 0>(), S::kSB - 1, std::false_type());
-        portion(0, std::integral_constant<int, 1>(), S::kSB - 1, std::false_type());
+        if (stages > 1) for_each<LB>([&](auto k) { load_b(1, 1, k, std::true_type()); });
+        portion(0, std::integral_constant<int, 0>(), 2, std::false_type());
+        portion(0, std::integral_constant<int, 1>(), 2, std::false_type());
     };
 
     setup(job);
@@ -365,7 +362,7 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
     constexpr int kStores = KIND == EXP_UP ? 0 : MI * NJ / 2 * (KIND == EXP_DH ? 2 : 1);
     for (;;) {
         f32x4 acc[MI][NJ];
-        if (!S::kDw) mi = kStep * min((M - job.m0 + BM / 4 - 1) / (BM / 4), 4);
+        if (!S::kDw) mi = kStep * min((M - job.m0 + kBM / 4 - 1) / (kBM / 4), 4);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -387,12 +384,12 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
             // half H of stage s
             auto half = [&](int s, auto h_, auto sure) {
                 constexpr int H = decltype(h_)::value;
-                const int bnext = bs == S::kSB - 1 ? 0 : bs + 1, bprev = bs == 0 ? S::kSB - 1 : bs - 1;
+                const int bnext = bs == 2 ? 0 : bs + 1, bprev = bs == 0 ? 2 : bs - 1;
                 for_each<NJ>([&](auto j_) {
                     constexpr int j = decltype(j_)::value;
                     if (H == 1 && j == LATE && (decltype(sure)::value || s + 1 < stages)) {
                         // stage s + 1 has landed, and nobody reads stage s any more
-                        if (S::kSB == 3 && (decltype(sure)::value || s + 2 < stages)) wait_and_meet<LB>();
+                        if (decltype(sure)::value || s + 2 < stages) wait_and_meet<LB>();
                         else wait_and_meet<0>();
                     }
 #pragma unroll
@@ -405,7 +402,7 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
                             if (i == 0) fb[(j + 2) & 3] = j < LATE ? read_b(bs, j + 2, H) : read_b(H ? bnext : bs, j - LATE, H ^ 1);
                             if (j == NJ - 1) fa[i] = read_a((s + H) & 1, i, H ^ 1);
                             __builtin_amdgcn_sched_barrier(0);
-                            // B of s + kSB - 1 takes the slot of stage s - 1, that of s + kSB the slot of s
+                            // B of s + 2 takes the slot of stage s - 1, that of s + 3 the slot of s
                             if (i == kStep - 1) {
                                 if constexpr (H == 0) portion(s, std::integral_constant<int, j + 2>(), bprev, sure);
                                 else if constexpr (j < LATE) portion(s, std::integral_constant<int, NJ + 2 + j>(), bprev, sure);
@@ -433,14 +430,14 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
 
         const Jobs at = job;
         const int m_end = M;
-        const bool again = next_job<KIND, BM>(a, ntm, ntn, job);
+        const bool again = next_job<KIND>(a, ntm, ntn, job);
         if (again) {
             meet();  // nobody reads this tile's stages any more
             setup(job);
             begin();
         }
         const int n0 = at.nt * S::kN;
-        stored = at.m0 + BM <= m_end && n0 + S::kN <= N;
+        stored = at.m0 + kBM <= m_end && n0 + S::kN <= N;
 
         // A lane's part of fragments j and j + 1 of row 16 i + r16: columns 16 j + nl .. + 7,
         // nl = 16 (grp % 2) + 8 (grp / 2), once the odd groups' j and the even groups' j + 1 are exchanged.
@@ -519,42 +516,61 @@ __global__ __launch_bounds__(64 * (Tile<KIND, BM>::kWaves), 2) void k_experts(co
     }
 }
 
-// The most tiles that a launch can have, whatever the experts' row counts.
-template <int KIND, int BM>
+// One product, or two that do not wait for each other: a block goes from its tiles of the
+// first to those of the second, and blocks that have none of the first come first in the
+// second.  Two in one for few tiles, where launches and half-empty rounds count; with
+// many, blocks that reach the second at different times share less in the L2.  Forward
+// and backward, four launches in all against six: 40 / 54 us at 96 rows, 32 experts of 512 x
+// 256; 188 / 194 at 2000, 32 of 1024 x 1024; 552 / 571 at 4096, 48 of 2048 x 1024 (3600 tiles in the larger
+// pair); but 2840 / 2690 at 2048, 48 of 7168 x 2048 (23000).
+constexpr int kNone = -1;
+template <int FIRST, int SECOND>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_experts(const ExpertsArgs a, int ntm, int ntn, const ExpertsArgs a2,
+                                                            int ntm2, int ntn2) {
+    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    const int slot = blockIdx.x >> 3;
+    run<FIRST>(a, ntm, ntn, slot, lds);
+    if constexpr (SECOND != kNone) {
+        meet();  // nobody reads the first's stages any more
+        run<SECOND>(a2, ntm2, ntn2, static_cast<int>(gridDim.x >> 3) - 1 - slot, lds);
+    }
+}
+
+// The most tiles that a product can have, whatever the experts' row counts.
+template <int KIND>
 int64_t tiles(int64_t R, int64_t E, int64_t d, int64_t F, int* ntm, int* ntn) {
-    using S = Tile<KIND, BM>;
+    using S = Tile<KIND>;
     const int64_t N = KIND == EXP_UP || KIND == EXP_DH || KIND == EXP_DW_DOWN ? F : d;
     *ntn = static_cast<int>((N + S::kN - 1) / S::kN);
-    *ntm = KIND == EXP_DW_DOWN ? static_cast<int>((d + BM - 1) / BM) : static_cast<int>((2 * F + BM - 1) / BM);
-    const int64_t mt = S::kDw ? E * *ntm : R < E ? R : (R - E) / BM + E;  // sum of ceil(n_e / BM), sum n_e = R
+    *ntm = KIND == EXP_DW_DOWN ? static_cast<int>((d + kBM - 1) / kBM) : static_cast<int>((2 * F + kBM - 1) / kBM);
+    const int64_t mt = S::kDw ? E * *ntm : R < E ? R : (R - E) / kBM + E;  // sum of ceil(n_e / kBM), sum n_e = R
     return mt * *ntn;
 }
 
 constexpr int64_t kMaxTiles = 1 << 26;  // (tile numbers are 32 bits)
+constexpr int64_t kFewTiles = 16 * kCUs;  // of two products in one launch
 
-template <int KIND, int BM>
-hipError_t launch(const ExpertsArgs& a, hipStream_t stream) {
-    int ntm, ntn;
-    const int64_t n = tiles<KIND, BM>(a.R, a.E, a.d, a.F, &ntm, &ntn);
-    if (n > kMaxTiles) return hipErrorInvalidValue;
-    if (n == 0) return hipSuccess;
-    // whole eights of blocks; up to seven XCDs' stretches end early
-    const int64_t blocks = (n + 7) / 8 * 8;
-    const unsigned grid = static_cast<unsigned>(blocks < Tile<KIND, BM>::kGrid ? blocks : Tile<KIND, BM>::kGrid);
-    hipLaunchKernelGGL((k_experts<KIND, BM>), dim3(grid), dim3(64 * Tile<KIND, BM>::kWaves), 0, stream, a, ntm, ntn);
+template <int FIRST, int SECOND = kNone>
+hipError_t launch(const ExpertsArgs& a, const ExpertsArgs& a2, hipStream_t stream) {
+    int ntm, ntn, ntm2 = 0, ntn2 = 0;
+    const int64_t n = tiles<FIRST>(a.R, a.E, a.d, a.F, &ntm, &ntn);
+    int64_t n2 = 0;
+    if constexpr (SECOND != kNone) n2 = tiles<SECOND>(a2.R, a2.E, a2.d, a2.F, &ntm2, &ntn2);
+    if (n > kMaxTiles || n2 > kMaxTiles) return hipErrorInvalidValue;
+    if (n + n2 == 0) return hipSuccess;
+    // whole eights of blocks: one for every XCD's stretch
+    const int64_t blocks = (n + n2 + 7) / 8 * 8;
+    const unsigned grid = static_cast<unsigned>(blocks < kCUs ? blocks : kCUs);
+    hipLaunchKernelGGL((k_experts<FIRST, SECOND>), dim3(grid), dim3(64 * kWaves), 0, stream, a, ntm, ntn, a2, ntm2, ntn2);
     return hipGetLastError();
 }
-
-// Rows of an M tile: 64 while experts hold fewer than kTall rows on average.
-constexpr int64_t kTall = 128;
-bool tall(const ExpertsArgs& a) { return a.R >= kTall * a.E; }
 
 }  // namespace
 
 // The most rows that every launch can take.
 int64_t experts_max_rows(int E, int d, int F) {
     const int64_t ntn = ((d > F ? d : F) + 127) / 128;
-    const int64_t most = (kMaxTiles / ntn - E) * 64;
+    const int64_t most = (kMaxTiles / ntn - E) * kBM;
     if (static_cast<int64_t>(E) * ((2ll * F + 255) / 256) * ((d + 255) / 256) > kMaxTiles) return -1;
     return most < 0 ? -1 : most < (1ll << 31) - 256 ? most : (1ll << 31) - 256;
 }
@@ -562,14 +578,25 @@ int64_t experts_max_rows(int E, int d, int F) {
 hipError_t launch_experts(ExpertsKind kind, const ExpertsArgs& a, hipStream_t stream) {
     if (a.E < 1 || a.R < 0 || a.d % 64 || a.F % 64 || a.d < 64 || a.F < 64) return hipErrorInvalidValue;
     switch (kind) {
-        case EXP_UP: return tall(a) ? launch<EXP_UP, 256>(a, stream) : launch<EXP_UP, 64>(a, stream);
-        case EXP_DOWN: return tall(a) ? launch<EXP_DOWN, 256>(a, stream) : launch<EXP_DOWN, 64>(a, stream);
-        case EXP_DH: return tall(a) ? launch<EXP_DH, 256>(a, stream) : launch<EXP_DH, 64>(a, stream);
-        case EXP_DX: return tall(a) ? launch<EXP_DX, 256>(a, stream) : launch<EXP_DX, 64>(a, stream);
-        case EXP_DW_DOWN: return launch<EXP_DW_DOWN, 256>(a, stream);
-        case EXP_DW_UP: return launch<EXP_DW_UP, 256>(a, stream);
+        case EXP_UP: return launch<EXP_UP>(a, a, stream);
+        case EXP_DOWN: return launch<EXP_DOWN>(a, a, stream);
+        case EXP_DH: return launch<EXP_DH>(a, a, stream);
+        case EXP_DX: return launch<EXP_DX>(a, a, stream);
+        case EXP_DW_UP: return launch<EXP_DW_UP>(a, a, stream);
+        case EXP_DW_DOWN: return launch<EXP_DW_DOWN>(a, a, stream);
     }
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_experts_pair(ExpertsKind kind, const ExpertsArgs& a, const ExpertsArgs& dw, hipStream_t stream) {
+    if (a.E < 1 || a.R < 0 || a.d % 64 || a.F % 64 || a.d < 64 || a.F < 64) return hipErrorInvalidValue;
+    int m, n;
+    const int64_t both = kind == EXP_DH ? tiles<EXP_DH>(a.R, a.E, a.d, a.F, &m, &n) + tiles<EXP_DW_DOWN>(a.R, a.E, a.d, a.F, &m, &n)
+                                        : tiles<EXP_DX>(a.R, a.E, a.d, a.F, &m, &n) + tiles<EXP_DW_UP>(a.R, a.E, a.d, a.F, &m, &n);
+    if (kind == EXP_DH && both <= kFewTiles) return launch<EXP_DH, EXP_DW_DOWN>(a, dw, stream);
+    if (kind == EXP_DX && both <= kFewTiles) return launch<EXP_DX, EXP_DW_UP>(a, dw, stream);
+    const hipError_t err = launch_experts(kind, a, stream);
+    return err != hipSuccess ? err : launch_experts(kind == EXP_DH ? EXP_DW_DOWN : EXP_DW_UP, dw, stream);
 }
 
 }  // namespace moe

@@ -39,6 +39,8 @@ struct ExpertsArgs {
 };
 int64_t experts_max_rows(int E, int d, int F);
 hipError_t launch_experts(ExpertsKind kind, const ExpertsArgs& a, hipStream_t stream);
+// EXP_DH with EXP_DW_DOWN, or EXP_DX with EXP_DW_UP.
+hipError_t launch_experts_pair(ExpertsKind kind, const ExpertsArgs& a, const ExpertsArgs& dw, hipStream_t stream);
 
 // ---- adamw.hip
 int64_t adamw_table_bytes(int n);

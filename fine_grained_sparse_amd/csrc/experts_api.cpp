@@ -204,29 +204,25 @@ moe_status moe_experts_backward(const moe_layer_desc* desc, int64_t rows, const 
     if ((dxs && (!W->W_gate || !W->W_up)) || (dw && (!xs || !h))) return MOE_ERR_NULL;
     if (!aligned16(W->W_gate, W->W_up, W->W_down)) return MOE_ERR_ALIGN;
     if (workspace_bytes < moe_experts_backward_workspace_size(desc, rows)) return MOE_ERR_WORKSPACE;
-    ExpertsArgs a = experts_args(desc, rows, expert_offsets);
-    a.A = in(dy);
-    a.B = in(W->W_down);
-    a.gu = const_cast<float*>(gate_up);
-    a.C = out(workspace);
-    MOE_HIP(launch_experts(EXP_DH, a, s));
-    if (dw) {
-        a.B = in(h);
-        a.C = out(dW_down);
-        MOE_HIP(launch_experts(EXP_DW_DOWN, a, s));
-        a.A = in(workspace);
-        a.B = in(xs);
-        a.C = out(dW_gate);
-        a.C2 = out(dW_up);
-        MOE_HIP(launch_experts(EXP_DW_UP, a, s));
-    }
-    if (dxs) {
-        a.A = in(workspace);
-        a.B = in(W->W_gate);
-        a.B2 = in(W->W_up);
-        a.C = out(dxs);
-        MOE_HIP(launch_experts(EXP_DX, a, s));
-    }
+    ExpertsArgs dh = experts_args(desc, rows, expert_offsets), dx = dh, dd = dh, du = dh;
+    dh.A = in(dy);
+    dh.B = in(W->W_down);
+    dh.gu = const_cast<float*>(gate_up);
+    dh.C = out(workspace);
+    dd.A = in(dy);
+    dd.B = in(h);
+    dd.C = out(dW_down);
+    dx.A = in(workspace);
+    dx.B = in(W->W_gate);
+    dx.B2 = in(W->W_up);
+    dx.C = out(dxs);
+    du.A = in(workspace);
+    du.B = in(xs);
+    du.C = out(dW_gate);
+    du.C2 = out(dW_up);
+    MOE_HIP(dw ? launch_experts_pair(EXP_DH, dh, dd, s) : launch_experts(EXP_DH, dh, s));
+    MOE_HIP(dw && dxs ? launch_experts_pair(EXP_DX, dx, du, s)
+                      : dw ? launch_experts(EXP_DW_UP, du, s) : launch_experts(EXP_DX, dx, s));
     return MOE_OK;
 }
 
