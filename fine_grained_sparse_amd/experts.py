@@ -69,10 +69,10 @@ def _experts_plan(R, E, d, F):
     return D, nbytes
 
 
-def dispatch(topk_idx, E, *, e0=0, token_mask=None, workspace=None, stream=None):
+def dispatch(topk_idx, E, *, e0=0, token_mask=None, sorted_token=False, workspace=None, stream=None):
     """moe_dispatch: the Order of topk_idx (int32 [T, K]) over experts e0 ..
     e0 + E - 1; token_mask, uint8 or bool [T], is zero for tokens that get no
-    rows."""
+    rows.  sorted_token: write each row's token too."""
     _need(topk_idx, "topk_idx", torch.int32)
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [T, K]")
@@ -85,103 +85,97 @@ def dispatch(topk_idx, E, *, e0=0, token_mask=None, workspace=None, stream=None)
     D, nbytes = _order_plan(T, int(E), K)
     s, ctx = _launch(dev, stream)
     with ctx:
-        counts = torch.empty((E,), dtype=torch.int32, device=dev)
-        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-        token = torch.empty((T * K,), dtype=torch.int32, device=dev)
-        pos = torch.empty((T, K), dtype=torch.int32, device=dev)
+        counts = topk_idx.new_empty((E,))
+        offsets = topk_idx.new_empty((E + 1,))
+        token = topk_idx.new_empty((T * K,)) if sorted_token else None
+        pos = torch.empty_like(topk_idx)
         ws = (workspace or _default_ws).get(dev, nbytes, stream)
-        _call("moe_dispatch", D, _ptr(topk_idx), int(e0), _ptr(token_mask), _ptr(counts), _ptr(offsets), _ptr(token),
-              _ptr(pos), _ptr(ws), nbytes, s)
+        _call("moe_dispatch", D, topk_idx.data_ptr(), int(e0), _ptr(token_mask), counts.data_ptr(), offsets.data_ptr(),
+              _ptr(token), pos.data_ptr(), ws.data_ptr(), nbytes, s)
     return Order(counts, offsets, token, pos)
 
 
-def _rows(t, name, order, d=None, dtype=None, dev=None):
-    """A matrix [rows or T, d] of fp32 or bf16, and pos of the order: (T, K, d)."""
-    _need(t, name, dtype, device=dev)
-    if t.dim() != 2 or t.dtype not in _DT or (d is not None and t.shape[1] != d):
-        raise ValueError(f"{name} must be [.., d] fp32 or bf16" if d is None else f"{name} must be [.., {d}]")
-    pos = order.pos
-    _need(pos, "order.pos", torch.int32, device=t.device)
+def _rows(t, name, order):
+    """Of a matrix [rows or T, d] of fp32 or bf16 and an order: (pos, T, K, d, device, the descriptor)."""
+    _need(t, name)
+    if t.dim() != 2 or t.dtype not in _DT:
+        raise ValueError(f"{name} must be [.., d] fp32 or bf16")
+    dev, d, pos = t.device, t.shape[1], order.pos
+    _need(pos, "order.pos", torch.int32, device=dev)
     if pos.dim() != 2:
         raise ValueError("order.pos must be [T, K]")
-    return (*pos.shape, t.shape[1])
-
-
-def _out(out, name, shape, like, dev):
-    if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=dev)
-    _need(out, name, like.dtype, device=dev)
-    if out.dim() != 2 or out.shape[1] != shape[1]:
-        raise ValueError(f"{name} must be [rows, {shape[1]}]")
-    return out
+    T, K = pos.shape
+    return pos, T, K, d, dev, _rows_desc(T, d, K, _DT[t.dtype])
 
 
 def sort_tokens(x, order, *, out=None, stream=None):
     """moe_sort_tokens: xs [T K, d] (or `out` [rows, d]) with xs[pos[t,k]] = x[t]."""
-    T, K, d = _rows(x, "x", order)
-    dev = x.device
+    pos, T, K, d, dev, D = _rows(x, "x", order)
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows, the order {T} tokens")
+    if out is not None:
+        _need(out, "out", x.dtype, device=dev)
+        if out.dim() != 2 or out.shape[1] != d:
+            raise ValueError(f"out must be [rows, {d}]")
     s, ctx = _launch(dev, stream)
     with ctx:
-        out = _out(out, "out", (T * K, d), x, dev)
-        _call("moe_sort_tokens", _rows_desc(T, d, K, _DT[x.dtype]), _ptr(x), _ptr(order.pos), out.shape[0], _ptr(out), s)
+        if out is None:
+            out = x.new_empty((T * K, d))
+        _call("moe_sort_tokens", D, x.data_ptr(), pos.data_ptr(), out.shape[0], out.data_ptr(), s)
     return out
+
+
+def _tokens(out, residual, rows, T, d, dev):
+    """Checks the optional residual and output [T, d] of calls that return to tokens."""
+    if residual is not None:
+        _need(residual, "residual", rows.dtype, (T, d), dev)
+    if out is not None:
+        _need(out, "out", rows.dtype, (T, d), dev)
 
 
 def sort_tokens_backward(dxs, order, *, residual=None, out=None, stream=None):
     """moe_sort_tokens_backward: dx [T, d] = residual (or 0) + sum_k dxs[pos[t,k]]."""
-    T, K, d = _rows(dxs, "dxs", order)
-    dev = dxs.device
-    if residual is not None:
-        _need(residual, "residual", dxs.dtype, (T, d), dev)
+    pos, T, K, d, dev, D = _rows(dxs, "dxs", order)
+    _tokens(out, residual, dxs, T, d, dev)
     s, ctx = _launch(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty((T, d), dtype=dxs.dtype, device=dev)
-        else:
-            _need(out, "out", dxs.dtype, (T, d), dev)
-        _call("moe_sort_tokens_backward", _rows_desc(T, d, K, _DT[dxs.dtype]), _ptr(dxs), _ptr(order.pos),
-              _ptr(residual), dxs.shape[0], _ptr(out), s)
+            out = dxs.new_empty((T, d))
+        _call("moe_sort_tokens_backward", D, dxs.data_ptr(), pos.data_ptr(), _ptr(residual), dxs.shape[0],
+              out.data_ptr(), s)
     return out
 
 
 def combine(y, topk_w, order, *, residual=None, out=None, stream=None):
     """moe_combine: out [T, d] = residual (or 0) + sum_k topk_w[t,k] y[pos[t,k]]."""
-    T, K, d = _rows(y, "y", order)
-    dev = y.device
+    pos, T, K, d, dev, D = _rows(y, "y", order)
     _need(topk_w, "topk_w", torch.float32, (T, K), dev)
-    if residual is not None:
-        _need(residual, "residual", y.dtype, (T, d), dev)
+    _tokens(out, residual, y, T, d, dev)
     s, ctx = _launch(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty((T, d), dtype=y.dtype, device=dev)
-        else:
-            _need(out, "out", y.dtype, (T, d), dev)
-        _call("moe_combine", _rows_desc(T, d, K, _DT[y.dtype]), _ptr(y), _ptr(topk_w), _ptr(order.pos), _ptr(residual),
-              y.shape[0], _ptr(out), s)
+            out = y.new_empty((T, d))
+        _call("moe_combine", D, y.data_ptr(), topk_w.data_ptr(), pos.data_ptr(), _ptr(residual), y.shape[0],
+              out.data_ptr(), s)
     return out
 
 
 def combine_backward(dout, y, topk_w, order, *, need_dy=True, need_dw=True, out=None, stream=None):
     """moe_combine_backward: (dy, of y's shape, or None; d_topk_w fp32 [T, K]
     or None) from dout [T, d].  `out`: the tensor for dy."""
-    T, K, d = _rows(y, "y", order)
-    dev = y.device
+    pos, T, K, d, dev, D = _rows(y, "y", order)
     _need(dout, "dout", y.dtype, (T, d), dev)
     _need(topk_w, "topk_w", torch.float32, (T, K), dev)
     if not (need_dy or need_dw):
         raise ValueError("neither dy nor d_topk_w is wanted")
+    if out is not None:
+        _need(out, "out", y.dtype, y.shape, dev)
     s, ctx = _launch(dev, stream)
     with ctx:
-        dy = None
-        if need_dy:
-            dy = torch.empty_like(y) if out is None else out
-            _need(dy, "out", y.dtype, y.shape, dev)
-        dw = torch.empty((T, K), dtype=torch.float32, device=dev) if need_dw else None
-        _call("moe_combine_backward", _rows_desc(T, d, K, _DT[y.dtype]), _ptr(dout), _ptr(y), _ptr(topk_w),
-              _ptr(order.pos), y.shape[0], _ptr(dy), _ptr(dw), s)
+        dy = None if not need_dy else torch.empty_like(y) if out is None else out
+        dw = torch.empty_like(topk_w) if need_dw else None
+        _call("moe_combine_backward", D, dout.data_ptr(), y.data_ptr(), topk_w.data_ptr(), pos.data_ptr(), y.shape[0],
+              _ptr(dy), _ptr(dw), s)
     return dy, dw
 
 
@@ -218,8 +212,9 @@ def experts_forward(xs, offsets, weights, *, save=True, out=None, stream=None):
         y = torch.empty_like(xs) if out is None else out
         _need(y, "out", torch.bfloat16, (R, d), dev)
         gu = torch.empty((R, 2 * F), dtype=torch.float32, device=dev) if save else None
-        h = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
-        _call("moe_experts_forward", D, R, _ptr(xs), _ptr(offsets), ctypes.byref(W), _ptr(gu), _ptr(h), _ptr(y), s)
+        h = xs.new_empty((R, F))
+        _call("moe_experts_forward", D, R, xs.data_ptr(), offsets.data_ptr(), ctypes.byref(W), _ptr(gu), h.data_ptr(),
+              y.data_ptr(), s)
     return y, Saved(gu, h) if save else None
 
 
@@ -246,9 +241,9 @@ def experts_backward(dy, xs, offsets, weights, saved, *, need_dx=True, need_dW=T
                 _need(g, f"out[{n!r}]", torch.bfloat16, weights[n].shape, dev)
         ws = (workspace or _default_ws).get(dev, nbytes, stream)
         g = grads or {}
-        _call("moe_experts_backward", D, R, _ptr(dy), _ptr(xs), _ptr(offsets), ctypes.byref(W), _ptr(saved.gate_up),
-              _ptr(saved.h), _ptr(dxs), _ptr(g.get("W_gate")), _ptr(g.get("W_up")), _ptr(g.get("W_down")), _ptr(ws),
-              nbytes, s)
+        _call("moe_experts_backward", D, R, dy.data_ptr(), xs.data_ptr(), offsets.data_ptr(), ctypes.byref(W),
+              saved.gate_up.data_ptr(), saved.h.data_ptr(), _ptr(dxs), _ptr(g.get("W_gate")), _ptr(g.get("W_up")),
+              _ptr(g.get("W_down")), ws.data_ptr(), nbytes, s)
     return dxs, grads
 
 

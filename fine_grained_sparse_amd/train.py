@@ -38,6 +38,8 @@ TRAIN_EXPORTS = ("moe_router_train", "moe_balance_workspace_size", "moe_balance_
 
 
 _NOTHING = _Nothing()
+# (the tensors of a call are on a GPU: torch's lazy initialisation is behind them)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class Balance(ctypes.Structure):
@@ -98,7 +100,7 @@ def _launch(dev, stream):
     context in which that device and, for a stream of the caller's, that
     stream are current."""
     if stream is None:
-        same = dev.index == torch.cuda.current_device()
+        same = dev.index == _current_device()
         return _current_raw_stream(dev.index), _NOTHING if same else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")

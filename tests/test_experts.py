@@ -185,7 +185,7 @@ def test_order_matches_the_plain_one(T, E, K, e0, ids, masked):
     g = _gen(T + E)
     idx = _random_idx(g, T, ids, K)
     mask = (torch.rand(T, generator=g) >= masked) if masked else None
-    o = moe.dispatch(idx.to(DEV), E, e0=e0, token_mask=None if mask is None else mask.to(DEV))
+    o = moe.dispatch(idx.to(DEV), E, e0=e0, token_mask=None if mask is None else mask.to(DEV), sorted_token=True)
     counts, off, tok, pos = _order_ref(idx, E, e0, mask)
     assert o.counts.tolist() == counts
     assert o.offsets.tolist() == off
@@ -201,7 +201,8 @@ def test_order_of_repeated_and_foreign_ids(T, K):
     idx[5] = 2 ** 31 - 1
     idx[6] = -2 ** 31
     idx[7] = 4
-    o = moe.dispatch(idx.to(DEV), 6)
+    o = moe.dispatch(idx.to(DEV), 6, sorted_token=True)
+    assert moe.dispatch(idx.to(DEV), 6).sorted_token is None
     counts, off, tok, pos = _order_ref(idx, 6)
     assert o.counts.tolist() == counts and o.offsets.tolist() == off
     assert torch.equal(o.pos.cpu(), pos) and o.sorted_token[:len(tok)].tolist() == tok
