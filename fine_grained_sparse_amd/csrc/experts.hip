@@ -229,6 +229,14 @@ __device__ __forceinline__ uint4 pack8v(const float (&v)[8]) {
     return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
+// The value of the lane 8 further on among its 16.
+__device__ __forceinline__ uint32_t row_ror8(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x128, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint4 row_ror8(uint4 v) {
+    return make_uint4(row_ror8(v.x), row_ror8(v.y), row_ror8(v.z), row_ror8(v.w));
+}
+
 // f(0), f(1), .. f(N - 1), each a constant.
 template <typename F, int... I>
 __device__ __forceinline__ void for_each(F&& f, std::integer_sequence<int, I...>) {
@@ -493,22 +501,32 @@ __device__ __forceinline__ void run(const ExpertsArgs& a, int ntm, int ntn, int 
                     stg16(a.C + row * 2 * F + F + n, pack8v(du));
                 }
             } else {
-                bf16_t* out;
-                if (KIND == EXP_DW_DOWN)
-                    out = a.C + (at.e * d + m) * F;
-                else if (KIND == EXP_DW_UP)
-                    out = m < a.F ? a.C + (at.e * F + m) * d : a.C2 + (at.e * F + m - F) * d;
-                else
-                    out = a.C + (at.r0 + m) * d;
+                // Half of what a lane has goes to the lane of row r16 ^ 8, so that eight lanes write 128
+                // bytes of a row: half-written lines of the L2 reach only part of the memory's rate.
+                uint4 p[2];
 #pragma unroll
                 for (int j = 0; j < NJ; j += 2) {
-                    const int n = n0 + (wn * NJ + j) * 16 + nl;
                     const auto q0 = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][0], acc[i][j][1]),
                                                                      pack2(acc[i][j + 1][0], acc[i][j + 1][1]), false, false);
                     const auto q1 = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][2], acc[i][j][3]),
                                                                      pack2(acc[i][j + 1][2], acc[i][j + 1][3]), false, false);
-                    if (m >= m_end || n >= N) continue;
-                    stg16(out + n, make_uint4(q0[0], q1[0], q0[1], q1[1]));
+                    p[j / 2] = make_uint4(q0[0], q1[0], q0[1], q1[1]);
+                }
+                const bool low = r16 < 8;
+                const uint4 get = row_ror8(low ? p[1] : p[0]);
+                const int n = n0 + wn * NJ * 16 + (low ? 0 : 32) + nl;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int mu = m - r16 + (r16 & 7) + 8 * u;
+                    if (mu >= m_end || n >= N) continue;
+                    bf16_t* out;
+                    if (KIND == EXP_DW_DOWN)
+                        out = a.C + (at.e * d + mu) * F;
+                    else if (KIND == EXP_DW_UP)
+                        out = mu < a.F ? a.C + (at.e * F + mu) * d : a.C2 + (at.e * F + mu - F) * d;
+                    else
+                        out = a.C + (at.r0 + mu) * d;
+                    stg16(out + n, low == (u == 0) ? p[u] : get);
                 }
             }
         }
