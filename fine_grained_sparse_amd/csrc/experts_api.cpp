@@ -26,8 +26,9 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
     } while (0)
 
 constexpr int32_t kMaxTensors = 65536;
+constexpr float kMinEps = 0x1p-40f;  // (far above the root of any subnormal v, which is taken as 0)
 constexpr int64_t kMaxBlocks = 1 << 24;  // (a launch has less than 2^32 threads)
-constexpr int32_t kMaxD = 1 << 24;  // columns of a row: byte offsets within a tile of rows stay below 2^32
+constexpr int32_t kMaxD = 1 << 22;  // columns of a row: byte offsets within a tile of 256 rows stay below 2^32
 
 // The fields of a call on rows: T, d, K and the type.
 moe_status check_rows(const moe_layer_desc* D, int64_t rows) {
@@ -235,7 +236,7 @@ moe_status moe_adamw(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors
     if (!desc || (n_tensors > 0 && !tensors)) return MOE_ERR_NULL;
     if (n_tensors < 0 || n_tensors > kMaxTensors || (desc->step < 1 && !desc->step_device)) return MOE_ERR_SHAPE;
     auto beta = [](double b) { return b >= 0.0 && b < 1.0; };
-    if (!beta(desc->beta_avg) || !beta(desc->beta_sq)) return MOE_ERR_SHAPE;
+    if (!beta(desc->beta_avg) || !beta(desc->beta_sq) || !(desc->eps >= kMinEps)) return MOE_ERR_SHAPE;
     auto type = [](int32_t t) { return t == MOE_F32 || t == MOE_BF16; };
     if (!type(desc->param_dtype) || !type(desc->grad_dtype) || (desc->moment_bits != 32 && desc->moment_bits != 8))
         return MOE_ERR_UNSUPPORTED;

@@ -129,7 +129,8 @@ moe_status moe_router_backward(const moe_layer_desc *desc, const void *x,
  * moe_router_backward), moe_experts_backward, moe_sort_tokens_backward.
  *
  * Descriptor fields used: T, d, E, K, F and act_dtype, with 1 <= K <= 16,
- * 1 <= E <= 1024, T K < 2^31 and d (F) a positive multiple of 64.  E is the
+ * 1 <= E <= 1024, T K < 2^31, d (F) a positive multiple of 64 and at most
+ * 2^22 (2^21).  E is the
  * number of this GPU's experts: K may exceed it.  A row whose place is behind
  * expert_offsets[E], or outside 0 .. rows - 1, belongs to no assignment: it is
  * neither read nor written.                                                 */
@@ -213,7 +214,7 @@ moe_status moe_experts_backward(const moe_layer_desc *desc, int64_t rows,
  * One AdamW step over many tensors (decoupled weight decay), t = step >= 1:
  *   g = grad_scale grad,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g g,
  *   param = (1 - lr weight_decay) param
- *           - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps).
+ *           - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps),  eps >= 2^-40.
  * Moments in 32 bits are fp32.  In 8 bits, 128 consecutive values of a tensor share
  * a scale 2^(s - 127) (one byte s; s = 255: the block holds NaN, as after an
  * infinite or NaN moment in it); m is an E4M3 code (sign, 4 exponent bits with

@@ -52,7 +52,8 @@ def test_adamw_rejects_bad_arguments():
     assert f(_d(), _t(), table=None) == NULL and f(_d(), _t(), table=FAKE_ODD) == ALIGN
     assert f(_d(), *[_t(n=(1 << 36) - 1)] * 3) == SHAPE and f(_d(), _t(), n=65537) == SHAPE
     assert f(_d(), _t(), n=-1) == SHAPE
-    for bad in (dict(step=0), dict(beta_avg=1.0), dict(beta_sq=-0.1), dict(beta_avg=math.nan)):
+    for bad in (dict(step=0), dict(beta_avg=1.0), dict(beta_sq=-0.1), dict(beta_avg=math.nan), dict(eps=0.0),
+                dict(eps=math.nan)):
         assert f(_d(**bad), _t()) == SHAPE, bad
     for bad in (dict(param_dtype=2), dict(grad_dtype=3), dict(moment_bits=16)):
         assert f(_d(**bad), _t()) == UNSUP, bad
@@ -293,3 +294,56 @@ def test_adamw_captured_with_a_step_on_the_device(bits):
             # (1 - beta^t by repeated squaring on the device, and lr as fp32: a few steps of fp32 in the rate)
             assert ((eager[i] - graph[i]).abs() <= 16 * t * E32 * (0.02 * t + eager[i].abs())).all(), (t, i)
         torch.randn(256, 256, device=DEV).sum().item()
+
+
+@pytest.mark.gpu
+def test_eight_bits_past_32_bit_elements():
+    """One tensor of over 2^32 values: codes of its last ones, whose random bits take the high half of the index."""
+    n = (1 << 32) + 1000
+    p, g = torch.zeros(n, dtype=B16, device=DEV), torch.full((n,), 0.37, dtype=B16, device=DEV)
+    opt = moe.AdamW([p], state_bits=8, seed=9, lr=0.25, weight_decay=0.0)
+    opt.step([g])
+    for first in (0, (1 << 32) - 256, 1 << 32):
+        i = torch.arange(first, first + 256)
+        key = _mix((_mix((_mix(torch.tensor(9)) + 1) & 0xFFFFFFFF)) & 0xFFFFFFFF)
+        w = _mix((i % (1 << 32) + key + (i >> 32) * 0x9E3779B9) & 0xFFFFFFFF)
+        v = g[:256].float().cpu()
+        m, q = v * torch.tensor(1 - 0.9), v * torch.tensor(1 - 0.999) * v
+        cm, sm = _encode(m, E4M3, 7, w & 0xFFFF)
+        cv, sv = _encode(q, E5M3, 15, w >> 16)
+        at = slice(first, first + 256)
+        assert torch.equal(opt.exp_avg[0][at].cpu().long(), cm) and torch.equal(opt.exp_avg_sq[0][at].cpu().long(), cv), first
+        assert opt.exp_avg_scale[0][first // 128].item() == sm[0] and opt.exp_avg_sq_scale[0][first // 128].item() == sv[0]
+        up = _mix(w ^ 0x9E3779B9) & 0xFFFF  # p = -0.25 (1 to some steps of fp32), between two bf16
+        assert ((p[at].cpu().float() + 0.25).abs() <= 2.0 ** -9).all() and len(up) == 256
+    assert int((p[-1000:] == 0).sum()) == 0
+
+
+@pytest.mark.gpu
+def test_adamw_on_a_stream_with_new_gradients_each_step():
+    ps, _ = _tensors(F32, F32, 5)
+    a, b = ([torch.nn.Parameter(p.to(DEV)) for p in ps] for _ in range(2))
+    x, y = moe.AdamW(a, state_bits=8), moe.AdamW(b, state_bits=8)
+    s = torch.cuda.Stream()
+    for t in range(3):
+        _, gs = _tensors(F32, F32, 60 + t)
+        gs = [g.to(DEV) for g in gs]
+        x.step(gs)
+        s.wait_stream(torch.cuda.current_stream())
+        y.step(gs, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert all(torch.equal(u, v) for u, v in zip(x.exp_avg + x.exp_avg_sq_scale, y.exp_avg + y.exp_avg_sq_scale))
+    with pytest.raises(ValueError, match="gradients"):
+        x.step(gs[:-1])
+    with pytest.raises(ValueError, match="no gradients"):
+        x.step()
+    with pytest.raises(ValueError, match="shape"):
+        x.step([g[:-1] if g.numel() > 1 else g for g in gs])
+    with pytest.raises(TypeError, match="on the GPU"):
+        x.step(gs, step=3)
+    with pytest.raises(moe.MoeError, match="ALIGN"):
+        x.step([torch.zeros(p.numel() + 1, device=DEV)[1:] for p in ps])
+    with pytest.raises(ValueError, match="values"):
+        moe.AdamW(a, state_bits=8, exp_avg_scale=[torch.zeros(1, dtype=torch.uint8, device=DEV)] * len(a))

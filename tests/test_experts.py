@@ -103,8 +103,8 @@ def test_experts_reject_bad_arguments():
     for f in (fwd, bwd):
         assert f(_k2(act_dtype=moe.MOE_F32)) == UNSUP
         assert f(_k2(w_layout=1)) == UNSUP and f(_k2(w_dtype=2)) == UNSUP
-        for bad in (dict(d=100), dict(F=100), dict(F=0), dict(E=0), dict(E=1025), dict(d=1 << 25),
-                    dict(d=1 << 16, F=1 << 15)):
+        for bad in (dict(d=100), dict(F=100), dict(F=0), dict(E=0), dict(E=1025), dict(d=1 << 23),
+                    dict(d=64, F=1 << 22), dict(d=1 << 16, F=1 << 15)):
             assert f(_k2(**bad)) == SHAPE, bad
         assert f(R=-1) == SHAPE
         most = L.moe_experts_max_rows(ref(D))
@@ -380,6 +380,8 @@ EXPERTS = [  # R, E, d, F, rows' spread
     (96, 32, 512, 256, "skew"), (1, 1, 64, 64, "even"), (1, 8, 64, 64, "one"), (31, 3, 64, 192, "even"),
     (33, 3, 192, 64, "even"), (300, 5, 320, 448, "skew"), (129, 1, 256, 128, "even"), (257, 1, 64, 320, "one"),
     (1000, 4, 576, 192, "skew"), (1537, 3, 448, 640, "skew"), (2048, 70, 128, 128, "skew"), (900, 130, 64, 64, "skew"),
+    # several tiles a block, in pairs of products and one by one
+    (12000, 4, 2048, 2048, "skew"), (9000, 64, 2048, 2048, "skew"),
     (700, 5, 1024, 512, "one"), (5000, 9, 768, 1088, "skew"), (4096, 1, 7168, 256, "even"), (640, 4, 256, 2048, "even"),
 ]
 
@@ -572,3 +574,91 @@ def test_two_calls_on_two_streams():
     for a, b in zip(got, want):
         for n in a:
             assert torch.equal(a[n], b[n]), n
+
+
+# ------------------------------------------------------------ corners and sizes
+@pytest.mark.gpu
+def test_nothing_to_do():
+    for T, K in ((0, 4), (3, 4)):
+        idx = torch.full((T, K), 9, dtype=torch.int32, device=DEV)          # no expert of this GPU's
+        o = moe.dispatch(idx, 5)
+        assert o.offsets.tolist() == [0] * 6 and (o.pos == -1).all()
+        x = torch.randn(T, 64, device=DEV)
+        none = x.new_empty((0, 64))
+        assert moe.sort_tokens(x, o).shape == (T * K, 64)
+        assert moe.sort_tokens(x, o, out=none) is none
+        w = torch.rand(T, K, device=DEV)
+        assert torch.equal(moe.combine(none, w, o, residual=x), x)
+        assert (moe.combine(none, w, o) == 0).all()
+        assert (moe.sort_tokens_backward(none, o) == 0).all()
+        dy, dw = moe.combine_backward(x, none, w, o)
+        assert dy.shape == (0, 64) and (dw == 0).all()
+
+
+@pytest.mark.gpu
+def test_experts_rows_before_the_first_and_a_shared_expert():
+    # rows before offsets[0] are nobody's either
+    sizes, off, W, xs, dy = _experts_case(200, 3, 128, 64, "even", 5)
+    pad = torch.full((7, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    y, saved = moe.experts_forward(torch.cat((pad, xs)), off + 7, W, out=torch.full((207, 128), 7.0, dtype=torch.bfloat16, device=DEV))
+    dxs, grads = moe.experts_backward(torch.cat((pad, dy)), torch.cat((pad, xs)), off + 7, W, saved)
+    want, saved = moe.experts_forward(xs, off, W)
+    wdx, wg = moe.experts_backward(dy, xs, off, W, saved)
+    assert (y[:7] == 7).all() and torch.equal(y[7:], want) and torch.equal(dxs[7:], wdx)
+    for n in wg:  # other rows share a stage: sums in another order
+        _close(grads[n], _experts_ref(xs, dy, W, sizes)[n], n)
+    # the always-on shared expert is one expert with every token; its sum with the routed ones a residual
+    y1, _ = moe.experts_forward(xs, torch.tensor([0, 200], dtype=torch.int32, device=DEV), {n: v[:1] for n, v in W.items()})
+    _close(y1, _experts_ref(xs, dy, {n: v[:1] for n, v in W.items()}, [200])["y"], "shared")
+
+
+@pytest.mark.gpu
+def test_bad_offsets_stay_in_bounds():
+    """Offsets out of range or order are clamped to 0 .. rows; what comes out is not said."""
+    _, off, W, xs, dy = _experts_case(300, 4, 128, 64, "even", 6)
+    good = moe.experts_forward(xs, off, W)[0]
+    for bad in ([-5, 100, 90, 200, 400], [400, 0, 500, -1, 300], [0, 0, 0, 0, 2 ** 31 - 1]):
+        o = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        y, saved = moe.experts_forward(xs, o, W, out=torch.zeros_like(xs))
+        moe.experts_backward(dy, xs, o, W, moe.Saved(torch.zeros_like(saved.gate_up), torch.zeros_like(saved.h)))
+        torch.cuda.synchronize()
+    assert torch.equal(moe.experts_forward(xs, off, W)[0], good)
+
+
+@pytest.mark.gpu
+def test_rows_past_32_bit_offsets():
+    T, K, E, d = 4_300_001, 8, 16, 64                        # 34.4 M rows: 2.2 G values, 4.4 GB
+    idx = torch.randint(0, E, (T, K), device=DEV, dtype=torch.int32, generator=torch.Generator(DEV).manual_seed(1))
+    o = moe.dispatch(idx, E)
+    assert int(o.offsets[-1]) == T * K and torch.equal(o.counts.long(), torch.bincount(idx.flatten(), minlength=E))
+    where = torch.argsort(idx.flatten().long() * (T * K) + torch.arange(T * K, device=DEV))  # no two alike
+    assert torch.equal(o.pos.flatten()[where], torch.arange(T * K, device=DEV, dtype=torch.int32))
+    del where
+    x = torch.randn(T, d, device=DEV, dtype=torch.bfloat16)
+    xs = moe.sort_tokens(x, o)
+    for t in (slice(0, 1000), slice(T // 2, T // 2 + 1000), slice(T - 1000, T)):
+        assert (xs[o.pos[t].long()] == x[t, None]).all()
+    assert torch.equal(moe.sort_tokens_backward(xs, o), 8 * x)     # 8 equal terms: exact
+    w = torch.full((T, K), 0.5, device=DEV)
+    assert torch.equal(moe.combine(xs, w, o), 4 * x)
+    dy, dw = moe.combine_backward(x, xs, w, o)
+    t = slice(T - 1000, T)
+    assert (dy[o.pos[t].long()] == 0.5 * x[t, None]).all()
+    n2 = (x[t].double() ** 2).sum(1)
+    assert ((dw[t].double() - n2[:, None]).abs() <= 64 * E32 * n2[:, None]).all()
+
+
+@pytest.mark.gpu
+def test_experts_past_32_bit_offsets():
+    R, E, d, F = 1_100_003, 2, 64, 1024                      # a and b: 2.25 G values, 9 GB
+    g = torch.Generator(DEV).manual_seed(2)
+    off = torch.tensor([0, 1000, R], dtype=torch.int32, device=DEV)
+    W = {n: (torch.randn(E, r, c, device=DEV, generator=g) * c ** -0.5).to(torch.bfloat16)
+         for n, (r, c) in dict(W_gate=(F, d), W_up=(F, d), W_down=(d, F)).items()}
+    xs, dy = (torch.randn(R, d, device=DEV, generator=g).to(torch.bfloat16) for _ in range(2))
+    y, saved = moe.experts_forward(xs, off, W)
+    dxs, _ = moe.experts_backward(dy, xs, off, W, saved, need_dW=False)
+    tail = slice(R - 500, R)
+    ref = _experts_ref(xs[tail], dy[tail], {n: v[1:] for n, v in W.items()}, [500])
+    _close(y[tail], ref["y"], "y")
+    _close(dxs[tail], ref["dxs"], "dxs")
