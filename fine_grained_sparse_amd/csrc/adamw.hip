@@ -22,8 +22,8 @@
 namespace moe {
 namespace {
 
-constexpr int kPerThread = 8, kSpan = 256 * kPerThread, kRounds = 4;
-constexpr int64_t kChunk = static_cast<int64_t>(kSpan) * kRounds;  // elements of a block
+constexpr int kPerThread = 8, kSpan = 256 * kPerThread, kTurns = 4;
+constexpr int64_t kChunk = static_cast<int64_t>(kSpan) * kTurns;  // elements of a block
 
 // The tensors' table in device memory: an entry each, then each one's first block.
 constexpr int kPiece = 56;  // entries that a launch writes, from its arguments
@@ -52,7 +52,7 @@ struct Step {
     const float* grad_scale;
 };
 
-// The finaliser of MurmurHash3 (Austin Appleby, public domain).
+// A. Appleby's 32-bit mixer (public domain).
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
     h = (h ^ (h >> 16)) * 0x85ebca6bu;
     h = (h ^ (h >> 13)) * 0xc2b2ae35u;
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
     uint8_t *const avg_scale = (uint8_t*)t.avg_scale, *const sq_scale = (uint8_t*)t.sq_scale;
     bf16_t* const copy = (bf16_t*)t.copy;
 #pragma unroll 1
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < kTurns; ++r) {
         const int64_t i = c0 + r * kSpan + tid * kPerThread;
         const int live = static_cast<int>(min(max(n - i, int64_t(0)), int64_t(8)));
         if (c0 + r * kSpan >= n) break;  // (uniform)
@@ -351,13 +351,13 @@ __global__ __launch_bounds__(256) void k_moments(const MomentsTable T) {
         else hi = mid - 1;
     }
     const int64_t n = T.len[lo], c0 = static_cast<int64_t>(blockIdx.x - T.first[lo]) * kChunk;
-    // four values a thread and round, so that a wave's stores are whole lines
+    // four values a thread and turn, so that a wave's stores are whole lines
     auto one = [&](const uint8_t* codes, const uint8_t* scales, float* out, auto value) {
         if (!out) return;
-        uint32_t w[2 * kRounds];
-        int s[2 * kRounds];
+        uint32_t w[2 * kTurns];
+        int s[2 * kTurns];
 #pragma unroll
-        for (int r = 0; r < 2 * kRounds; ++r) {
+        for (int r = 0; r < 2 * kTurns; ++r) {
             const int64_t i = c0 + r * 1024 + threadIdx.x * 4;
             if (i + 4 <= n) {
                 w[r] = *reinterpret_cast<const uint32_t*>(codes + i);
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(256) void k_moments(const MomentsTable T) {
             }
         }
 #pragma unroll
-        for (int r = 0; r < 2 * kRounds; ++r) {
+        for (int r = 0; r < 2 * kTurns; ++r) {
             const int64_t i = c0 + r * 1024 + threadIdx.x * 4;
             if (i + 4 <= n)
                 *reinterpret_cast<float4*>(out + i) = make_float4(value(w[r] << 24, s[r]), value(w[r] << 16, s[r]),

@@ -536,7 +536,7 @@ __device__ __forceinline__ void run(const ExpertsArgs& a, int ntm, int ntn, int 
 
 // One product, or two that do not wait for each other: a block goes from its tiles of the
 // first to those of the second, and blocks that have none of the first come first in the
-// second.  Two in one for few tiles, where launches and half-empty rounds count; with
+// second.  Two in one for few tiles, where launches and idle CUs count; with
 // many, blocks that reach the second at different times share less in the L2.  Forward
 // and backward, four launches in all against six: 40 / 54 us at 96 rows, 32 experts of 512 x
 // 256; 188 / 194 at 2000, 32 of 1024 x 1024; 552 / 571 at 4096, 48 of 2048 x 1024 (3600 tiles in the larger

@@ -12,7 +12,7 @@ namespace {
 // 16 waves takes `per` consecutive assignments, a wave 1/16 of them, 64 at a
 // time: lanes with the same expert find each other by one ballot per bit of the
 // id, so an assignment's place among the wave's is a popcount, and only one
-// lane per expert touches the wave's running counts (LDS).  No atomics: the
+// lane per expert touches the wave's running counts (LDS).  The
 // order never depends on timing, and an expert chosen twice by a token has two
 // places.  What is not this call's (foreign ids, masked tokens) counts as
 // expert E and is dropped.
@@ -178,8 +178,10 @@ struct Div {
 };
 
 // 16 bytes that are read, or written, once in the call, past the caches.  16384 tokens of 7168
-// bf16 columns, top-8, with and without: rows out 355 / 405 us (5.9 TB/s; only with x itself
-// through them: 402), summed back 359 / 410 (5.9), weighted 420 / 451, its gradients 760 / 807 (5.3).
+// bf16 columns, top-8: sorted and summed back in turn 415 + 366 us, 408 + 428 with cached stores
+// (which the next kernel pays for), 405 + 410 with neither, each by itself; the weighted sum and its
+// gradients in turn 404 + 822, 468 + 794 with cached stores.  (x itself is read through the
+// caches: 355 against 402 us.)  5.1 to 5.8 TB/s; a large copy reaches 4.9 here.
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint4 once(const uint4* p) {
     const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
@@ -282,7 +284,8 @@ __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ y, con
 // ones), hold 16 bytes of dout at a time and go over the rows with it.  dy of a
 // row is written where y of it was read.  Eight rows a time, so that dout is read
 // once or twice; one (a block of 1024) where the tokens are too few to fill the chip:
-// 10.1 -> 5.1 us at 64 tokens of 7168 columns, top-8.
+// 10.1 -> 5.4 us at 64 tokens of 7168 columns, top-8.  4001 tokens of 3584, top-16: 176 us (sixteen
+// rows a time, which spilled: 256), 5.2 TB/s.
 template <typename T, int KM, bool DY, bool DW>
 __global__ __launch_bounds__(KM == 1 ? 1024 : 256) void k_gather_backward(const uint4* __restrict__ dout, const uint4* __restrict__ y,
                                                           const float* __restrict__ w, const int32_t* __restrict__ pos,

@@ -31,7 +31,7 @@
  * allocated; concurrent calls, and captured graphs that may run at the same
  * time, need distinct workspaces.  Results do not depend on timing: the same
  * call gives the same bits.  T is at most 2^28 - 65536 (moe_router_train: as
- * moe_router).  T == 0 is a no-op but for loss (0), seq_counts
+ * moe_router; the experts' side: T K < 2^31).  T == 0 is a no-op but for loss (0), seq_counts
  * (zeros) and dW_r (zeros).  A NaN logit of a token that counts (see
  * moe_balance) makes the loss NaN, and that token's gradient as far as it
  * depends on the logit; in tokens that do not count it is harmless.  Logits past
@@ -129,11 +129,12 @@ moe_status moe_router_backward(const moe_layer_desc *desc, const void *x,
  * moe_router_backward), moe_experts_backward, moe_sort_tokens_backward.
  *
  * Descriptor fields used: T, d, E, K, F and act_dtype, with 1 <= K <= 16,
- * 1 <= E <= 1024, T K < 2^31, d (F) a positive multiple of 64 and at most
- * 2^22 (2^21).  E is the
- * number of this GPU's experts: K may exceed it.  A row whose place is behind
- * expert_offsets[E], or outside 0 .. rows - 1, belongs to no assignment: it is
- * neither read nor written.                                                 */
+ * 1 <= E <= 1024, T K < 2^31, d (F) a positive multiple of 64 and at most 2^22
+ * (2^21).  E is the number of this GPU's experts: K may exceed it.  A row whose
+ * place is behind expert_offsets[E], or outside 0 .. rows - 1, belongs to no
+ * assignment: it is neither read nor written.  Offsets that are not ascending
+ * within 0 .. rows are not detected; they are taken as if clamped to it, and what
+ * comes out is not said.                                                     */
 
 /* The order.
  *   topk_idx [T, K] int32; e0: the id of this GPU's first expert; token_mask
@@ -222,8 +223,10 @@ moe_status moe_experts_backward(const moe_layer_desc *desc, int64_t rows,
  * 15 and 3 fraction bits; the value is code x scale.  A new moment x, computed in
  * fp32, is rounded to one of its two neighbours at random, up with the
  * probability that keeps the mean; so is a bf16 parameter.  The random bits are
- * of (seed, step, the tensor's number in `tensors`, the element): with mix the
- * finaliser of MurmurHash3 and all sums modulo 2^32,
+ * of (seed, step, the tensor's number in `tensors`, the element i): with
+ *   mix(h): h = (h ^ (h >> 16)) 0x85ebca6b, h = (h ^ (h >> 13)) 0xc2b2ae35,
+ *           h ^ (h >> 16)          [A. Appleby's 32-bit mixer, public domain]
+ * and all sums and products modulo 2^32,
  *   word = mix(i % 2^32 + mix(mix(mix(seed) + step) + tensor)
  *              + (i / 2^32) 0x9e3779b9);
  * m takes its low 16 bits, v its high ones, a parameter the low ones of
@@ -246,8 +249,8 @@ typedef struct {
 } moe_adamw_desc;
 
 /* One tensor of n elements; 16-byte aligned pointers (scales: any).
- *   copy (may be NULL, and is for bf16 parameters): bf16 [n], receives fp32
- *   parameters rounded to nearest.
+ *   copy: bf16 [n], receives fp32 parameters rounded to nearest; or NULL (as it
+ *   must be with bf16 parameters).
  *   exp_avg, exp_avg_sq: fp32 [n], or uint8 [n] codes with their scales
  *   uint8 [(n + 127) / 128] (NULL with 32 bits).                              */
 typedef struct {
