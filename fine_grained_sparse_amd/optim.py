@@ -153,15 +153,15 @@ class AdamW:
             D.lr = float(lr)
         s, ctx = _launch(self.device, stream)
         with ctx:
-            table = self._tables.get(s)
-            if table is None or torch.cuda.is_current_stream_capturing():
-                # (a captured step writes a table of its own, which the graph's memory keeps)
+            # (a captured step writes a table of its own, which the graph's memory keeps)
+            capturing = torch.cuda.is_current_stream_capturing()
+            table = None if capturing else self._tables.get(s)
+            D.keep_table = int(table is not None)
+            if table is None:
                 table = torch.empty(self._nbytes, dtype=torch.uint8, device=self.device)
-                if not torch.cuda.is_current_stream_capturing():
-                    self._tables[s] = table
-            else:
-                D.keep_table = 1
             _call("moe_adamw", ctypes.byref(D), self._table, len(self.params), table.data_ptr(), self._nbytes, s)
+            if not capturing:
+                self._tables[s] = table  # (not before the call: one that is refused writes none)
         if step is None:
             self.steps += 1
 

@@ -86,6 +86,29 @@ def test_adamw_object_refuses():
         moe.AdamW([p], state_bits=16)
 
 
+def test_a_refused_step_keeps_no_table(monkeypatch):
+    """The call that is refused has written no table: the next one writes it."""
+    opt = object.__new__(moe.AdamW)
+    vars(opt).update(params=[None], grads=[None], device=torch.device("cpu"), state_bits=32, steps=0, seed=0, lr=1e-3,
+                     eps=1e-8, weight_decay=0.0, betas=(0.9, 0.999), _param_dtype=0, _grad_dtype=0, _tables={},
+                     _table=None, _nbytes=256)
+    kept = []
+
+    def call(name, D, *args):
+        kept.append(D._obj.keep_table)
+        if len(kept) == 1:
+            raise moe.MoeError(name, SHAPE)
+    monkeypatch.setattr(optim, "_call", call)
+    monkeypatch.setattr(optim, "_launch", lambda dev, stream: (0, train._NOTHING))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    with pytest.raises(moe.MoeError):
+        opt.step()
+    assert opt.steps == 0 and not opt._tables
+    opt.step()
+    opt.step()
+    assert kept == [0, 0, 1] and opt.steps == 2
+
+
 # ------------------------------------------------------------------- plain form
 def _mix(h):
     h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
@@ -317,6 +340,22 @@ def test_eight_bits_past_32_bit_elements():
         up = _mix(w ^ 0x9E3779B9) & 0xFFFF  # p = -0.25 (1 to some steps of fp32), between two bf16
         assert ((p[at].cpu().float() + 0.25).abs() <= 2.0 ** -9).all() and len(up) == 256
     assert int((p[-1000:] == 0).sum()) == 0
+
+
+@pytest.mark.gpu
+def test_adamw_steps_after_a_refused_one():
+    ps, gs = _tensors(F32, F32, 5)
+    a, b = ([p.to(DEV) for p in ps] for _ in range(2))
+    gs = [g.to(DEV) for g in gs]
+    x, y = moe.AdamW(a, grads=gs, eps=0.0), moe.AdamW(b, grads=gs)
+    with pytest.raises(moe.MoeError, match="SHAPE"):
+        x.step()
+    assert x.steps == 0 and not x._tables
+    x.eps = y.eps
+    for _ in range(2):
+        x.step()
+        y.step()
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
 @pytest.mark.gpu
