@@ -105,6 +105,12 @@ class AdamW:
                                      self.exp_avg_scale[i].data_ptr() if eight else None,
                                      self.exp_avg_sq_scale[i].data_ptr() if eight else None,
                                      None if c is None else c.data_ptr(), p.numel())
+        # (no two may share memory: a tensor given twice would be updated by two blocks at a time)
+        used = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                      for ts in (params, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale,
+                                 self.copies) if ts is not None for t in ts if t is not None and t.numel())
+        if any(a[1] > b[0] for a, b in zip(used, used[1:])):
+            raise ValueError("two of the parameters, moments and copies share memory")
         self._nbytes = int(train_lib().moe_adamw_table_size(len(params)))
         if self._nbytes == 0:
             raise ValueError(f"{len(params)} parameters: too many")

@@ -359,6 +359,16 @@ def test_adamw_steps_after_a_refused_one():
 
 
 @pytest.mark.gpu
+def test_adamw_refuses_shared_memory():
+    flat = torch.zeros(64, device=DEV)
+    for ps, kw in (([flat, flat], {}), ([flat[:32], flat[16:48]], {}), ([flat], dict(exp_avg=[flat])),
+                   ([flat], dict(exp_avg_sq=[flat]))):
+        with pytest.raises(ValueError, match="share memory"):
+            moe.AdamW(ps, **kw)
+    moe.AdamW([flat[:32], flat[32:], flat[32:32]])
+
+
+@pytest.mark.gpu
 def test_adamw_on_a_stream_with_new_gradients_each_step():
     ps, _ = _tensors(F32, F32, 5)
     a, b = ([torch.nn.Parameter(p.to(DEV)) for p in ps] for _ in range(2))
