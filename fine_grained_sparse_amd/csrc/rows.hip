@@ -282,15 +282,15 @@ __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ y, con
 // The gradients of the weighted sum in one pass over y: G threads take KM of a
 // token's rows (several tokens per wave for short rows, several waves for long
 // ones), hold 16 bytes of dout at a time and go over the rows with it.  dy of a
-// row is written where y of it was read.  Eight rows a time, so that dout is read
+// row is written where y of it was read, which may be the same memory.  Eight rows a time, so that dout is read
 // once or twice; one (a block of 1024) where the tokens are too few to fill the chip:
 // 10.1 -> 5.4 us at 64 tokens of 7168 columns, top-8.  4001 tokens of 3584, top-16: 176 us (sixteen
 // rows a time, which spilled: 256), 5.2 TB/s.
 template <typename T, int KM, bool DY, bool DW>
-__global__ __launch_bounds__(KM == 1 ? 1024 : 256) void k_gather_backward(const uint4* __restrict__ dout, const uint4* __restrict__ y,
+__global__ __launch_bounds__(KM == 1 ? 1024 : 256) void k_gather_backward(const uint4* __restrict__ dout, const uint4* y,
                                                           const float* __restrict__ w, const int32_t* __restrict__ pos,
                                                           int64_t T0, int64_t Tn, uint32_t C, int K, int G, int64_t rows,
-                                                          uint4* __restrict__ dy, float* __restrict__ dw) {
+                                                          uint4* dy, float* __restrict__ dw) {
     constexpr int N = Chunk<T>::N;
     __shared__ float sh[16][KM];
     const int g = threadIdx.x & (G - 1), k0 = blockIdx.y * KM;

@@ -162,7 +162,7 @@ def combine(y, topk_w, order, *, residual=None, out=None, stream=None):
 
 def combine_backward(dout, y, topk_w, order, *, need_dy=True, need_dw=True, out=None, stream=None):
     """moe_combine_backward: (dy, of y's shape, or None; d_topk_w fp32 [T, K]
-    or None) from dout [T, d].  `out`: the tensor for dy."""
+    or None) from dout [T, d].  `out`: the tensor for dy, which may be y itself."""
     pos, T, K, d, dev, D = _rows(y, "y", order)
     _need(dout, "dout", y.dtype, (T, d), dev)
     _need(topk_w, "topk_w", torch.float32, (T, K), dev)
@@ -174,6 +174,8 @@ def combine_backward(dout, y, topk_w, order, *, need_dy=True, need_dw=True, out=
     with ctx:
         dy = None if not need_dy else torch.empty_like(y) if out is None else out
         dw = torch.empty_like(topk_w) if need_dw else None
+        if not need_dw and y.shape[0] == 0:
+            return dy, dw  # (no rows: an empty tensor's address is NULL)
         _call("moe_combine_backward", D, dout.data_ptr(), y.data_ptr(), topk_w.data_ptr(), pos.data_ptr(), y.shape[0],
               _ptr(dy), _ptr(dw), s)
     return dy, dw

@@ -134,7 +134,8 @@ moe_status moe_router_backward(const moe_layer_desc *desc, const void *x,
  * place is behind expert_offsets[E], or outside 0 .. rows - 1, belongs to no
  * assignment: it is neither read nor written.  Offsets that are not ascending
  * within 0 .. rows are not detected; they are taken as if clamped to it, and what
- * comes out is not said.                                                     */
+ * comes out is not said.  Results may not overlap what a call reads, but where it
+ * says so.                                                                   */
 
 /* The order.
  *   topk_idx [T, K] int32; e0: the id of this GPU's first expert; token_mask
@@ -168,8 +169,8 @@ moe_status moe_sort_tokens_backward(const moe_layer_desc *desc, const void *dxs,
  * NULL for 0, or out itself), topk_w [T, K] fp32.  Its gradients from dout [T, d]:
  * dy[pos[t,k]] = topk_w[t,k] dout[t], dy [rows, d]; d_topk_w[t,k] = <dout[t],
  * y[pos[t,k]]>, fp32 [T, K], 0 without a row.  dy or d_topk_w may be NULL (both:
- * MOE_ERR_NULL); y is needed for d_topk_w, topk_w for dy.  (residual's gradient
- * is dout.)                                                                  */
+ * MOE_ERR_NULL); y is needed for d_topk_w, topk_w for dy; dy may be y.
+ * (residual's gradient is dout.)                                             */
 moe_status moe_combine(const moe_layer_desc *desc, const void *y,
                        const float *topk_w, const int32_t *pos,
                        const void *residual, int64_t rows, void *out,

@@ -315,6 +315,46 @@ def test_rows_in_place_and_out_of_range():
         assert torch.equal(moe.combine_backward(xd, yd, wd, p)[1], moe.combine_backward(xd, yd, wd, q)[1])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,K,d", [(9, 4, 64), (50, 4, 2048), (700, 12, 1024), (301, 9, 64)])
+def test_combine_gradient_in_place_of_its_rows(T, K, d, dt):
+    o, pos, x, rows, w = _rows_case(T, 16, K, d, dt, 0.1, T + d, 1.0)
+    n = int(o.offsets[-1])
+    yd, wd, xd = rows.to(DEV), w.to(DEV), x.to(DEV)
+    dy, dw = moe.combine_backward(xd, yd, wd, o)
+    own = yd.clone()
+    got, gw = moe.combine_backward(xd, own, wd, o, out=own)
+    bits = torch.int32 if dt is torch.float32 else torch.int16  # (the rows behind the last one are NaN)
+    assert got is own and torch.equal(own[:n], dy[:n]) and torch.equal(own[n:].view(bits), yd[n:].view(bits))
+    assert torch.equal(gw, dw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 3000])
+def test_order_of_1024_experts_captured(T):
+    """(More shared memory than a launch has unasked.)"""
+    K, E = 8, 1024
+    g = torch.Generator().manual_seed(T)
+    idx = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32).to(DEV)
+    ws, s = moe.Workspace(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    moe.dispatch(idx, E, workspace=ws, stream=s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        o = moe.dispatch(idx, E, sorted_token=True, workspace=ws, stream=s)
+    for seed in range(3):
+        g = torch.Generator().manual_seed(T + 1 + seed)
+        idx.copy_(torch.randint(0, E, (T, K), generator=g, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = moe.dispatch(idx, E, sorted_token=True)
+        assert all(torch.equal(a, b) for a, b in zip(o, want)), seed
+        order = torch.sort(idx.flatten().cpu().long(), stable=True).indices
+        assert torch.equal(o.sorted_token.cpu().long(), order // K)
+
+
 # ------------------------------------------------------------------ the experts
 def _sizes(g, R, E, kind):
     if kind == "one":
@@ -593,6 +633,7 @@ def test_nothing_to_do():
         assert (moe.sort_tokens_backward(none, o) == 0).all()
         dy, dw = moe.combine_backward(x, none, w, o)
         assert dy.shape == (0, 64) and (dw == 0).all()
+        assert moe.combine_backward(x, none, w, o, need_dw=False)[0].shape == (0, 64)
 
 
 @pytest.mark.gpu
