@@ -98,19 +98,18 @@ class AdamW:
             for c, p in zip(self.copies, params):
                 if c is not None:
                     _need(c, "copies", torch.bfloat16, p.shape, dev)
-        self._table = (_Tensor * len(params))()
-        for i, p in enumerate(params):
-            c = None if self.copies is None else self.copies[i]
-            self._table[i] = _Tensor(p.data_ptr(), None, self.exp_avg[i].data_ptr(), self.exp_avg_sq[i].data_ptr(),
-                                     self.exp_avg_scale[i].data_ptr() if eight else None,
-                                     self.exp_avg_sq_scale[i].data_ptr() if eight else None,
-                                     None if c is None else c.data_ptr(), p.numel())
+        sizes = [p.numel() for p in params]
+        ptrs = [[None if t is None else t.data_ptr() for t in ts] if ts is not None else [None] * len(params)
+                for ts in (params, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.copies)]
         # (no two may share memory: a tensor given twice would be updated by two blocks at a time)
-        used = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                      for ts in (params, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale,
-                                 self.copies) if ts is not None for t in ts if t is not None and t.numel())
+        wide = 1 if eight else 4
+        per = (params[0].element_size(), wide, wide, None, None, 2)  # bytes of an element; scales: of 128
+        used = sorted((a, a + (n * b if b else (n + 127) // 128)) for at, b in zip(ptrs, per)
+                      for a, n in zip(at, sizes) if a is not None and n)
         if any(a[1] > b[0] for a, b in zip(used, used[1:])):
             raise ValueError("two of the parameters, moments and copies share memory")
+        p, m, v, ms, vs, c = ptrs
+        self._table = (_Tensor * len(params))(*[_Tensor(*t) for t in zip(p, [None] * len(params), m, v, ms, vs, c, sizes)])
         self._nbytes = int(train_lib().moe_adamw_table_size(len(params)))
         if self._nbytes == 0:
             raise ValueError(f"{len(params)} parameters: too many")
