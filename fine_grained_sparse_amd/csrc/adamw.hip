@@ -8,7 +8,10 @@
 // [128, 256); v, never negative, has 5 exponent bits (bias 15) and 3 fraction
 // bits, the largest in [2^15, 2^16).  v keeps no root: the average is linear in
 // v, and rounded at random it keeps its mean, while rounded to nearest a
-// change of 1 - b2 = 1e-3 would never leave a value of 3 fraction bits.  The random
+// change of 1 - b2 = 1e-3 would never leave a value of 3 fraction bits.  Under the root a
+// code of 0 counts as the smallest one above it, 2^-33 to 2^-32 of the block's largest v:
+// beside a v that was rounded to 0, an m that was rounded up moved its parameter by up to 1390
+// lr (values of 1e-5 to 1e-7 of their block's largest; 1.8 lr now, 1.1 with fp32 moments).  The random
 // bits are a hash of (seed, step, tensor, element): the same step gives the same
 // bits, whatever the launch.  A product or sum of the moments is rounded by itself (no
 // fused multiply-add), so that the codes are those of the formula in fp32.
@@ -236,6 +239,7 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
         get8(p, i, live, pv);
         get8(g, i, live, gv);
         int sm = 0, sv = 0;
+        uint32_t least = 0;  // of v under the root
         if (EIGHT) {
             uint2 cm = make_uint2(0, 0), cv = cm;
             if (live) {
@@ -250,6 +254,7 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
                 m[k] = value_m(wm[k >> 2] << (24 - 8 * (k & 3)), sm);
                 v[k] = value_v(wv[k >> 2] << (24 - 8 * (k & 3)), sv);
             }
+            least = __float_as_uint(ldexpf(S.b2, sv + kShiftV - 129));  // b2 times code 1
             if (__any(sm == 255 || sv == 255)) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -266,7 +271,9 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
             const float gk = gv[k] * gs;
             m[k] = average(m[k], S.b1, gk * S.n1);
             v[k] = average(v[k], S.b2, product(gk * S.n2, gk));
-            pv[k] = pv[k] * keep - rate * m[k] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[k]) * root + S.eps);
+            // (as whole numbers, one instruction: neither is negative, and NaN stays)
+            const float u = EIGHT ? __uint_as_float(max(__float_as_uint(v[k]), least)) : v[k];
+            pv[k] = pv[k] * keep - rate * m[k] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(u) * root + S.eps);
         }
         constexpr bool kHash = EIGHT || sizeof(TP) == 2;
         uint32_t word[8];

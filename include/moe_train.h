@@ -223,8 +223,10 @@ moe_status moe_experts_backward(const moe_layer_desc *desc, int64_t rows,
  * bias 7, 3 fraction bits), v an unsigned code of 5 exponent bits with bias
  * 15 and 3 fraction bits; the value is code x scale.  A new moment x, computed in
  * fp32, is rounded to one of its two neighbours at random, up with the
- * probability that keeps the mean; so is a bf16 parameter.  The random bits are
- * of (seed, step, the tensor's number in `tensors`, the element i): with
+ * probability that keeps the mean; so is a bf16 parameter.  Under the root, v is
+ * at least b2 times the value of code 1 in the block that it was read from (an m that
+ * was rounded up would else move its parameter by any amount beside a v that was
+ * rounded to 0).  The random bits are of (seed, step, the tensor's number in `tensors`, the element i): with
  *   mix(h): h = (h ^ (h >> 16)) 0x85ebca6b, h = (h ^ (h >> 13)) 0xc2b2ae35,
  *           h ^ (h >> 16)          [A. Appleby's 32-bit mixer, public domain]
  * and all sums and products modulo 2^32,

@@ -396,3 +396,71 @@ def test_adamw_on_a_stream_with_new_gradients_each_step():
         x.step([torch.zeros(p.numel() + 1, device=DEV)[1:] for p in ps])
     with pytest.raises(ValueError, match="values"):
         moe.AdamW(a, state_bits=8, exp_avg_scale=[torch.zeros(1, dtype=torch.uint8, device=DEV)] * len(a))
+
+
+# ------------------------------------------------- second moments near zero
+def _steps(g, ratios, n):
+    """n gradients of blocks of 128 values whose first one is an outlier of 1, the others a block's ratio of it."""
+    scale = torch.tensor(ratios).repeat_interleave(128).view(-1, 128).clone()
+    scale[:, 0] = 1.0
+    for _ in range(n):
+        yield (torch.randn(scale.shape, generator=g) * scale).flatten()
+
+
+@pytest.mark.gpu
+def test_a_second_moment_of_code_zero_counts_as_the_smallest_code():
+    """Under the root, in the block that it was read from: the update against float64, the stored moments as without it."""
+    b1, b2, lr, eps, t = 0.9, 0.999, 2.0 ** -6, 1e-12, 41
+    S, M = torch.tensor([90, 120, 0, 255]), 118          # blocks' scales of v; of m
+    c = torch.arange(128) % 8                               # codes of v: 0 .. 7
+    g = torch.where(torch.arange(128) < 64, 0.0, 2.0 ** -21)
+    p = torch.zeros(512, device=DEV)
+    byte = lambda v: v.to(torch.uint8).to(DEV)  # noqa: E731
+    opt = moe.AdamW([p], state_bits=8, lr=lr, betas=(b1, b2), eps=eps, weight_decay=0.0, step=t - 1,
+                    exp_avg=[byte(torch.arange(128).repeat(4) // 8 % 2)], exp_avg_scale=[byte(torch.full((4,), M))],
+                    exp_avg_sq=[byte(c.repeat(4))], exp_avg_sq_scale=[byte(S)])
+    m, v = (x[0].cpu().double() for x in opt.moments())
+    g4 = g.double().repeat(4)
+    assert m.max() == 2.0 ** (M - 127 - 9) and int((v == 0).sum()) == 48
+    opt.step([g.repeat(4).to(DEV)])
+    m, v = b1 * m + (1 - b1) * g4, b2 * v + (1 - b2) * g4 ** 2
+    least = b2 * 2.0 ** (S.double() - 127 - 17).repeat_interleave(128)
+    want = -lr / (1 - b1 ** t) * m / (torch.sqrt(torch.maximum(v, least) / (1 - b2 ** t)) + eps)
+    q = p.cpu().double()
+    assert (q[:384] - want[:384]).abs().le(16 * E32 * want[:384].abs()).all() and q[384:].isnan().all()
+    # a block of fresh moments (scale 0) and no gradient: nothing moves that has no m
+    assert int((q[:384] == 0).sum()) == 3 * 32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("outlier", [1.0, 1e-2])
+def test_eight_bit_updates_beside_an_outlier(outlier):
+    """Updates with 8-bit moments against those with fp32 ones, of values far below their block's largest.
+
+    A step of m's smallest codes is at most 2^-16 of the block's largest m, and the root of v, which
+    is no less than its smallest code, at least 2^-16.5 of the block's largest root.  A random code of m
+    therefore weighs at most sqrt(2) times the block's largest update; two of them are allowed for.  Their
+    variance: a step's at most 1/4 code^2, summed over b1^2 at most 1.3 code^2, sqrt(1.3 * 2) = 1.6 times
+    the largest value's m / sqrt(v), whose mean square is the fp32 update's; with that itself 1.9 of it."""
+    ratios = [r for r in (1e-3, 1e-4, 1e-5, 1e-6, 1e-7) for _ in range(16)]
+    n, steps, lr = 128 * len(ratios), 300, 2.0 ** -10
+    p, q = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    a = moe.AdamW([p], state_bits=8, lr=lr, weight_decay=0.0, seed=5)
+    b = moe.AdamW([q], state_bits=32, lr=lr, weight_decay=0.0)
+    most = torch.zeros((2, n), device=DEV)
+    square = torch.zeros((2, n), dtype=torch.float64, device=DEV)
+    for g in _steps(torch.Generator().manual_seed(11), ratios, steps):
+        g = (g * outlier).to(DEV)
+        for i, (opt, x) in enumerate(((a, p), (b, q))):
+            x.zero_()                    # (the update itself, not a difference of parameters)
+            opt.step([g])
+            u = x / lr
+            most[i] = torch.maximum(most[i], u.abs())
+            square[i] += u.double() ** 2
+    most, rms = most.cpu().view(2, -1, 128), torch.sqrt(square.cpu() / steps).view(2, -1, 128)
+    for r in sorted(set(ratios)):
+        at = torch.tensor([x == r for x in ratios])
+        big, mean = most[:, at, 1:].amax((1, 2)), torch.sqrt((rms[:, at, 1:] ** 2).mean((1, 2)))
+        print(f"  ratio {r:g}: largest update {big[0]:.2f} lr ({big[1]:.2f} with fp32 moments), rms {mean[0]:.3f} ({mean[1]:.3f})", flush=True)
+        assert big[0] <= 2 * 2 ** 0.5 * most[1].max(), r
+        assert mean[0] <= 2 * torch.sqrt((rms[1] ** 2).mean()), r
