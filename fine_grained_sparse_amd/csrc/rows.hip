@@ -383,9 +383,10 @@ hipError_t launch_order(const int32_t* idx, int T, int E, int e0, int K, const u
     while ((E >> bits) != 0) ++bits;  // ids 0 .. E
     const int nb = order_blocks(A);
     const size_t lds = static_cast<size_t>(kOrderWaves) * (E + 1) * 4;
+    const bool ask = lds + kOrderWaves * 4 > 64 * 1024;  // (with k_order's own array, more than a launch has unasked)
     if (nb == 1) {
         const int64_t per = (A + 1023) / 1024 * 1024;
-        if (lds > 64 * 1024) {
+        if (ask) {
             const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_order<true>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
             if (err != hipSuccess) return err;
@@ -394,7 +395,7 @@ hipError_t launch_order(const int32_t* idx, int T, int E, int e0, int K, const u
                            part, counts, offsets, sorted_token, pos);
         return hipGetLastError();
     }
-    if (lds > 64 * 1024) {
+    if (ask) {
         const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_order<false>),
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (err != hipSuccess) return err;

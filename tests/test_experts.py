@@ -355,6 +355,24 @@ def test_order_of_1024_experts_captured(T):
         assert torch.equal(o.sorted_token.cpu().long(), order // K)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 3000])
+@pytest.mark.parametrize("E", [1022, 1023, 1024])
+def test_order_at_the_limit_of_a_launch_s_shared_memory(T, E):
+    """1023 experts: the running counts alone are 64 KiB, with the kernel's own array they are more."""
+    idx = torch.randint(0, E, (T, 8), generator=torch.Generator().manual_seed(T + E), dtype=torch.int32)
+    o = moe.dispatch(idx.to(DEV), E, sorted_token=True)
+    flat = idx.flatten().long()
+    order = torch.sort(flat, stable=True).indices
+    counts = torch.bincount(flat, minlength=E)
+    assert torch.equal(o.counts.cpu().long(), counts)
+    assert torch.equal(o.offsets.cpu().long(), torch.cat((torch.zeros(1, dtype=torch.int64), counts.cumsum(0))))
+    assert torch.equal(o.sorted_token.cpu().long(), order // 8)
+    pos = torch.empty_like(order)
+    pos[order] = torch.arange(len(order))
+    assert torch.equal(o.pos.cpu().long().flatten(), pos)
+
+
 # ------------------------------------------------------------------ the experts
 def _sizes(g, R, E, kind):
     if kind == "one":
