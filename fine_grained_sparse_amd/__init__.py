@@ -103,8 +103,15 @@ def lib():
     return _lib
 
 
+def _int32(name, *values):
+    """Refuses whole numbers that the ABI's 32 bits do not hold (ctypes would drop their high bits)."""
+    if max(values) > 0x7fffffff or min(values) < -0x80000000:
+        raise ValueError(f"{name}: {max(values, key=abs)} does not fit 32 bits")
+
+
 def desc(*, T, d, E, K, F=0, n_shared=0, F_shared=0, d_latent=0, scale=2.827,
          act_dtype=MOE_BF16, w_dtype=None, w_layout=MOE_LAYOUT_ROWS, n_group=1, topk_group=1):
+    _int32("sizes of the layer", T, d, E, K, F, n_shared, F_shared, d_latent, n_group, topk_group)
     return LayerDesc(T, d, E, K, F, n_shared, F_shared, d_latent, scale, act_dtype,
                      act_dtype if w_dtype is None else w_dtype, w_layout, n_group, topk_group)
 
@@ -446,6 +453,7 @@ def forward(x, W_r, b, weights, K, scale=2.827, *, n_shared=None, out=None,
 
 
 def slice_workspace_size(layer_desc: LayerDesc, e0: int, E_total: int) -> int:
+    _int32("e0, E_total", e0, E_total)
     return int(lib().moe_slice_workspace_size(ctypes.byref(layer_desc), e0, E_total))
 
 

@@ -26,7 +26,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import ExpertWeights, MoeError, _DT, _default_ws, _need, _ptr, desc
+from . import ExpertWeights, MoeError, _DT, _default_ws, _int32, _need, _ptr, desc
 from .train import _call, _launch, train_lib
 
 
@@ -47,7 +47,8 @@ class Saved(NamedTuple):
 
 
 @functools.lru_cache(maxsize=256)
-def _order_plan(T, E, K):
+def _order_plan(T, E, K, e0):
+    _int32("e0", e0)
     D = ctypes.byref(desc(T=T, d=64, E=E, K=K))
     nbytes = int(train_lib().moe_dispatch_workspace_size(D))
     if nbytes == 0:
@@ -82,7 +83,7 @@ def dispatch(topk_idx, E, *, e0=0, token_mask=None, sorted_token=False, workspac
         if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
         _need(token_mask, "token_mask", torch.uint8, (T,), dev)
-    D, nbytes = _order_plan(T, int(E), K)
+    D, nbytes = _order_plan(T, int(E), K, int(e0))
     s, ctx = _launch(dev, stream)
     with ctx:
         counts = topk_idx.new_empty((E,))

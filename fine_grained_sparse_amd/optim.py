@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import _DT, _need
+from . import _DT, _int32, _need
 from .train import _call, _launch, train_lib
 
 
@@ -66,6 +66,7 @@ class AdamW:
         self.params, self.device, self.state_bits = params, dev, state_bits
         self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, betas, eps, weight_decay, seed
         self.steps = int(step)
+        _int32("step", self.steps + 1)
         self._param_dtype = _DT[_typed(params, "params", dev)]
         eight = state_bits == 8
         sdt = torch.uint8 if eight else torch.float32

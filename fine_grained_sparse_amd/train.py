@@ -25,7 +25,8 @@ import os
 
 import torch
 
-from . import HERE, ExpertWeights, LayerDesc, MoeError, _current_raw_stream, _DT, _Nothing, _default_ws, _need, _ptr, desc
+from . import (HERE, ExpertWeights, LayerDesc, MoeError, _current_raw_stream, _DT, _int32, _Nothing, _default_ws, _need,
+               _ptr, desc)
 from . import lib as _moe_lib
 
 TRAIN_LIB_PATH = os.path.join(HERE, "libmoe_train.so")
@@ -155,6 +156,7 @@ def _balance(T, dev, alpha, seq_offsets, token_mask):
         S = seq_offsets.numel() - 1
         if seq_offsets.dim() != 1 or S < 1:
             raise ValueError("seq_offsets must be [S + 1], S >= 1")
+        _int32("sequences", S)
     if token_mask is not None:
         if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)

@@ -18,7 +18,7 @@ import pytest
 import torch
 
 import fine_grained_sparse_amd as moe
-from fine_grained_sparse_amd import train
+from fine_grained_sparse_amd import experts, optim, train
 from test_abi import ALIGN, FAKE, FAKE_ODD, NULL, OK, SHAPE, UNSUP, WS, _k2
 
 E32, U = 2.0 ** -24, 2.0 ** -8
@@ -140,6 +140,38 @@ def test_python_calls_refuse_cpu_tensors():
               lambda: moe.experts_backward(b16, b16, order.offsets, W, moe.Saved(b16, b16))):
         with pytest.raises(ValueError, match="GPU"):
             f()
+
+
+@pytest.mark.parametrize("past", [2 ** 31, 2 ** 32 + 8, -2 ** 31 - 1])
+def test_sizes_past_32_bits_are_refused(past, monkeypatch):
+    """The ABI's fields have 32 bits: 2^32 + 8 experts would be taken as 8 (shapes alone: meta tensors)."""
+    sizes = dict(T=1, d=64, E=8, K=1, F=64, n_shared=0, F_shared=0, d_latent=0, n_group=1, topk_group=1)
+    for n in sizes:
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.desc(**{**sizes, n: past})
+    assert moe.desc(**{**sizes, "T": 2 ** 31 - 1}).T == 2 ** 31 - 1 and moe.desc(**{**sizes, "T": -1}).T == -1
+    for mod in (moe, experts, optim, train):
+        monkeypatch.setattr(mod, "_need", lambda *a, **kw: None)
+    idx = torch.zeros((4, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.dispatch(idx, past)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.dispatch(idx, 8, e0=past)
+    for e0, E_total in ((past, 384), (0, past)):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.slice_workspace_size(moe.desc(**sizes), e0, E_total)
+    if past < 0:
+        return
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.AdamW([torch.zeros(4)], step=past)
+    meta = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    order = moe.Order(None, meta(9), None, meta(4, 1))
+    wide = meta(4, past, dtype=torch.bfloat16)
+    for call in (lambda: moe.dispatch(meta(past, 1), 8), lambda: moe.sort_tokens(wide, order),
+                 lambda: moe.sort_tokens_backward(wide, order), lambda: moe.combine(wide, meta(4, 1, dtype=torch.float32), order),
+                 lambda: moe.balance_loss(meta(4, 8, dtype=torch.float32), meta(4, 1), 0.1, seq_offsets=meta(past + 1))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
 
 
 # ------------------------------------------------------------------- the order
