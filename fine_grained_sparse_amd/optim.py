@@ -53,6 +53,8 @@ class AdamW:
     them, and keeps it alive: a parameter that is moved (p.data = ...) needs a new
     object, a gradient buffer that is moved is handed over again."""
 
+    _others = False  # the table holds gradients that were given to a step, not the constructor's
+
     def __init__(self, params, *, grads=None, state_bits=32, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, seed=0, exp_avg=None, exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None,
                  step=0):
@@ -127,7 +129,8 @@ class AdamW:
         for i, (g, p) in enumerate(zip(grads, self.params)):
             if g.shape != p.shape:
                 raise ValueError(f"grads[{i}] has shape {tuple(g.shape)}, expected {tuple(p.shape)}")
-            self._table[i].grad = g.data_ptr()
+        for entry, g in zip(self._table, grads):  # (not before all are looked at: those of a refused call are not taken)
+            entry.grad = g.data_ptr()
         self._grad_dtype = _DT[dt]
         self._tables.clear()
         return grads
@@ -139,10 +142,13 @@ class AdamW:
         replayed (the object's own count is then left alone); grad_scale, fp32
         [1], multiplies the gradients."""
         if grads is not None:
-            self.grads = None
             self._take(grads)
+            self._others = True
         elif self.grads is None:
             raise ValueError("no gradients")
+        elif self._others:
+            self._take(self.grads)
+            self._others = False
         D = _Desc(self._param_dtype, self._grad_dtype, self.state_bits, self.steps + 1, int(self.seed) & 0xffffffff, 0.0,
                   float(self.eps), float(self.weight_decay), float(self.betas[0]), float(self.betas[1]))
         lr = self.lr if lr is None else lr

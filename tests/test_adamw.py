@@ -109,6 +109,32 @@ def test_a_refused_step_keeps_no_table(monkeypatch):
     assert kept == [0, 0, 1] and opt.steps == 2
 
 
+def test_the_constructor_s_gradients_stay_the_default(monkeypatch):
+    """Through steps with others, and through refused ones (on the CPU: the addresses that each call is given)."""
+    calls = []
+
+    def call(name, D, table, n, *args):
+        calls.append((D._obj.grad_dtype, D._obj.keep_table, [table[i].grad for i in range(n)]))
+    for name, fn in (("_need", lambda *a, **kw: None), ("_call", call), ("_launch", lambda dev, stream: (0, train._NOTHING))):
+        monkeypatch.setattr(optim, name, fn)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ps = [torch.zeros(n) for n in (5, 9)]
+    own, others = ([torch.zeros(n, dtype=dt) for n in (5, 9)] for dt in (F32, B16))
+    at = lambda gs: [g.data_ptr() for g in gs]  # noqa: E731
+    opt = moe.AdamW(ps, grads=own)
+    opt.step()
+    opt.step(others)
+    opt.step()
+    opt.step()
+    assert calls == [(0, 0, at(own)), (1, 0, at(others)), (0, 0, at(own)), (0, 1, at(own))]
+    with pytest.raises(ValueError, match="shape"):
+        opt.step([others[0], torch.zeros(8, dtype=B16)])
+    with pytest.raises(ValueError, match="gradients"):
+        opt.step(others[:1])
+    opt.step()
+    assert calls[4:] == [(0, 1, at(own))] and opt.steps == 5
+
+
 # ------------------------------------------------------------------- plain form
 def _mix(h):
     h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
