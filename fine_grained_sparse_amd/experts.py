@@ -13,6 +13,7 @@ gradient.
     dxs, grads = experts_backward(dy, xs, order.offsets, weights, saved)
     dx_r, dW_r = router_backward(x, W_r, z, idx, dw, ...)
     dx = sort_tokens_backward(dxs, order, residual=dx_r)
+    ... AdamW of the experts and of W_r ...
 
 Results carry no autograd graph, whatever their inputs do.  An order may be for a
 part of the experts (e0, and E of them, of an expert-parallel layer): the

@@ -1,12 +1,16 @@
 """AdamW over many tensors at once: Python binding of moe_adamw
 (include/moe_train.h: formula, 8-bit moments and their rounding there).
 
-    opt = AdamW([W_r, *experts], state_bits=8, lr=1e-4)
-    opt.step([dW_r, *grads])
+    names = ("W_gate", "W_up", "W_down")
+    experts = AdamW([weights[n] for n in names], state_bits=8, lr=1e-2)
+    router = AdamW([W_r], lr=1e-3)
+    experts.step([grads[n] for n in names])
+    router.step([dW_r])
 
-The object holds what a program keeps over the steps (parameters, moments, the
-number of steps) and the table of their addresses; a step only enqueues
-kernels on the launch stream.
+An object is for parameters of one type whose gradients have one type: the
+layer's bf16 experts and its fp32 router take one each.  It holds what a program
+keeps over the steps (parameters, moments, the number of steps) and the table of
+their addresses; a step only enqueues kernels on the launch stream.
 """
 import ctypes
 
@@ -39,7 +43,8 @@ def _typed(tensors, name, dev=None):
 
 
 class AdamW:
-    """moe_adamw over `params`: tensors of one device, all fp32 or all bf16.
+    """moe_adamw over `params`: tensors of one device, all fp32 or all bf16; their
+    gradients likewise, of the same type or the other.
 
     state_bits   32: fp32 moments; 8: codes of 8 bits with a scale per 128 values.
     copies       bf16 tensors that receive the updated fp32 parameters (one per

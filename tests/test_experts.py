@@ -611,6 +611,43 @@ def test_training_step_of_the_layer_against_autograd(T, d, E, K, F):
         assert err <= 7 * U, n
 
 
+def _moments(opt, i, p):
+    return [x[i].double().view_as(p) for x in opt.moments()]
+
+
+@pytest.mark.gpu
+def test_training_steps_of_the_layer_with_adamw():
+    """The optimizer as its module shows it, over three steps of the layer; each against float64 from the gradients and
+    moments before it.  fp32: 16 E32 of the change's terms and 3 E32 of the parameter; bf16, rounded at random: one of the two
+    neighbours, less than a step of at most 2^-7 of the value, besides."""
+    T, d, E, K, F = 300, 256, 10, 4, 128
+    x, W_r, b, weights, dout, shared = _layer(T, d, E, K, F, 4)
+    code = [line[4:] for line in optim.__doc__.splitlines() if line.startswith("    ")]
+    made = next(i for i, line in enumerate(code) if ".step(" in line)
+    names = dict(AdamW=moe.AdamW, W_r=W_r, weights=weights)
+    exec("\n".join(code[:made]), names)
+    for t in range(1, 4):
+        got = _step(x, W_r, b, weights, K, dout, shared, None)
+        each = [(names["experts"], i, weights[n], got[n]) for i, n in enumerate(("W_gate", "W_up", "W_down"))]
+        each.append((names["router"], 0, W_r, got["dW_r"]))
+        before = [(p.double(), *_moments(opt, i, p)) for opt, i, p, _ in each]
+        least = [opt.betas[1] * 2.0 ** (opt.exp_avg_sq_scale[i].double() - 144) if opt.state_bits == 8 else None
+                 for opt, i, _, _ in each]
+        exec("\n".join(code[made:]), dict(names, grads=got, dW_r=got["dW_r"]))
+        for (opt, _, p, g), (q, m, v), lo in zip(each, before, least):
+            (b1, b2), g = opt.betas, g.double()
+            v = b2 * v + (1 - b2) * g * g
+            if lo is not None:  # (a code of 0 counts as the smallest one under the root)
+                v = torch.maximum(v, lo.repeat_interleave(128)[:v.numel()].view_as(v))
+            rate = opt.lr / (1 - b1 ** t) / (torch.sqrt(v / (1 - b2 ** t)) + opt.eps)
+            want = q * (1 - opt.lr * opt.weight_decay) - rate * (b1 * m + (1 - b1) * g)
+            tol = (3 * q.abs() + 16 * rate * (b1 * m.abs() + (1 - b1) * g.abs())) * E32
+            if p.dtype == torch.bfloat16:
+                tol += 2.0 ** -7 * (want.abs() + tol)
+            assert ((p.double() - want).abs() <= tol).all() and opt.steps == t
+            assert (p.double() != q).double().mean() > 0.5
+
+
 @pytest.mark.gpu
 def test_training_step_captured_on_a_stream():
     """Captured once and replayed with new inputs and routing, eager work in between; every replay has the eager bits."""
