@@ -490,3 +490,64 @@ def test_eight_bit_updates_beside_an_outlier(outlier):
         print(f"  ratio {r:g}: largest update {big[0]:.2f} lr ({big[1]:.2f} with fp32 moments), rms {mean[0]:.3f} ({mean[1]:.3f})", flush=True)
         assert big[0] <= 2 * 2 ** 0.5 * most[1].max(), r
         assert mean[0] <= 2 * torch.sqrt((rms[1] ** 2).mean()), r
+
+
+# ------------------------------------------------------ bf16 at random, bit by bit
+def _bf16_between(want, tol, word):
+    """The stored bits (sign apart) of values within tol of `want` (float64) under these random words, the least and the most."""
+    w = want.abs()
+    r = _mix(word ^ 0x9E3779B9) & 0xFFFF
+    bits = lambda v: (v.float().view(torch.int32).long() + r) >> 16  # noqa: E731
+    return bits((w - tol).clamp(min=0.0)), bits(w + tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits,gdt", [(8, F32), (8, B16), (32, F32)])
+def test_bf16_parameters_rounded_by_the_stated_bits(bits, gdt):
+    """Each value has the bits that the formula and its random word give; where the fp32 tolerance spans the border, one of both."""
+    ps, _ = _tensors(B16, gdt, 7)
+    dev = [p.to(DEV) for p in ps]
+    b1, b2, lr, eps, wd, seed = 0.9, 0.999, 1e-3, 1e-8, 0.01, 12345
+    opt = moe.AdamW(dev, state_bits=bits, lr=lr, betas=(b1, b2), eps=eps, weight_decay=wd, seed=seed)
+    sure = total = 0
+    for t in range(1, 4):
+        _, gs = _tensors(B16, gdt, 80 + t)
+        old = [[x.cpu().double() for x in ms] for ms in opt.moments()]
+        scales = opt.exp_avg_sq_scale and [s.cpu().double() for s in opt.exp_avg_sq_scale]
+        before = [p.cpu().double() for p in dev]
+        opt.step([g.to(DEV) for g in gs])
+        for i, n in enumerate(SIZES):
+            g = gs[i].double()
+            v = b2 * old[1][i] + (1 - b2) * g * g
+            if bits == 8:
+                v = torch.maximum(v, (b2 * 2.0 ** (scales[i] - 144)).repeat_interleave(128)[:n])
+            rate = lr / (1 - b1 ** t) / (torch.sqrt(v / (1 - b2 ** t)) + eps)
+            want = before[i] * (1 - lr * wd) - rate * (b1 * old[0][i] + (1 - b1) * g)
+            tol = (3 * before[i].abs() + 16 * rate * (b1 * old[0][i].abs() + (1 - b1) * g.abs())) * E32
+            lo, hi = _bf16_between(want, tol, _word(n, seed, t, i))
+            at = dev[i].cpu().view(torch.int16).long()
+            big = want.abs() > tol           # (else the sign is open)
+            assert ((at & 0x7FFF) >= lo).all() and ((at & 0x7FFF) <= hi).all(), (t, i)
+            assert (((at >> 15) & 1) == torch.signbit(want).long())[big].all(), (t, i)
+            sure, total = sure + int((lo == hi).sum()), total + n
+    # the tolerance is some 2^-21 of the value (lr is 2% of the parameters), a step of bf16 2^-7 to 2^-8 of it; small ones more
+    assert sure >= 0.99 * total
+
+
+@pytest.mark.gpu
+def test_bf16_parameters_past_32_bit_elements():
+    """The random bits of elements past 2^32, which take the high half of the index, show in parameters half-way between two
+    bf16 numbers."""
+    n = (1 << 32) + 1000
+    p, g = torch.full((n,), 1.5, dtype=B16, device=DEV), torch.full((n,), 0.37, dtype=B16, device=DEV)
+    opt = moe.AdamW([p], state_bits=8, seed=21, lr=2.0 ** -8, weight_decay=0.0)  # 1.5 - 2^-8: steps of bf16 are 2^-7
+    opt.step([g])
+    for first in (0, (1 << 32) - 256, 1 << 32, n - 256):
+        i = torch.arange(first, first + 256)
+        key = _mix((_mix((_mix(torch.tensor(21)) + 1) & 0xFFFFFFFF)) & 0xFFFFFFFF)
+        w = _mix((i % (1 << 32) + key + (i >> 32) * 0x9E3779B9) & 0xFFFFFFFF)
+        want = torch.full((256,), 1.5 - 2.0 ** -8 * 0.37 / (0.37 + 1e-8), dtype=torch.float64)
+        lo, hi = _bf16_between(want, 3 * 1.5 * E32 + 16 * 2.0 ** -8 * E32, w)
+        at = p[first:first + 256].cpu().view(torch.int16).long()
+        assert (at >= lo).all() and (at <= hi).all(), first
+        assert int((lo == hi).sum()) >= 250 and 64 < int((at == at.max()).sum()) < 192, first

@@ -532,6 +532,20 @@ def test_experts_keep_infinities_and_nan_to_their_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,E,d,F", [(96, 32, 512, 256), (3000, 12, 1024, 512), (9000, 6, 2048, 1024)])
+def test_experts_give_the_same_bits_again(R, E, d, F):
+    """Few tiles and blocks that stay for several, products in one launch and in their own: results do not depend on timing."""
+    sizes, off, W, xs, dy = _experts_case(R, E, d, F, "uneven", 8)
+    first = None
+    for _ in range(6):
+        y, saved = moe.experts_forward(xs, off, W)
+        dxs, grads = moe.experts_backward(dy, xs, off, W, saved)
+        got = [y, dxs, *saved, *grads.values()]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.gpu
 def test_experts_gradients_match_differences():
     """<gradient, direction> against central differences of the float64 forward."""
     R, E, d, F = 90, 3, 128, 64
