@@ -11,10 +11,12 @@
 // change of 1 - b2 = 1e-3 would never leave a value of 3 fraction bits.  Under the root a
 // code of 0 counts as the smallest one above it, 2^-33 to 2^-32 of the block's largest v:
 // beside a v that was rounded to 0, an m that was rounded up moved its parameter by up to 1390
-// lr (values of 1e-5 to 1e-7 of their block's largest; 1.8 lr now, 1.1 with fp32 moments).  The random
-// bits are a hash of (seed, step, tensor, element): the same step gives the same
-// bits, whatever the launch.  A product or sum of the moments is rounded by itself (no
-// fused multiply-add), so that the codes are those of the formula in fp32.
+// lr (values of 1e-5 to 1e-7 of their block's largest; 1.9 lr now, 1.1 with fp32 moments).  Not beside
+// an m too large for so small a v: a state that was given so, and is no average of
+// gradients, is taken as it is.  The random bits are a hash of (seed, step, tensor,
+// element): the same step gives the same bits, whatever the launch.  A product or sum of
+// the moments is rounded by itself (no fused multiply-add), so that the codes are those of
+// the formula in fp32.
 // bf16 parameters are rounded at random too: lr of a step is mostly below half
 // a step of bf16.
 #include <cmath>
@@ -203,6 +205,11 @@ __device__ __forceinline__ float product(float x, float y) {
     return x * y;
 }
 
+// An m over this many times the root of v's smallest code does not belong to a v below it: of averages of the
+// same gradients it is at most (1 - b1) / sqrt((1 - b2) (1 - b1^2 / b2)) times the root of v (7.3 with 0.9 and
+// 0.999), and a code that rounding adds to it is 10 such roots at most.
+constexpr float kMostM = 64.f;
+
 template <typename TP, typename TG, bool EIGHT>
 __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restrict__ table,
                                                const uint32_t* __restrict__ first, int tensors, const Step S) {
@@ -239,7 +246,7 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
         get8(p, i, live, pv);
         get8(g, i, live, gv);
         int sm = 0, sv = 0;
-        uint32_t least = 0;  // of v under the root
+        float least = 0.f;
         if (EIGHT) {
             uint2 cm = make_uint2(0, 0), cv = cm;
             if (live) {
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
                 m[k] = value_m(wm[k >> 2] << (24 - 8 * (k & 3)), sm);
                 v[k] = value_v(wv[k >> 2] << (24 - 8 * (k & 3)), sv);
             }
-            least = __float_as_uint(ldexpf(S.b2, sv + kShiftV - 129));  // b2 times code 1
+            least = ldexpf(S.b2, sv + kShiftV - 129);  // b2 times code 1
             if (__any(sm == 255 || sv == 255)) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -266,14 +273,25 @@ __global__ __launch_bounds__(256) void k_adamw(const moe_adamw_tensor* __restric
             get8(static_cast<const float*>(avg), i, live, m);
             get8(static_cast<const float*>(sq), i, live, v);
         }
+        uint32_t low = ~0u;  // (bits of floats that are not negative; NaN's are the largest)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float gk = gv[k] * gs;
             m[k] = average(m[k], S.b1, gk * S.n1);
             v[k] = average(v[k], S.b2, product(gk * S.n2, gk));
-            // (as whole numbers, one instruction: neither is negative, and NaN stays)
-            const float u = EIGHT ? __uint_as_float(max(__float_as_uint(v[k]), least)) : v[k];
-            pv[k] = pv[k] * keep - rate * m[k] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(u) * root + S.eps);
+            low = min(low, __float_as_uint(v[k]));
+        }
+        auto update = [&](int k, float x) {
+            pv[k] = pv[k] * keep - rate * m[k] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(x) * root + S.eps);
+        };
+        // (a branch, rarely taken: 600 M bf16 parameters 1309 -> 1330 us; with the choice in every update 1281 -> 1321)
+        if (EIGHT && __any(low < __float_as_uint(least))) {
+            const float most = kMostM * __builtin_amdgcn_sqrtf(least);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) update(k, v[k] < least && fabsf(m[k]) <= most ? least : v[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) update(k, v[k]);
         }
         constexpr bool kHash = EIGHT || sizeof(TP) == 2;
         uint32_t word[8];

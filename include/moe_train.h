@@ -226,7 +226,9 @@ moe_status moe_experts_backward(const moe_layer_desc *desc, int64_t rows,
  * probability that keeps the mean; so is a bf16 parameter.  Under the root, v is
  * at least b2 times the value of code 1 in the block that it was read from (an m that
  * was rounded up would else move its parameter by any amount beside a v that was
- * rounded to 0).  The random bits are of (seed, step, the tensor's number in `tensors`, the element i): with
+ * rounded to 0), unless |m| is over 64 times the root of that: moments that are no
+ * averages of the same gradients are taken as they are.  The random bits are of
+ * (seed, step, the tensor's number in `tensors`, the element i): with
  *   mix(h): h = (h ^ (h >> 16)) 0x85ebca6b, h = (h ^ (h >> 13)) 0xc2b2ae35,
  *           h ^ (h >> 16)          [A. Appleby's 32-bit mixer, public domain]
  * and all sums and products modulo 2^32,

@@ -425,17 +425,17 @@ def test_adamw_on_a_stream_with_new_gradients_each_step():
 
 
 # ------------------------------------------------- second moments near zero
-def _steps(g, ratios, n):
-    """n gradients of blocks of 128 values whose first one is an outlier of 1, the others a block's ratio of it."""
+def _steps(g, ratios, n, every):
+    """n gradients of blocks of 128 values whose first one is an outlier of 1 in every `every`-th, the others a block's ratio of it."""
     scale = torch.tensor(ratios).repeat_interleave(128).view(-1, 128).clone()
-    scale[:, 0] = 1.0
-    for _ in range(n):
+    for t in range(n):
+        scale[:, 0] = 1.0 if t % every == 0 else torch.tensor(ratios)
         yield (torch.randn(scale.shape, generator=g) * scale).flatten()
 
 
 @pytest.mark.gpu
 def test_a_second_moment_of_code_zero_counts_as_the_smallest_code():
-    """Under the root, in the block that it was read from: the update against float64, the stored moments as without it."""
+    """Under the root, in the block that it was read from, unless m is over 64 times its root: the update against float64."""
     b1, b2, lr, eps, t = 0.9, 0.999, 2.0 ** -6, 1e-12, 41
     S, M = torch.tensor([90, 120, 0, 255]), 118          # blocks' scales of v; of m
     c = torch.arange(128) % 8                               # codes of v: 0 .. 7
@@ -451,16 +451,18 @@ def test_a_second_moment_of_code_zero_counts_as_the_smallest_code():
     opt.step([g.repeat(4).to(DEV)])
     m, v = b1 * m + (1 - b1) * g4, b2 * v + (1 - b2) * g4 ** 2
     least = b2 * 2.0 ** (S.double() - 127 - 17).repeat_interleave(128)
-    want = -lr / (1 - b1 ** t) * m / (torch.sqrt(torch.maximum(v, least) / (1 - b2 ** t)) + eps)
+    counts = m.abs() <= 64 * torch.sqrt(least)
+    want = -lr / (1 - b1 ** t) * m / (torch.sqrt(torch.where(counts, torch.maximum(v, least), v) / (1 - b2 ** t)) + eps)
     q = p.cpu().double()
+    assert [int((counts & (v < least))[i:i + 128].sum()) for i in (0, 128)] == [4, 16]
     assert (q[:384] - want[:384]).abs().le(16 * E32 * want[:384].abs()).all() and q[384:].isnan().all()
     # a block of fresh moments (scale 0) and no gradient: nothing moves that has no m
     assert int((q[:384] == 0).sum()) == 3 * 32
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("outlier", [1.0, 1e-2])
-def test_eight_bit_updates_beside_an_outlier(outlier):
+@pytest.mark.parametrize("outlier,every", [(1.0, 1), (1e-2, 1), (1.0, 50)])
+def test_eight_bit_updates_beside_an_outlier(outlier, every):
     """Updates with 8-bit moments against those with fp32 ones, of values far below their block's largest.
 
     A step of m's smallest codes is at most 2^-16 of the block's largest m, and the root of v, which
@@ -475,7 +477,7 @@ def test_eight_bit_updates_beside_an_outlier(outlier):
     b = moe.AdamW([q], state_bits=32, lr=lr, weight_decay=0.0)
     most = torch.zeros((2, n), device=DEV)
     square = torch.zeros((2, n), dtype=torch.float64, device=DEV)
-    for g in _steps(torch.Generator().manual_seed(11), ratios, steps):
+    for g in _steps(torch.Generator().manual_seed(11), ratios, steps, every):
         g = (g * outlier).to(DEV)
         for i, (opt, x) in enumerate(((a, p), (b, q))):
             x.zero_()                    # (the update itself, not a difference of parameters)
@@ -518,11 +520,12 @@ def test_bf16_parameters_rounded_by_the_stated_bits(bits, gdt):
         opt.step([g.to(DEV) for g in gs])
         for i, n in enumerate(SIZES):
             g = gs[i].double()
-            v = b2 * old[1][i] + (1 - b2) * g * g
+            m, v = b1 * old[0][i] + (1 - b1) * g, b2 * old[1][i] + (1 - b2) * g * g
             if bits == 8:
-                v = torch.maximum(v, (b2 * 2.0 ** (scales[i] - 144)).repeat_interleave(128)[:n])
+                least = (b2 * 2.0 ** (scales[i] - 144)).repeat_interleave(128)[:n]
+                v = torch.where(m.abs() <= 64 * torch.sqrt(least), torch.maximum(v, least), v)
             rate = lr / (1 - b1 ** t) / (torch.sqrt(v / (1 - b2 ** t)) + eps)
-            want = before[i] * (1 - lr * wd) - rate * (b1 * old[0][i] + (1 - b1) * g)
+            want = before[i] * (1 - lr * wd) - rate * m
             tol = (3 * before[i].abs() + 16 * rate * (b1 * old[0][i].abs() + (1 - b1) * g.abs())) * E32
             lo, hi = _bf16_between(want, tol, _word(n, seed, t, i))
             at = dev[i].cpu().view(torch.int16).long()

@@ -651,7 +651,7 @@ def test_training_steps_of_the_layer_with_adamw():
         for (opt, _, p, g), (q, m, v), lo in zip(each, before, least):
             (b1, b2), g = opt.betas, g.double()
             v = b2 * v + (1 - b2) * g * g
-            if lo is not None:  # (a code of 0 counts as the smallest one under the root)
+            if lo is not None:  # (a code of 0 counts as the smallest one under the root, no m here being past it)
                 v = torch.maximum(v, lo.repeat_interleave(128)[:v.numel()].view_as(v))
             rate = opt.lr / (1 - b1 ** t) / (torch.sqrt(v / (1 - b2 ** t)) + opt.eps)
             want = q * (1 - opt.lr * opt.weight_decay) - rate * (b1 * m + (1 - b1) * g)
