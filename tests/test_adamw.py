@@ -554,3 +554,53 @@ def test_bf16_parameters_past_32_bit_elements():
         at = p[first:first + 256].cpu().view(torch.int16).long()
         assert (at >= lo).all() and (at <= hi).all(), first
         assert int((lo == hi).sum()) >= 250 and 64 < int((at == at.max()).sum()) < 192, first
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_captured_step_keeps_its_gradients_beside_eager_ones(bits):
+    """A graph of a step with gradients of its own, replayed between eager steps with the constructor's and with third ones."""
+    ps, gs = _tensors(F32, B16, 90)
+    new = lambda: [p.to(DEV) for p in ps]  # noqa: E731
+    sets = [[g.to(DEV) for g in _tensors(F32, dt, 91 + i)[1]] for i, dt in enumerate((B16, B16, F32))]
+    half = [[torch.zeros(p.shape, dtype=B16, device=DEV) for p in ps] for _ in range(2)]
+    a, b = new(), new()
+    x = moe.AdamW(a, state_bits=bits, seed=1, grads=sets[0], copies=half[0])
+    y = moe.AdamW(b, state_bits=bits, seed=1, grads=sets[0], copies=half[1])
+    n = torch.zeros(1, dtype=torch.int32, device=DEV)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        x.step(sets[1], step=n)
+    t = 0
+    for turn in range(3):
+        for which in (0, 1, 2, 1):
+            t += 1
+            n.fill_(t)
+            if which == 1:
+                graph.replay()
+            else:
+                x.step(sets[2] if which == 2 else None, step=n)
+            y.step(sets[which], step=n)
+        torch.randn(256, 256, device=DEV).sum().item()
+        for u, v in zip((*a, *x.exp_avg, *x.exp_avg_sq, *half[0]), (*b, *y.exp_avg, *y.exp_avg_sq, *half[1])):
+            assert torch.equal(u, v), (turn, u.shape)
+    assert all(torch.equal(h, u.to(B16)) for h, u in zip(half[0], a)) and x.steps == 0
+
+
+@pytest.mark.gpu
+def test_two_optimizers_on_two_streams():
+    (ps, gs), steps = _tensors(F32, F32, 95), 5
+    gs = [g.to(DEV) for g in gs]
+
+    def run(streams):
+        sets = [[p.to(DEV) for p in ps] for _ in range(2)]
+        opts = [moe.AdamW(p, state_bits=8, seed=i, grads=gs) for i, p in enumerate(sets)]
+        torch.cuda.synchronize()
+        for _ in range(steps):
+            for o, s in zip(opts, streams):
+                o.step(stream=s)
+        torch.cuda.synchronize()
+        return sets
+    want, got = run([None, None]), run([torch.cuda.Stream() for _ in range(2)])
+    assert all(torch.equal(u, v) for a, b in zip(want, got) for u, v in zip(a, b))
